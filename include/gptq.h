@@ -62,7 +62,8 @@ typedef enum {
                                 access was skipped); see gptq_bounds_report */
 } gptq_status;
 
-typedef enum { GPTQ_BF16 = 0, GPTQ_F32 = 1 } gptq_dtype;
+/* GPTQ_F16 is taken by the packed-weight products (gptq_matmul_*), which take 16-bit rows. */
+typedef enum { GPTQ_BF16 = 0, GPTQ_F32 = 1, GPTQ_F16 = 2 } gptq_dtype;
 
 /* Largest K (input coordinates) and N (output channels) any call accepts. */
 #define GPTQ_MAX_DIM 65535

@@ -20,7 +20,7 @@ LIB_PATH = os.environ.get("GPTQ_LIBRARY") or os.path.join(_HERE, "libgptq.so")
 
 GPTQ_OK, GPTQ_ERR_ARG, GPTQ_ERR_NOT_PD, GPTQ_ERR_NONFINITE = 0, 1, 2, 3
 GPTQ_ERR_CUDA, GPTQ_ERR_TIMEOUT, GPTQ_ERR_WORKSPACE, GPTQ_ERR_BOUNDS = 4, 5, 6, 7
-GPTQ_BF16, GPTQ_F32 = 0, 1
+GPTQ_BF16, GPTQ_F32, GPTQ_F16 = 0, 1, 2
 GPTQ_OP_PREPARE, GPTQ_OP_RESIDUAL, GPTQ_OP_QUANTIZE, GPTQ_OP_QUANTIZE_GROUPED = 0, 1, 2, 3
 GPTQ_OP_FIRST_ORDER = 4
 GPTQ_WS_CAE = 0x100
@@ -36,7 +36,19 @@ EXPORTS = ("gptq_accumulate_hessian", "gptaq_accumulate_cross", "gptq_prepare",
            "gptq_profile_read", "gptq_profile_timeline", "gptq_chain_latency",
            "gptq_bounds_report", "gptq_bounds_selftest")
 
+# the products of packed layers (include/gptq_matmul.h)
+MATMUL_EXPORTS = ("gptq_matmul_grouped", "gptq_matmul_grouped_dx", "gptq_matmul_grouped_dw",
+                  "gptq_matmul_lora", "gptq_matmul_lora_backward", "gptq_lora_workspace_size")
+
 _lib = None
+
+
+class GPTQPacked(ctypes.Structure):
+    """gptq_packed of include/gptq_matmul.h."""
+    _fields_ = [("words", ctypes.c_void_p), ("ld_words", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("g_idx", ctypes.c_void_p),
+                ("experts", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
+                ("bits", ctypes.c_int), ("groupsize", ctypes.c_int)]
 
 
 class GPTQError(RuntimeError):
@@ -55,6 +67,7 @@ def load_library():
                            "`python -m post_weight_quantization_solve_b200.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, I64, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    W = ctypes.POINTER(GPTQPacked)
     sig = {
         "gptq_accumulate_hessian": [P, I, I, P, I, I64, I64, P, I64, P, P],
         "gptaq_accumulate_cross": [P, I, P, P, I, I64, I64, P, P],
@@ -68,6 +81,13 @@ def load_library():
                                         SZ, P, P],
         "gptq_pack_codes": [P, I, I, I64, I, P, I64, P],
         "gptq_unpack_codes": [P, I, I, I64, I, P, I64, P],
+        "gptq_matmul_grouped": [P, I64, P, I64, I, I64, W, P, P, P],
+        "gptq_matmul_grouped_dx": [P, I64, P, I64, I, I64, W, P, P, P],
+        "gptq_matmul_grouped_dw": [P, P, I64, P, I64, I, I64, I, I, I, P, I, P, P],
+        "gptq_matmul_lora": [P, I64, P, I64, I, I64, W, P, P, P, I, I, P, P, I, P, SZ, P, P],
+        "gptq_matmul_lora_backward": [P, I64, P, P, P, I64, P, I64, I, I64, W, P, P, P, I, I, P, P,
+                                      I, P, SZ, P, P],
+        "gptq_lora_workspace_size": [I, I64, I, I, I, I, I],
         "gptq_first_order_shift": [P, I, I, P, P, I, F, P, P, SZ, P, P],
         "gptq_trust_region_beta": [F, ctypes.c_double, ctypes.c_double],
         "gptq_selftest_timeout": [P, P],
@@ -89,6 +109,7 @@ def load_library():
         fn.argtypes = args
         fn.restype = ctypes.c_int
     lib.gptq_workspace_size.restype = ctypes.c_size_t
+    lib.gptq_lora_workspace_size.restype = ctypes.c_size_t
     lib.gptq_trust_region_beta.restype = ctypes.c_float
     lib.gptq_status_string.restype = ctypes.c_char_p
     lib.gptq_kernel_launches.restype = ctypes.c_ulonglong
@@ -372,6 +393,234 @@ def gptq_unpack_codes(words, bits, K, codes=None, stream=None):
         code = lib.gptq_unpack_codes(*args)
     _check(code, "gptq_unpack_codes")
     return codes
+
+
+def _rows(t, dev, name, cols=None, dtype=None):
+    """(pointer, row pitch, 16-bit dtype code) of a [rows][cols] matrix of 16-bit values."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if t.dtype == torch.bfloat16:
+        code = GPTQ_BF16
+    elif t.dtype == torch.float16:
+        code = GPTQ_F16
+    else:
+        raise TypeError(f"{name}: bfloat16 or float16 rows, got {t.dtype}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
+    # the pitch of a single row is never used
+    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return _ptr(t, dev, name, rows=True), ld, code
+
+
+def _typed(t, dev, name, dtype, shape):
+    """Pointer of a dense tensor of the given type and shape (None stays None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return _ptr(t, dev, name)
+
+
+def _packed(words, scales, bits, K, groupsize, g_idx, dev):
+    """gptq_packed of words [E][N][>= nw] or [N][>= nw] with its scales and g_idx."""
+    if not isinstance(words, torch.Tensor) or words.dim() not in (2, 3):
+        raise ValueError("words must be [N][words] or [experts][N][words]")
+    if words.dtype not in (torch.int32, torch.uint32):
+        raise TypeError(f"words: int32 (bit patterns) or uint32, got {words.dtype}")
+    if words.shape[-1] < (K * bits + 31) // 32:
+        raise ValueError(f"words has {words.shape[-1]} words a row, {K} columns of {bits} bits need "
+                         f"{(K * bits + 31) // 32}")
+    E, N = (1, words.shape[0]) if words.dim() == 2 else words.shape[:2]
+    ld = words.stride(-2) if E * N > 1 else words.shape[-1]
+    if words.dim() == 3 and N == 1 and E > 1:
+        ld = words.stride(0)
+    elif words.dim() == 3 and E > 1 and words.stride(0) != N * ld:
+        raise ValueError("words: the experts' rows must follow one another at one pitch")
+    groups = (K + groupsize - 1) // groupsize if groupsize else 0
+    lead = () if words.dim() == 2 else (E,)
+    W = GPTQPacked()
+    W.words = _ptr(words, dev, "words", rows=True)
+    W.ld_words = ld
+    W.scales = _typed(scales, dev, "scales", torch.float32, lead + ((N, groups) if groupsize else (N,)))
+    if g_idx is not None and not groupsize:
+        raise ValueError("g_idx needs a groupsize")
+    W.g_idx = _typed(g_idx, dev, "g_idx", torch.int32, lead + (K,))
+    W.experts, W.N, W.K, W.bits, W.groupsize = E, N, K, bits, groupsize
+    return W
+
+
+def _offsets(offsets, dev, n):
+    return _typed(offsets, dev, "offsets", torch.int32, (n + 1,))
+
+
+def _scratch(nbytes, dev, workspace, stream):
+    """The caller's workspace, or a new one that outlives the call on its stream."""
+    if workspace is None:
+        workspace = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    return workspace, _ptr(workspace, dev, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def _fresh(shape, dtype, dev, stream):
+    out = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None:
+        out.record_stream(stream)
+    return out
+
+
+def gptq_matmul_grouped(X, words, scales, bits, offsets=None, groupsize=0, g_idx=None, out=None,
+                        status=None, stream=None):
+    """out[t] = W^_e X[t] for offsets[e] <= t < offsets[e + 1] over packed layers (see
+    include/gptq_matmul.h). words [experts][N][..] or [N][..] (one layer; then scales and g_idx
+    have no leading dimension either). Without `out`, a new [M][N] tensor, whose rows
+    outside the ranges are not initialised. Returns out."""
+    lib = load_library()
+    dev = _device(X, "X")
+    x, ldx, code = _rows(X, dev, "X")
+    M, K = X.shape
+    W = _packed(words, scales, bits, K, groupsize, g_idx, dev)
+    if out is None:
+        out = _fresh((M, W.N), X.dtype, dev, stream)
+    y, ldy, _ = _rows(out, dev, "out", W.N, X.dtype)
+    if out.shape[0] != M:
+        raise ValueError(f"out has {out.shape[0]} rows, X has {M}")
+    args = (y, ldy, x, ldx, code, M, ctypes.byref(W), _offsets(offsets, dev, W.experts),
+            _ptr(status, dev, "status"), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        code = lib.gptq_matmul_grouped(*args)
+    _check(code, "gptq_matmul_grouped")
+    return out
+
+
+def gptq_matmul_grouped_dx(dY, words, scales, bits, K, offsets=None, groupsize=0, g_idx=None,
+                           out=None, status=None, stream=None):
+    """out[t] = W^_e^T dY[t]: the gradient of gptq_matmul_grouped's rows ([M][K])."""
+    lib = load_library()
+    dev = _device(dY, "dY")
+    d, ldd, code = _rows(dY, dev, "dY", words.shape[-2] if isinstance(words, torch.Tensor) else None)
+    M = dY.shape[0]
+    W = _packed(words, scales, bits, K, groupsize, g_idx, dev)
+    if out is None:
+        out = _fresh((M, K), dY.dtype, dev, stream)
+    y, ldy, _ = _rows(out, dev, "out", K, dY.dtype)
+    if out.shape[0] != M:
+        raise ValueError(f"out has {out.shape[0]} rows, dY has {M}")
+    args = (y, ldy, d, ldd, code, M, ctypes.byref(W), _offsets(offsets, dev, W.experts),
+            _ptr(status, dev, "status"), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        code = lib.gptq_matmul_grouped_dx(*args)
+    _check(code, "gptq_matmul_grouped_dx")
+    return out
+
+
+def gptq_matmul_grouped_dw(dY, X, offsets=None, experts=None, out=None, accumulate=False,
+                           status=None, stream=None):
+    """out[e] = sum of dY[t]^T X[t] over the rows of expert e, fp32 [experts][N][K] (added to
+    `out` with accumulate=True). experts: from `offsets` when not given; 1 without them."""
+    lib = load_library()
+    dev = _device(dY, "dY")
+    d, ldd, code = _rows(dY, dev, "dY")
+    x, ldx, _ = _rows(X, dev, "X", None, dY.dtype)
+    if X.shape[0] != dY.shape[0]:
+        raise ValueError(f"X has {X.shape[0]} rows, dY has {dY.shape[0]}")
+    if experts is None:
+        experts = 1 if offsets is None else offsets.shape[0] - 1
+    M, N, K = dY.shape[0], dY.shape[1], X.shape[1]
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs `out`")
+        out = _fresh((experts, N, K), torch.float32, dev, stream)
+    args = (_typed(out, dev, "out", torch.float32, (experts, N, K)), d, ldd, x, ldx, code, M, N, K,
+            experts, _offsets(offsets, dev, experts), int(bool(accumulate)),
+            _ptr(status, dev, "status"), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        code = lib.gptq_matmul_grouped_dw(*args)
+    _check(code, "gptq_matmul_grouped_dw")
+    return out
+
+
+def _adapter_args(A, B, alpha, offsets, ids, dtype, N, K, dev):
+    """(pointers of A, B, alpha, adapters, rank, offsets, ids, requests), checked."""
+    if not isinstance(A, torch.Tensor) or A.dim() != 3:
+        raise ValueError("A must be [adapters][rank][K]")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
+        raise ValueError("ids must be a 1-D int32 tensor")
+    L, r, R = A.shape[0], A.shape[1], ids.shape[0]
+    return (_typed(A, dev, "A", dtype, (L, r, K)), _typed(B, dev, "B", dtype, (L, N, r)),
+            _typed(alpha, dev, "alpha", torch.float32, (L,)), L, r, _offsets(offsets, dev, R),
+            _typed(ids, dev, "ids", torch.int32, (R,)), R)
+
+
+def gptq_lora_workspace_size(backward, M, N, K, requests, adapters, rank):
+    return int(load_library().gptq_lora_workspace_size(int(backward), M, N, K, requests, adapters, rank))
+
+
+def gptq_matmul_lora(X, words, scales, bits, A, B, alpha, offsets, ids, groupsize=0, g_idx=None,
+                     out=None, workspace=None, status=None, stream=None):
+    """out[t] = W^ X[t] + alpha[a] B[a] A[a] X[t], a the adapter of t's request (ids[r] for
+    offsets[r] <= t < offsets[r + 1], -1 none); see include/gptq_matmul.h. Returns out."""
+    lib = load_library()
+    dev = _device(X, "X")
+    x, ldx, code = _rows(X, dev, "X")
+    M, K = X.shape
+    W = _packed(words, scales, bits, K, groupsize, g_idx, dev)
+    a = _adapter_args(A, B, alpha, offsets, ids, X.dtype, W.N, K, dev)
+    if out is None:
+        out = _fresh((M, W.N), X.dtype, dev, stream)
+    y, ldy, _ = _rows(out, dev, "out", W.N, X.dtype)
+    if out.shape[0] != M:
+        raise ValueError(f"out has {out.shape[0]} rows, X has {M}")
+    need = lib.gptq_lora_workspace_size(0, M, W.N, K, a[7], a[3], a[4])
+    workspace, ws, nbytes = _scratch(need, dev, workspace, stream)
+    args = (y, ldy, x, ldx, code, M, ctypes.byref(W), *a, ws, nbytes, _ptr(status, dev, "status"),
+            _stream(stream, dev))
+    with torch.cuda.device(dev):
+        code = lib.gptq_matmul_lora(*args)
+    _check(code, "gptq_matmul_lora")
+    return out
+
+
+def gptq_matmul_lora_backward(dY, X, words, scales, bits, A, B, alpha, offsets, ids, groupsize=0,
+                              g_idx=None, dX=None, dA=None, dB=None, want=(True, True, True),
+                              workspace=None, status=None, stream=None):
+    """(dX, dA, dB) of gptq_matmul_lora; `want` leaves out gradients (None in their place).
+    dX is of dY's type, dA and dB fp32; see include/gptq_matmul.h."""
+    lib = load_library()
+    dev = _device(dY, "dY")
+    d, ldd, code = _rows(dY, dev, "dY")
+    x, ldx, _ = _rows(X, dev, "X", None, dY.dtype)
+    (M, N), K = dY.shape, X.shape[1]
+    if X.shape[0] != M:
+        raise ValueError(f"X has {X.shape[0]} rows, dY has {M}")
+    W = _packed(words, scales, bits, K, groupsize, g_idx, dev)
+    if W.N != N:
+        raise ValueError(f"dY has {N} columns, the layer has {W.N} channels")
+    a = _adapter_args(A, B, alpha, offsets, ids, dY.dtype, N, K, dev)
+    L, r = a[3], a[4]
+    dX = (_fresh((M, K), dY.dtype, dev, stream) if dX is None else dX) if want[0] else None
+    dA = (_fresh((L, r, K), torch.float32, dev, stream) if dA is None else dA) if want[1] else None
+    dB = (_fresh((L, N, r), torch.float32, dev, stream) if dB is None else dB) if want[2] else None
+    g, ldg = None, K
+    if dX is not None:
+        g, ldg, _ = _rows(dX, dev, "dX", K, dY.dtype)
+        if dX.shape[0] != M:
+            raise ValueError(f"dX has {dX.shape[0]} rows, dY has {M}")
+    need = lib.gptq_lora_workspace_size(1, M, N, K, a[7], L, r)
+    workspace, ws, nbytes = _scratch(need, dev, workspace, stream)
+    args = (g, ldg, _typed(dA, dev, "dA", torch.float32, (L, r, K)),
+            _typed(dB, dev, "dB", torch.float32, (L, N, r)), d, ldd, x, ldx, code, M,
+            ctypes.byref(W), *a, ws, nbytes, _ptr(status, dev, "status"), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        code = lib.gptq_matmul_lora_backward(*args)
+    _check(code, "gptq_matmul_lora_backward")
+    return dX, dA, dB
 
 
 def gptq_first_order_shift(W, U, G, beta, gamma=None, workspace=None, status=None, stream=None):

@@ -1,0 +1,357 @@
+// Low-rank adapters beside a packed projection: the rank-space rows, the requests of each
+// adapter, and the calls that put the pieces together.
+//
+//   T[t] = alpha_a A_a X[t]        (forward, and the gradient of B)
+//   U[t] = alpha_a B_a^T dY[t]     (gradients of X and A)
+//
+// Both are one kernel (k_rank_rows): a thin product rows x [rank][inner], bound by reading the
+// rows (long prompts) or the adapters (requests that decode, each with an adapter of its own).
+// Row and adapter fragments of mma.sync m16n8k16 are read straight from global memory: a lane
+// takes 16 bytes (8 neighbouring columns) of its row and of its adapter row, which permutes
+// the contraction index alike on both sides. The result leaves as a pair of 16-bit halves
+// [hi | lo], 16 bits of the fp32 sum, which the products that follow read as matrix operands.
+// B_a is stored [N][rank]; its gradient pass reads it transposed once (k_transpose).
+#include <algorithm>
+
+#include "matmul.cuh"
+
+namespace gptq {
+
+int adapter_parts(int64_t M, int L, int width);
+gptq_status adapter_gradient(float *out, float *parts, int split, const void *P, int64_t ldp, int np,
+                             const void *T2, int rank, int transposed, int dtype, int64_t M,
+                             const int32_t *offsets, const int32_t *ids, const int32_t *list_off,
+                             const int32_t *list, int R, int L, int32_t *status, cudaStream_t st);
+gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStream_t st);
+gptq_status matmul_token(const MatmulArg &m, int dtype, int bits, cudaStream_t st);
+bool matmul_few_rows(int64_t M, int E);
+
+struct RankArg {
+    const void *X;            // [M][ldx]
+    int64_t ldx, M;
+    const void *A;            // [L][rank][inner]
+    const float *alpha;       // [L]
+    const int32_t *offsets, *ids;
+    int R, L, rank, inner;
+    void *T2;                 // [M][2 rank]
+    int xvec, avec, split;
+    int32_t *status;
+};
+
+template <typename T>
+__device__ __forceinline__ void mma_rank(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    if constexpr (Half2<T>::kType == 1)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 piece(const T *row, int c, int cols, bool vec) {
+    if (row == nullptr || c >= cols) return make_uint4(0u, 0u, 0u, 0u);
+    if (vec && c + 8 <= cols) return __ldg(reinterpret_cast<const uint4 *>(row + c));
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    const unsigned short *s = reinterpret_cast<const unsigned short *>(row + c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (c + e < cols) v[e >> 1] |= (uint32_t)__ldg(s + e) << (16 * (e & 1));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Block (row tile, part of the contraction): MW warps of 16 rows x KW warps of the contraction;
+// a cluster of `split` blocks shares a tile's contraction. Tiles are cut inside each request, so
+// a tile has one adapter; block b looks at row off[0] + b and works when a tile starts there.
+template <typename T, int NR, int MW, int KW>
+__global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constant__ RankArg p) {
+    constexpr int THREADS = MW * KW * 32, ROWS = 16 * MW;
+    __shared__ float part[KW][ROWS][NR * 8 + 1];
+    __shared__ int flag[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quad = lane & 3, g = lane >> 2;
+    const int mw = warp % MW, kw = warp / MW;
+    const uint32_t rank = p.split > 1 ? tc::cluster_ctarank() : 0u;
+    const int64_t tile = blockIdx.x / p.split;
+    grid_dependency();
+    if (threadIdx.x < 2) flag[threadIdx.x] = 0;
+    __syncthreads();
+    bool bad = offsets_bad(p.offsets, p.R, p.M, threadIdx.x, THREADS);
+    bad |= ids_bad(p.ids, p.R, p.L, threadIdx.x, THREADS);
+    if (bad) flag[0] = 1;
+    // request of the row: the requests that end at or before it
+    const int64_t t = (int64_t)__ldg(p.offsets) + tile;
+    int before = 0;
+    for (int i = threadIdx.x; i < p.R; i += THREADS) before += (int64_t)__ldg(p.offsets + i + 1) <= t;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(~0u, before, d);
+    if (lane == 0 && before) atomicAdd(&flag[1], before);
+    __syncthreads();
+    // every block of a cluster sees the same offsets, so they agree on what follows
+    if (flag[0]) {
+        if (threadIdx.x == 0) set_status(p.status, GPTQ_ERR_ARG);
+        return;
+    }
+    const int s = flag[1];
+    if (s >= p.R) return;
+    const int begin = __ldg(p.offsets + s), end = __ldg(p.offsets + s + 1), id = __ldg(p.ids + s);
+    if (id < 0 || (t - begin) % ROWS != 0) return;
+
+    const int r0 = (int)t + mw * 16;
+    const T *X = static_cast<const T *>(p.X);
+    const T *x0 = r0 + g < end ? X + (int64_t)(r0 + g) * p.ldx : nullptr;
+    const T *x1 = r0 + g + 8 < end ? X + (int64_t)(r0 + g + 8) * p.ldx : nullptr;
+    const T *A = static_cast<const T *>(p.A) + (int64_t)id * p.rank * p.inner;
+    float acc[NR][4];
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    const int steps = (p.inner + 31) / 32;
+    const int s0 = (int)((int64_t)steps * rank / p.split), s1 = (int)((int64_t)steps * (rank + 1) / p.split);
+    const bool xv = p.xvec != 0, av = p.avec != 0;
+#pragma unroll 2
+    for (int step = s0 + kw; step < s1; step += KW) {
+        const int c = step * 32 + quad * 8;
+        const uint4 a = piece<T>(x0, c, p.inner, xv), b = piece<T>(x1, c, p.inner, xv);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            const int row = j * 8 + g;
+            const uint4 w = piece<T>(row < p.rank ? A + (int64_t)row * p.inner : nullptr, c, p.inner, av);
+            mma_rank<T>(acc[j], a.x, b.x, a.y, b.y, w.x, w.y);
+            mma_rank<T>(acc[j], a.z, b.z, a.w, b.w, w.z, w.w);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            part[kw][mw * 16 + g + 8 * (i >> 1)][j * 8 + 2 * quad + (i & 1)] = acc[j][i];
+    __syncthreads();
+    const int rows = min(ROWS, end - (int)t);
+    for (int i = threadIdx.x; i < rows * NR * 8; i += THREADS) {
+        const int row = i / (NR * 8), j = i % (NR * 8);
+        float sum = part[0][row][j];
+#pragma unroll
+        for (int k = 1; k < KW; ++k) sum += part[k][row][j];
+        part[0][row][j] = sum;
+    }
+    if (p.split > 1) tc::cluster_sync();
+    else __syncthreads();
+    const float alpha = __ldg(p.alpha + id);
+    T *out = static_cast<T *>(p.T2);
+    const int per = (rows * NR * 8 + p.split - 1) / p.split;
+    for (int i = (int)rank * per + threadIdx.x; i < min(rows * NR * 8, ((int)rank + 1) * per); i += THREADS) {
+        const int row = i / (NR * 8), j = i % (NR * 8);
+        float sum = 0.f;
+        if (p.split > 1) {
+            const uint32_t at = tc::smem_u32(&part[0][row][j]);
+            for (int c = 0; c < p.split; ++c)
+                sum += __uint_as_float(tc::ld_shared_cluster(tc::mapa_shared(at, c)));
+        } else {
+            sum = part[0][row][j];
+        }
+        if (j < p.rank) {
+            const float v = alpha * sum;
+            const T hi = from_f32<T>(v);
+            const float f = to_f32<T>(hi);
+            // an infinite half has no rest
+            const T lo = from_f32<T>(isfinite(f) ? v - f : 0.f);
+            T *d = out + ((int64_t)t + row) * 2 * p.rank + j;
+            d[0] = hi;
+            d[p.rank] = lo;
+        }
+    }
+    if (p.split > 1) tc::cluster_sync();
+}
+
+template <typename T, int NR>
+static gptq_status launch_rank_nr(RankArg &p, cudaStream_t st) {
+    const int64_t rows = p.M;
+    if (rows >= 1024) {
+        // long prompts: bound by the rows; 64 rows a block share the adapter
+        constexpr int KW = NR > 8 ? 1 : 2;
+        p.split = 1;
+        return launch_pdl(k_rank_rows<T, NR, 4, KW>, dim3((unsigned)rows), 128 * KW, 0, 1, st, p);
+    }
+    constexpr int KW = NR > 8 ? 4 : 8;
+    const int steps = (p.inner + 31) / 32;
+    p.split = 1;
+    const int64_t tiles = std::min<int64_t>(rows, p.R + rows / 16);
+    while (p.split < 8 && tiles * p.split * 2 <= 2 * device_sms() && steps >= 4 * KW * p.split) p.split *= 2;
+    return launch_pdl(k_rank_rows<T, NR, 1, KW>, dim3((unsigned)(rows * p.split)), 32 * KW, 0, p.split, st, p);
+}
+
+template <typename T>
+static gptq_status launch_rank(RankArg &p, cudaStream_t st) {
+    if (p.rank <= 8) return launch_rank_nr<T, 1>(p, st);
+    if (p.rank <= 16) return launch_rank_nr<T, 2>(p, st);
+    if (p.rank <= 32) return launch_rank_nr<T, 4>(p, st);
+    if (p.rank <= 64) return launch_rank_nr<T, 8>(p, st);
+    return launch_rank_nr<T, 16>(p, st);
+}
+
+// out[l][j][n] = in[l][n][j], 16-bit elements, 32 x 32 tiles through shared memory.
+__global__ void __launch_bounds__(256) k_transpose(const uint16_t *__restrict__ in, uint16_t *__restrict__ out,
+                                                   int N, int r) {
+    __shared__ uint16_t tile[32][34];
+    grid_dependency();
+    const int n0 = blockIdx.x * 32, j0 = blockIdx.y * 32;
+    const int64_t base = (int64_t)blockIdx.z * N * r;
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    for (int i = y; i < 32; i += 8)
+        if (n0 + i < N && j0 + x < r) tile[i][x] = in[base + (int64_t)(n0 + i) * r + j0 + x];
+    __syncthreads();
+    for (int i = y; i < 32; i += 8)
+        if (j0 + i < r && n0 + x < N) out[base + (int64_t)(j0 + i) * N + n0 + x] = tile[x][i];
+}
+
+// Requests of each adapter, in request order: list_off [L + 1], list [R]. One block; a thread
+// takes whole adapters, so the order is fixed.
+__global__ void __launch_bounds__(256) k_adapter_lists(const int32_t *__restrict__ ids, int R, int L,
+                                                       int32_t *list_off, int32_t *list, int32_t *status) {
+    __shared__ int bad, warp_sum[8], base;
+    grid_dependency();
+    if (threadIdx.x == 0) {
+        bad = 0;
+        base = 0;
+    }
+    __syncthreads();
+    if (ids_bad(ids, R, L, threadIdx.x, 256)) bad = 1;
+    __syncthreads();
+    if (bad && threadIdx.x == 0) set_status(status, GPTQ_ERR_ARG);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int a0 = 0; a0 < L; a0 += 256) {
+        const int a = a0 + threadIdx.x;
+        int n = 0;
+        if (a < L && !bad)
+            for (int i = 0; i < R; ++i) n += __ldg(ids + i) == a;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(~0u, sum, d);
+            if (lane >= d) sum += v;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        int at = base + sum - n;
+        for (int w = 0; w < warp; ++w) at += warp_sum[w];
+        if (a < L) {
+            list_off[a] = at;
+            if (!bad)
+                for (int i = 0, k = at; i < R; ++i)
+                    if (__ldg(ids + i) == a) list[k++] = i;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int w = 0; w < 8; ++w) base += warp_sum[w];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) list_off[L] = base;
+}
+
+static gptq_status rank_rows(void *T2, const void *X, int64_t ldx, int64_t M, const void *A, int inner,
+                             const float *alpha, const int32_t *offsets, const int32_t *ids, int R, int L,
+                             int rank, int dtype, int32_t *status, cudaStream_t st) {
+    RankArg p{};
+    p.X = X; p.ldx = ldx; p.M = M;
+    p.A = A; p.alpha = alpha;
+    p.offsets = offsets; p.ids = ids;
+    p.R = R; p.L = L; p.rank = rank; p.inner = inner;
+    p.T2 = T2;
+    p.xvec = aligned(X, 16) && ldx % 8 == 0;
+    p.avec = aligned(A, 16) && inner % 8 == 0;
+    p.status = status;
+    return dtype == GPTQ_BF16 ? launch_rank<__nv_bfloat16>(p, st) : launch_rank<__half>(p, st);
+}
+
+struct LoraSpace {
+    void *T2, *U2, *Bt;
+    float *parts;
+    int32_t *list_off, *list;
+    size_t bytes;
+};
+
+static LoraSpace lora_space(void *ws, bool backward, int64_t M, int N, int K, int R, int L, int rank) {
+    Carver c(ws);
+    LoraSpace s{};
+    s.T2 = c.take<uint16_t>((size_t)M * 2 * rank);
+    if (backward) {
+        s.U2 = c.take<uint16_t>((size_t)M * 2 * rank);
+        s.Bt = c.take<uint16_t>((size_t)L * N * rank);
+        const size_t pb = (size_t)adapter_parts(M, L, N) * L * N * rank, pa = (size_t)adapter_parts(M, L, K) * L * K * rank;
+        s.parts = c.take<float>(std::max(pa, pb));
+        s.list_off = c.take<int32_t>(L + 1);
+        s.list = c.take<int32_t>(std::max(R, 1));
+    }
+    s.bytes = round_up(c.off, 256);
+    return s;
+}
+
+size_t lora_workspace(bool backward, int64_t M, int N, int K, int R, int L, int rank) {
+    return lora_space(nullptr, backward, M, N, K, R, L, rank).bytes;
+}
+
+gptq_status matmul_lora(MatmulArg m, const void *A, const void *B, const float *alpha, int dtype, int bits,
+                        void *ws, cudaStream_t st) {
+    const LoraArg &l = m.lora;
+    const LoraSpace s = lora_space(ws, false, m.M, m.w.N, m.w.K, l.R, l.L, l.rank);
+    gptq_status r = rank_rows(s.T2, m.X, m.ldx, m.M, A, m.w.K, alpha, m.offsets, l.ids, l.R, l.L, l.rank,
+                              dtype, m.status, st);
+    if (r != GPTQ_OK) return r;
+    m.lora.P = B;
+    m.lora.T2 = s.T2;
+    if (matmul_few_rows(m.M, 1)) return matmul_token(m, dtype, bits, st);
+    return matmul_tc(m, 0, dtype, bits, st);
+}
+
+// m.X = dY, m.Y = dX (NULL: not wanted).
+gptq_status matmul_lora_backward(MatmulArg m, float *dA, float *dB, const void *X, int64_t ldx, const void *A,
+                                 const void *B, const float *alpha, int dtype, int bits, void *ws,
+                                 cudaStream_t st) {
+    const LoraArg l = m.lora;
+    const int N = m.w.N, K = m.w.K;
+    const LoraSpace s = lora_space(ws, true, m.M, N, K, l.R, l.L, l.rank);
+    gptq_status r = GPTQ_OK;
+    if (dA || dB) {
+        r = launch_pdl(k_adapter_lists, dim3(1), 256, 0, 1, st, l.ids, l.R, l.L, s.list_off, s.list, m.status);
+        if (r != GPTQ_OK) return r;
+    }
+    if ((m.Y || dA) && m.M > 0) {
+        r = launch_pdl(k_transpose, dim3((N + 31) / 32, (l.rank + 31) / 32, l.L), 256, 0, 1, st,
+                       (const uint16_t *)B, (uint16_t *)s.Bt, N, l.rank);
+        if (r != GPTQ_OK) return r;
+        r = rank_rows(s.U2, m.X, m.ldx, m.M, s.Bt, N, alpha, m.offsets, l.ids, l.R, l.L, l.rank, dtype,
+                      m.status, st);
+        if (r != GPTQ_OK) return r;
+    }
+    if (dB) {
+        if (m.M > 0) {
+            r = rank_rows(s.T2, X, ldx, m.M, A, K, alpha, m.offsets, l.ids, l.R, l.L, l.rank, dtype, m.status, st);
+            if (r != GPTQ_OK) return r;
+        }
+        r = adapter_gradient(dB, s.parts, adapter_parts(m.M, l.L, N), m.X, m.ldx, N, s.T2, l.rank, 0, dtype, m.M,
+                             m.offsets, l.ids, s.list_off, s.list, l.R, l.L, m.status, st);
+        if (r != GPTQ_OK) return r;
+    }
+    if (dA) {
+        r = adapter_gradient(dA, s.parts, adapter_parts(m.M, l.L, K), X, ldx, K, s.U2, l.rank, 1, dtype, m.M,
+                             m.offsets, l.ids, s.list_off, s.list, l.R, l.L, m.status, st);
+        if (r != GPTQ_OK) return r;
+    }
+    if (m.Y && m.M > 0) {
+        m.lora.P = A;
+        m.lora.T2 = s.U2;
+        r = matmul_tc(m, 1, dtype, bits, st);
+    }
+    return r;
+}
+
+}  // namespace gptq

@@ -1,0 +1,407 @@
+// Shared parts of the packed-weight products (matmul_tc.cu, matmul_token.cu, matmul_dw.cu,
+// lora.cu): the packed layer as kernels see it, unpacking of 32 codes into 16-bit pairs, the
+// table of ragged row ranges, and the tiled-copy descriptors.
+//
+// A packed row is a little-endian bit stream (gptq_pack_codes), so 32 codes fill exactly
+// `bits` words and one thread turns those words into 16 registers of two values each. The
+// values c - z are integers of at most 8 bits, exact in bf16 and fp16.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "gptq_matmul.h"
+#include "tc_ptx.cuh"
+
+namespace gptq {
+
+// ---- arguments as kernels see them ---------------------------------------------------------
+
+struct PackedArg {
+    const uint32_t *words;    // [E][N][ldw]
+    int64_t ldw;
+    const float *scales;      // [E][N] (groups == 0) or [E][N][groups]
+    const int32_t *g_idx;     // [E][K] or NULL (column k in group k >> gshift)
+    int E, N, K;
+    int groups, gshift;
+};
+
+// Adapters beside a product, and the rows that use them.
+struct LoraArg {
+    const void *P;            // forward: B [L][N][rank]; input gradient: A [L][rank][K]
+    const void *T2;           // [M][2 rank]: hi and lo halves of the rank-space rows
+    const int32_t *ids;       // [R] adapter of each request, -1 none
+    int R, L, rank;
+};
+
+struct MatmulArg {
+    PackedArg w;
+    const void *X;            // [M][ldx]: tokens (forward) or output gradients (input gradient)
+    int64_t ldx;
+    void *Y;                  // [M][ldy]
+    int64_t ldy;
+    const int32_t *offsets;   // [E + 1], or [R + 1] with adapters, or NULL (all M rows)
+    int64_t M;
+    LoraArg lora;             // R == 0: none
+    int32_t *status;
+};
+
+constexpr int MATMUL_MAX_EXPERTS = 1024;
+
+// ---- 16-bit types --------------------------------------------------------------------------
+
+template <typename T>
+struct Half2;
+template <>
+struct Half2<__nv_bfloat16> {
+    static constexpr uint32_t kMagic = 0x43004300u;     // 128 + c for c < 128
+    static constexpr uint32_t kType = 1;                // instruction-descriptor type code
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t d;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+        return d;
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t v) {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    }
+};
+template <>
+struct Half2<__half> {
+    static constexpr uint32_t kMagic = 0x64006400u;     // 1024 + c for c < 1024
+    static constexpr uint32_t kType = 0;
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t d;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+        return d;
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t v) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    }
+};
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// ---- unpacking -----------------------------------------------------------------------------
+
+template <uint32_t MASK, uint32_t OR>
+__device__ __forceinline__ uint32_t and_or(uint32_t a) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "n"(MASK), "n"(OR));
+    return d;
+}
+
+// 32 codes (B words) -> c - z as 16 pairs in column order. Each code is placed under the
+// exponent bits of 128 (bf16) or 1024 (fp16), where its value is the number's low mantissa;
+// one packed subtraction then gives c - z exactly. Codes come out of a word two 16-bit lanes
+// at a time (code i with code i + 4, ...); byte permutes put neighbours together.
+template <int B, typename T>
+__device__ __forceinline__ void unpack32(const uint32_t (&w)[B], uint32_t (&out)[16]) {
+    using H = Half2<T>;
+    constexpr uint32_t M = H::kMagic;
+    if constexpr (B == 8) {
+        constexpr uint32_t hi = M >> 24;     // the exponent byte
+        constexpr uint32_t hi4 = hi * 0x01010101u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t p = __byte_perm(w[i], hi4, h ? 0x4342 : 0x4140);
+                if constexpr (H::kType == 1) {
+                    // 128 + (c & 127) less 128 where c >= 128 and 256 elsewhere
+                    const uint32_t x = p & 0xff7fff7fu;
+                    const uint32_t y = (p & 0x43804380u) ^ 0x00800080u;
+                    out[2 * i + h] = H::sub(x, y);
+                } else {
+                    out[2 * i + h] = H::sub(p, M + 0x00800080u);
+                }
+            }
+        }
+    } else if constexpr (B == 4) {
+        constexpr uint32_t Z = M + 0x00080008u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = w[i];
+            const uint32_t a = H::sub(and_or<0x000f000fu, M>(v), Z);           // c0 c4
+            const uint32_t b = H::sub(and_or<0x000f000fu, M>(v >> 4), Z);      // c1 c5
+            const uint32_t c = H::sub(and_or<0x000f000fu, M>(v >> 8), Z);      // c2 c6
+            const uint32_t d = H::sub(and_or<0x000f000fu, M>(v >> 12), Z);     // c3 c7
+            out[4 * i + 0] = __byte_perm(a, b, 0x5410);
+            out[4 * i + 1] = __byte_perm(c, d, 0x5410);
+            out[4 * i + 2] = __byte_perm(a, b, 0x7632);
+            out[4 * i + 3] = __byte_perm(c, d, 0x7632);
+        }
+    } else if constexpr (B == 2) {
+        constexpr uint32_t Z = M + 0x00020002u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t q[8];                                                     // c_j c_(j+8)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = H::sub(and_or<0x00030003u, M>(w[i] >> (2 * j)), Z);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                out[8 * i + j] = __byte_perm(q[2 * j], q[2 * j + 1], 0x5410);
+                out[8 * i + 4 + j] = __byte_perm(q[2 * j], q[2 * j + 1], 0x7632);
+            }
+        }
+    } else {
+        static_assert(B == 3, "bits");
+        constexpr uint32_t Z = M + 0x00040004u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // the 24 bits of codes 8i .. 8i + 7, four codes to a 16-bit lane
+            const uint32_t g = i == 0 ? w[0]
+                               : i == 1 ? __funnelshift_r(w[0], w[1], 24)
+                               : i == 2 ? __funnelshift_r(w[1], w[2], 16)
+                                        : (w[2] >> 8);
+            const uint32_t h = (g & 0xfffu) | ((g << 4) & 0x0fff0000u);
+            const uint32_t a = H::sub(and_or<0x00070007u, M>(h), Z);
+            const uint32_t b = H::sub(and_or<0x00070007u, M>(h >> 3), Z);
+            const uint32_t c = H::sub(and_or<0x00070007u, M>(h >> 6), Z);
+            const uint32_t d = H::sub(and_or<0x00070007u, M>(h >> 9), Z);
+            out[4 * i + 0] = __byte_perm(a, b, 0x5410);
+            out[4 * i + 1] = __byte_perm(c, d, 0x5410);
+            out[4 * i + 2] = __byte_perm(a, b, 0x7632);
+            out[4 * i + 3] = __byte_perm(c, d, 0x7632);
+        }
+    }
+}
+
+// The 32 values times one scale, each product rounded once to the 16-bit type. bf16: the
+// scale as a pair of bf16 (16 significant bits), v s_lo + v s_hi in one packed multiply-add.
+// fp16 scales can lie below fp16's normal range, so there the products are formed in fp32.
+template <typename T>
+__device__ __forceinline__ void scale32(uint32_t (&v)[16], float s) {
+    if constexpr (Half2<T>::kType == 1) {
+        const uint32_t hi = Half2<T>::pack(s, s);
+        const float rest = s - __uint_as_float(hi & 0xffff0000u);
+        const uint32_t lo = Half2<T>::pack(rest, rest);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            uint32_t t;
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t) : "r"(v[i]), "r"(lo));
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(v[i]), "r"(hi), "r"(t));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 f = Half2<T>::unpack(v[i]);
+            v[i] = Half2<T>::pack(f.x * s, f.y * s);
+        }
+    }
+}
+
+// The 32 values of columns k0 .. k0 + 31, each times the scale of its column's group.
+template <typename T>
+__device__ __forceinline__ void scale32_by_index(uint32_t (&v)[16], const float *row_scales,
+                                                 const int32_t *g_idx, int k0, int K, int groups,
+                                                 int32_t *status) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float s[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = k0 + 2 * i + h;
+            int g = k < K ? __ldg(g_idx + k) : 0;
+            if ((unsigned)g >= (unsigned)groups) {
+                set_status(status, GPTQ_ERR_ARG);
+                g = 0;
+            }
+            s[h] = __ldg(row_scales + g);
+        }
+        const float2 f = Half2<T>::unpack(v[i]);
+        v[i] = Half2<T>::pack(f.x * s[0], f.y * s[1]);
+    }
+}
+
+// B words of chunk `chunk` of a row; words at or past the row's end read as zero. `row` NULL:
+// zeros. vec: rows start on 16-byte boundaries.
+template <int B>
+__device__ __forceinline__ void load_chunk(const uint32_t *row, int chunk, int nw, bool vec,
+                                           uint32_t (&w)[B]) {
+    const int at = chunk * B;
+    if (row == nullptr || at >= nw) {
+#pragma unroll
+        for (int j = 0; j < B; ++j) w[j] = 0u;
+        return;
+    }
+    if constexpr (B % 4 == 0) {
+        if (vec && at + B <= nw) {
+#pragma unroll
+            for (int j = 0; j < B; j += 4) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + at + j));
+                w[j] = v.x; w[j + 1] = v.y; w[j + 2] = v.z; w[j + 3] = v.w;
+            }
+            return;
+        }
+    }
+    if constexpr (B == 2) {
+        if (vec && at + B <= nw) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + at));
+            w[0] = v.x; w[1] = v.y;
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < B; ++j) w[j] = at + j < nw ? __ldg(row + at + j) : 0u;
+}
+
+// ---- ragged ranges -------------------------------------------------------------------------
+
+// Row ranges are refused as a whole when an offset is negative, above M or below the one
+// before it: then no row is read or written through them. Every block checks all of them.
+__device__ __forceinline__ bool offsets_bad(const int32_t *off, int n, int64_t M, int tid,
+                                            int nthreads) {
+    bool bad = false;
+    for (int i = tid; i <= n; i += nthreads) {
+        const int v = __ldg(off + i);
+        bad |= v < 0 || (int64_t)v > M || (i > 0 && v < __ldg(off + i - 1));
+    }
+    return bad;
+}
+
+__device__ __forceinline__ bool ids_bad(const int32_t *ids, int R, int L, int tid, int nthreads) {
+    bool bad = false;
+    for (int i = tid; i < R; i += nthreads) {
+        const int v = __ldg(ids + i);
+        bad |= v < -1 || v >= L;
+    }
+    return bad;
+}
+
+// First request whose end lies behind row t (off[s + 1] > t), by bisection.
+__device__ __forceinline__ int request_of(const int32_t *off, int R, int t) {
+    int lo = 0, hi = R;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(off + mid + 1) > t) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// Walks the rows [t0, t1) in runs of one adapter: neighbouring requests with the same adapter
+// make one run; rows without an adapter are skipped.
+struct RunWalk {
+    const int32_t *off, *ids;
+    int R, t1, s, t;
+    int begin, end, id;       // the current run: rows [begin, end), its adapter
+    __device__ __forceinline__ RunWalk(const int32_t *off_, const int32_t *ids_, int R_, int t0,
+                                       int t1_)
+        : off(off_), ids(ids_), R(R_), t1(t1_), s(request_of(off_, R_, t0)), t(t0) {}
+    __device__ __forceinline__ bool next() {
+        while (s < R && t < t1) {
+            const int e = min(__ldg(off + s + 1), t1);
+            const int a = __ldg(ids + s);
+            if (e <= t) { ++s; continue; }
+            begin = t;
+            end = e;
+            id = a;
+            t = e;
+            ++s;
+            while (s < R && t < t1 && (__ldg(ids + s) == a || __ldg(off + s + 1) <= t)) {
+                end = max(end, min(__ldg(off + s + 1), t1));
+                t = end;
+                ++s;
+            }
+            if (a >= 0) return true;
+        }
+        return false;
+    }
+};
+
+// ---- host ----------------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            ptr = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(ptr);
+    }();
+    return fn;
+}
+
+// A row-major [rows][cols] matrix of a 16-bit type as boxes of 64 columns x box_rows rows in the
+// 128-byte swizzle. False when its layout does not allow tiled copies (then plain loads serve).
+inline bool rows_map(CUtensorMap *map, const void *ptr, int dtype, int64_t rows, int64_t cols,
+                     int64_t ld, int box_rows) {
+    EncodeTiled enc = encode_tiled();
+    if (!enc || !aligned(ptr, 16) || (ld * 2) % 16 != 0 || rows < 1) return false;
+    const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t stride[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t step[2] = {1, 1};
+    return enc(map,
+               dtype == GPTQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+               2, const_cast<void *>(ptr), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline int device_sms() {
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 148;
+}
+
+// One launch as a programmatic dependent of the previous kernel on the stream, in clusters of
+// `cluster` blocks along x.
+template <typename... KArgs, typename... Args>
+inline gptq_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
+                              int cluster, cudaStream_t st, Args... args) {
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        cudaGetLastError();
+        return GPTQ_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+    return launch_status();
+}
+
+// Wait for the previous kernel of the stream, then let the next one set up.
+__device__ __forceinline__ void grid_dependency() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
+}  // namespace gptq

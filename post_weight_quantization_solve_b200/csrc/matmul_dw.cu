@@ -1,0 +1,481 @@
+// Products over the rows of each range: G_e (+)= sum over t of P[t]^T Q[t], fp32. The experts'
+// weight gradients (P = dY, Q = X), and the adapters' gradients, where the range of an adapter
+// is the rows of all requests that use it and Q is the rank-space matrix as a pair of 16-bit
+// halves [hi | lo], whose two products are added in the epilogue.
+//
+// Both operands come straight from row-major matrices: rows are the contraction, so a box of
+// 64 rows x 64 columns in the 128-byte swizzle is an MN-major operand. A tile is 128 columns
+// of P (TMEM lanes) x up to 256 columns of Q; the 64-row steps of a range are accumulated in
+// TMEM. Range ends do not fall on step borders: the rows of the last step that belong to
+// others are set to zero in shared memory, in both operands, before the MMAs read it.
+//
+// The tensor core's fp32 accumulation rounds each step the same way, so a chain is at most
+// 2,048 rows (128 MMAs); longer ranges swap accumulators and the epilogue adds the next chain
+// to the stored sum in fp32 to nearest. The same thread adds every chain of an element, in
+// order, so results do not change from run to run.
+//
+// Roles (320 threads): warp 0 tiled copies, warp 1 TMEM, row ends and MMAs, warps 2-5 epilogue,
+// warps 6-9 plain copies where the layout refuses tiled ones.
+#include <algorithm>
+
+#include "matmul.cuh"
+
+namespace gptq {
+
+namespace {
+constexpr int DW_LANES = 128, DW_COLS = 256, DW_BK = 64, DW_STAGES = 4;
+constexpr int DW_BOX = 64 * 64 * 2;
+constexpr int DW_STAGE = (DW_LANES + DW_COLS) * DW_BK * 2;      // 48 KB
+constexpr int DW_EPI = 4 * 32 * 33 * 4;
+constexpr int DW_SMEM = DW_STAGES * DW_STAGE + DW_EPI + 1024 + 256;
+constexpr int DW_THREADS = 320;
+constexpr int DW_CHAIN = 32;                                    // steps of one accumulator
+}  // namespace
+
+struct DwArg {
+    const void *P, *Q;        // [M][ldp], [M][ldq]
+    int64_t ldp, ldq, M;
+    int np, nq;               // their columns
+    const int32_t *offsets;   // [R + 1] row ranges, or NULL (all M rows)
+    const int32_t *list_off;  // [groups + 1] ranges of each group in list, or NULL (range g)
+    const int32_t *list;
+    int R, groups, L;
+    const int32_t *ids;       // checked with the offsets when given
+    int split;                // parts of a group's steps; each writes its own output
+    int pair;                 // Q is [hi | lo]: columns j and j + nq / 2 are added
+    int transposed;           // output [q][p] instead of [p][q]
+    int accumulate;
+    float *out;               // [split][groups][np][nq'] (or [nq'][np])
+    int tiled, vec;
+    int32_t *status;
+};
+
+// The ranges of a group in order, cut to the steps [s0, s1) of one part.
+struct StepWalk {
+    const DwArg &p;
+    int i, iend;              // ranges left
+    int skip, left;           // steps to pass over, steps to take
+    int64_t row, end;         // the current range
+    __device__ __forceinline__ StepWalk(const DwArg &p_, int g, int s0, int s1) : p(p_) {
+        i = p.list_off ? __ldg(p.list_off + g) : g;
+        iend = p.list_off ? __ldg(p.list_off + g + 1) : g + 1;
+        skip = s0;
+        left = s1 - s0;
+        row = end = 0;
+    }
+    static __device__ __forceinline__ void range(const DwArg &p, int i, int64_t &b, int64_t &e) {
+        const int s = p.list ? __ldg(p.list + i) : i;
+        b = p.offsets ? __ldg(p.offsets + s) : 0;
+        e = p.offsets ? __ldg(p.offsets + s + 1) : p.M;
+    }
+    static __device__ __forceinline__ int total(const DwArg &p, int g) {
+        int i = p.list_off ? __ldg(p.list_off + g) : g;
+        const int iend = p.list_off ? __ldg(p.list_off + g + 1) : g + 1;
+        int n = 0;
+        for (; i < iend; ++i) {
+            int64_t b, e;
+            range(p, i, b, e);
+            n += (int)((e - b + DW_BK - 1) / DW_BK);
+        }
+        return n;
+    }
+    // The next step: its first row and how many rows it has.
+    __device__ __forceinline__ bool next(int64_t &r, int &n) {
+        if (left <= 0) return false;
+        while (row >= end) {
+            if (i >= iend) return false;
+            range(p, i++, row, end);
+            const int steps = (int)((end - row + DW_BK - 1) / DW_BK);
+            const int pass = min(skip, steps);
+            row += (int64_t)pass * DW_BK;
+            skip -= pass;
+        }
+        r = row;
+        n = (int)min((int64_t)DW_BK, end - row);
+        row += DW_BK;
+        --left;
+        return true;
+    }
+};
+
+// 64 rows x 64 columns from (r0, c0) into a swizzled box; zeros past `rows` or `cols`.
+template <typename T>
+__device__ __forceinline__ void dw_plain_box(uint8_t *dst, const T *x, int64_t ld, int64_t r0, int rows,
+                                             int c0, int cols, bool vec, int tid, int nthr) {
+    for (int i = tid; i < 64 * 8; i += nthr) {
+        const int r = i >> 3, q = i & 7, c = c0 + 8 * q;
+        uint32_t v[4] = {0u, 0u, 0u, 0u};
+        if (r < rows && c < cols) {
+            const T *src = x + (r0 + r) * ld + c;
+            if (vec && c + 8 <= cols) {
+                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src));
+                v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
+            } else {
+                const unsigned short *s = reinterpret_cast<const unsigned short *>(src);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < cols) v[e >> 1] |= (uint32_t)__ldg(s + e) << (16 * (e & 1));
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst + r * 128 + ((q ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(DW_THREADS, 1)
+    k_matmul_dw(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
+                const __grid_constant__ DwArg p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *epi = reinterpret_cast<float *>(smem + DW_STAGES * DW_STAGE);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + DW_STAGES * DW_STAGE + DW_EPI);
+    uint64_t *empty = full + DW_STAGES;
+    uint64_t *tfull = empty + DW_STAGES;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *drain = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *refuse = reinterpret_cast<int *>(tmem_slot + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < DW_STAGES; ++s) {
+            tc::mbar_init(&full[s], p.tiled ? 1 : 4);
+            tc::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(&tfull[b], 1);
+            tc::mbar_init(&tempty[b], 128);
+        }
+        tc::mbar_init(drain, 1);
+        *abort = 0;
+        *refuse = 0;
+        tc::fence_mbar_init();
+        if (p.tiled) {
+            tc::prefetch_tmap(&pmap);
+            tc::prefetch_tmap(&qmap);
+        }
+    }
+    if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency();
+    bool bad = p.offsets && offsets_bad(p.offsets, p.R, p.M, threadIdx.x, DW_THREADS);
+    if (p.ids) bad |= ids_bad(p.ids, p.R, p.L, threadIdx.x, DW_THREADS);
+    if (bad) *refuse = 1;
+    if (threadIdx.x == 0 && failed(p.status)) *refuse = 2;
+    __syncthreads();
+    if (*refuse == 1 && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_ARG);
+
+    const int tp = (p.np + DW_LANES - 1) / DW_LANES, tq = (p.nq + DW_COLS - 1) / DW_COLS;
+    const int per_group = tp * tq * p.split;
+    const int64_t units = *refuse ? 0 : (int64_t)p.groups * per_group;
+    const int qboxes = (min(p.nq, DW_COLS) + 63) / 64;
+    // unit -> group, part, tile of P fastest
+    auto decode = [&](int64_t u, int &g, int &part, int &pt, int &qt) {
+        g = (int)(u / per_group);
+        int r = (int)(u - (int64_t)g * per_group);
+        part = r / (tp * tq);
+        r -= part * tp * tq;
+        qt = r / tp;
+        pt = r - qt * tp;
+    };
+    auto steps_of = [&](int g, int part, int &s0, int &s1) {
+        const int n = StepWalk::total(p, g);
+        s0 = (int)((int64_t)n * part / p.split);
+        s1 = (int)((int64_t)n * (part + 1) / p.split);
+    };
+
+    if (warp == 0 && p.tiled) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                int g, part, pt, qt, s0, s1, n;
+                int64_t r;
+                decode(u, g, part, pt, qt);
+                steps_of(g, part, s0, s1);
+                StepWalk walk(p, g, s0, s1);
+                const int pb = min(2, (p.np - pt * DW_LANES + 63) / 64);
+                const int qb = min(qboxes, (p.nq - qt * DW_COLS + 63) / 64);
+                while (walk.next(r, n)) {
+                    if (!tc::mbar_wait(&empty[stage], phase ^ 1, abort)) { ok = false; break; }
+                    tc::mbar_arrive_expect_tx(&full[stage], (pb + qb) * DW_BOX);
+                    uint8_t *a = smem + stage * DW_STAGE, *b = a + 2 * DW_BOX;
+                    for (int i = 0; i < pb; ++i)
+                        tc::tma_load_2d(a + i * DW_BOX, &pmap, &full[stage], pt * DW_LANES + 64 * i, (int)r);
+                    for (int i = 0; i < qb; ++i)
+                        tc::tma_load_2d(b + i * DW_BOX, &qmap, &full[stage], qt * DW_COLS + 64 * i, (int)r);
+                    if (++stage == DW_STAGES) { stage = 0; phase ^= 1; }
+                }
+            }
+            if (!ok) {                      // loads still in flight land before the block exits
+                const long long from = clock64();
+                while (clock64() - from < 20000000ll) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            int g, part, pt, qt, s0, s1, n;
+            int64_t r;
+            decode(u, g, part, pt, qt);
+            steps_of(g, part, s0, s1);
+            StepWalk walk(p, g, s0, s1);
+            const int cols = min(DW_COLS, (p.nq - qt * DW_COLS + 15) & ~15);
+            const int qb = (cols + 63) / 64, pb = min(2, (p.np - pt * DW_LANES + 63) / 64);
+            const uint32_t id = tc::idesc_f16_f32(Half2<T>::kType, DW_LANES, cols, 1, 1);
+            int chain = 0;
+            while (ok && walk.next(r, n)) {
+                if (chain == 0) {
+                    ok = tc::mbar_wait(&tempty[acc], acc_phase ^ 1, abort);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                }
+                ok = tc::mbar_wait(&full[stage], phase, abort);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                uint8_t *a = smem + stage * DW_STAGE;
+                if (n < DW_BK) {
+                    // rows n .. the next multiple of 16 belong to others: zero in both operands
+                    const int zero = ((n + 15) & ~15) - n;
+                    for (int i = lane; i < zero * 8 * 6; i += 32) {
+                        const int box = i / (zero * 8), j = i - box * zero * 8;
+                        if (box < 2 ? box < pb : box - 2 < qb)
+                            *reinterpret_cast<uint4 *>(a + box * DW_BOX + (n + (j >> 3)) * 128 + ((j & 7) << 4)) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    tc::fence_async_shared();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    tc::fence_after_sync();
+                    const uint32_t sa = tc::smem_u32(a), sb = sa + 2 * DW_BOX;
+                    const int kks = (n + 15) / 16;
+                    for (int kk = 0; kk < kks; ++kk)
+                        tc::mma_bf16(tmem + acc * DW_COLS, tc::desc_sw128(sa + kk * 2048, DW_BOX, 1024),
+                                     tc::desc_sw128(sb + kk * 2048, DW_BOX, 1024), id, (chain > 0 || kk > 0) ? 1u : 0u);
+                    tc::mma_commit(&empty[stage]);
+                }
+                __syncwarp();
+                if (++stage == DW_STAGES) { stage = 0; phase ^= 1; }
+                if (++chain == DW_CHAIN) {
+                    if (lane == 0) tc::mma_commit(&tfull[acc]);
+                    chain = 0;
+                    if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                }
+            }
+            if (ok && chain > 0) {
+                if (lane == 0) tc::mma_commit(&tfull[acc]);
+                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            }
+        }
+        if (lane == 0) {
+            tc::mma_commit(drain);
+            volatile int never = 0;
+            tc::mbar_wait(drain, 0, &never);
+        }
+    } else if (warp >= 2 && warp < 6) {
+        const int quad = warp & 3;
+        float *buf = epi + (warp - 2) * 32 * 33;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        const int half = p.pair ? p.nq / 2 : 0, nout = p.pair ? half : p.nq;
+        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            int g, part, pt, qt, s0, s1;
+            decode(u, g, part, pt, qt);
+            steps_of(g, part, s0, s1);
+            float *out = p.out + ((int64_t)part * p.groups + g) * p.np * nout;
+            const int r0 = pt * DW_LANES + quad * 32;
+            const int chains = max(1, (s1 - s0 + DW_CHAIN - 1) / DW_CHAIN);
+            for (int c = 0; c < chains && ok; ++c) {
+                const bool none = s1 == s0;             // a range without rows: zeros
+                if (!none) {
+                    ok = tc::mbar_wait(&tfull[acc], acc_phase, abort);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                }
+                const bool add = p.accumulate || c > 0;
+                const int qn = min(DW_COLS, nout - qt * DW_COLS);
+                if (!(none && add)) {
+                    for (int cb = 0; cb < qn; cb += 32) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                        if (!none) {
+                            const uint32_t at = tmem + acc * DW_COLS + cb + ((uint32_t)(quad * 32) << 16);
+                            tc::tmem_ld_32x32b_x32(at, v);
+                            tc::tmem_ld_wait();
+                            if (p.pair) {
+                                uint32_t w[32];
+                                tc::tmem_ld_32x32b_x32(at + half, w);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+                            }
+                        }
+                        const int q0 = qt * DW_COLS + cb;
+                        if (p.transposed) {
+                            if (r0 + lane < p.np) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (cb + i < qn) {
+                                        float *d = out + (int64_t)(q0 + i) * p.np + r0 + lane;
+                                        *d = add ? *d + __uint_as_float(v[i]) : __uint_as_float(v[i]);
+                                    }
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = __uint_as_float(v[i]);
+                            __syncwarp();
+                            const int rows = min(32, p.np - r0);
+                            if (cb + lane < qn) {
+#pragma unroll 8
+                                for (int i = 0; i < rows; ++i) {
+                                    float *d = out + (int64_t)(r0 + i) * nout + q0 + lane;
+                                    const float x = buf[i * 33 + lane];
+                                    *d = add ? *d + x : x;
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    }
+                }
+                if (!none) {
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(&tempty[acc]);
+                    if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                }
+            }
+        }
+    } else if (warp >= 6 && !p.tiled) {
+        const int tid = threadIdx.x - 192;
+        const T *P = static_cast<const T *>(p.P), *Q = static_cast<const T *>(p.Q);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            int g, part, pt, qt, s0, s1, n;
+            int64_t r;
+            decode(u, g, part, pt, qt);
+            steps_of(g, part, s0, s1);
+            StepWalk walk(p, g, s0, s1);
+            const int pb = min(2, (p.np - pt * DW_LANES + 63) / 64);
+            const int qb = min(qboxes, (p.nq - qt * DW_COLS + 63) / 64);
+            while (ok && walk.next(r, n)) {
+                ok = tc::mbar_wait(&empty[stage], phase ^ 1, abort);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                uint8_t *a = smem + stage * DW_STAGE, *b = a + 2 * DW_BOX;
+                for (int i = 0; i < pb; ++i)
+                    dw_plain_box<T>(a + i * DW_BOX, P, p.ldp, r, n, pt * DW_LANES + 64 * i, p.np, (p.vec & 1) != 0, tid, 128);
+                for (int i = 0; i < qb; ++i)
+                    dw_plain_box<T>(b + i * DW_BOX, Q, p.ldq, r, n, qt * DW_COLS + 64 * i, p.nq, (p.vec & 2) != 0, tid, 128);
+                tc::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&full[stage]);
+                if (++stage == DW_STAGES) { stage = 0; phase ^= 1; }
+            }
+        }
+    }
+
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (*abort && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_TIMEOUT);
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// out[i] = the parts' sum, parts in order.
+__global__ void __launch_bounds__(256) k_sum_parts(const float *__restrict__ parts, int split, int64_t n,
+                                                   float *__restrict__ out, const int32_t *status) {
+    grid_dependency();
+    if (failed(status)) return;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float s = 0.f;
+    for (int k = 0; k < split; ++k) s += parts[k * n + i];
+    out[i] = s;
+}
+
+static gptq_status launch_dw(DwArg &p, int dtype, cudaStream_t st) {
+    CUtensorMap pm{}, qm{};
+    p.tiled = rows_map(&pm, p.P, dtype, p.M, p.np, p.ldp, DW_BK) &&
+              rows_map(&qm, p.Q, dtype, p.M, p.nq, p.ldq, DW_BK);
+    p.vec = (aligned(p.P, 16) && p.ldp % 8 == 0 ? 1 : 0) | (aligned(p.Q, 16) && p.ldq % 8 == 0 ? 2 : 0);
+    const int64_t tiles = (int64_t)((p.np + DW_LANES - 1) / DW_LANES) * ((p.nq + DW_COLS - 1) / DW_COLS);
+    const int64_t units = tiles * p.groups * p.split;
+    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(units, device_sms()));
+    if (dtype == GPTQ_BF16)
+        return launch_pdl(k_matmul_dw<__nv_bfloat16>, dim3(blocks), DW_THREADS, DW_SMEM, 1, st, pm, qm, p);
+    return launch_pdl(k_matmul_dw<__half>, dim3(blocks), DW_THREADS, DW_SMEM, 1, st, pm, qm, p);
+}
+
+// G[e] (+)= dY^T X over the rows of range e.
+gptq_status matmul_dw(float *G, const void *dY, int64_t lddy, const void *X, int64_t ldx, int dtype,
+                      int64_t M, int N, int K, int E, const int32_t *offsets, int accumulate,
+                      int32_t *status, cudaStream_t st) {
+    DwArg p{};
+    p.P = dY; p.ldp = lddy; p.np = N;
+    p.Q = X; p.ldq = ldx; p.nq = K;
+    p.M = M;
+    p.offsets = offsets;
+    p.R = p.groups = E;
+    p.split = 1;
+    p.accumulate = accumulate;
+    p.out = G;
+    p.status = status;
+    return launch_dw(p, dtype, st);
+}
+
+// Parts of an adapter's rows: enough blocks to fill the machine, at least 512 rows a part.
+int adapter_parts(int64_t M, int L, int width) {
+    const int64_t tiles = (int64_t)L * ((width + DW_LANES - 1) / DW_LANES);
+    int64_t s = (device_sms() + tiles - 1) / std::max<int64_t>(1, tiles);
+    s = std::min(s, M / 512);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(s, 16));
+}
+
+// One adapter gradient: dB[a][n][j] = sum dY[t][n] T[t][j] (transposed 0) or
+// dA[a][j][k] = sum U[t][j] X[t][k] (transposed 1), rows of the requests listed for a.
+gptq_status adapter_gradient(float *out, float *parts, int split, const void *P, int64_t ldp, int np,
+                             const void *T2, int rank, int transposed, int dtype, int64_t M,
+                             const int32_t *offsets, const int32_t *ids, const int32_t *list_off,
+                             const int32_t *list, int R, int L, int32_t *status, cudaStream_t st) {
+    DwArg p{};
+    p.P = P; p.ldp = ldp; p.np = np;
+    p.Q = T2; p.ldq = 2 * rank; p.nq = 2 * rank;
+    p.M = M;
+    p.offsets = offsets;
+    p.list_off = list_off;
+    p.list = list;
+    p.R = R;
+    p.groups = p.L = L;
+    p.ids = ids;
+    p.split = split;
+    p.pair = 1;
+    p.transposed = transposed;
+    p.out = split > 1 ? parts : out;
+    p.status = status;
+    gptq_status s = launch_dw(p, dtype, st);
+    if (s != GPTQ_OK || split == 1) return s;
+    const int64_t n = (int64_t)L * np * rank;
+    return launch_pdl(k_sum_parts, dim3((unsigned)((n + 255) / 256)), 256, 0, 1, st, (const float *)parts, split,
+                      n, out, (const int32_t *)status);
+}
+
+}  // namespace gptq
