@@ -152,6 +152,8 @@ def _check_layout(t, name, rows=False):
 
 def _stream(stream, dev=None):
     if stream is None:
+        if dev is not None and dev.index is not None:
+            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev.index))
         stream = torch.cuda.current_stream(dev)
     elif dev is not None and stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the call runs on {dev}")
@@ -395,77 +397,97 @@ def gptq_unpack_codes(words, bits, K, codes=None, stream=None):
     return codes
 
 
-def _rows(t, dev, name, cols=None, dtype=None):
-    """(pointer, row pitch, 16-bit dtype code) of a [rows][cols] matrix of 16-bit values."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+# The products are called once a layer and token, so their checks are written for few tensor
+# attribute reads: one _need a tensor.
+_ROW_CODES = {torch.bfloat16: GPTQ_BF16, torch.float16: GPTQ_F16}
+
+
+def _need(t, dev, name):
+    """A CUDA tensor on the call's device."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        _ptr(t, dev, name)
+        if t is None:
+            raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _rows(t, dev, name, cols=None, like=None):
+    """(rows, columns, pointer, row pitch) of a matrix of 16-bit values."""
+    _need(t, dev, name)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
-    if t.dtype == torch.bfloat16:
-        code = GPTQ_BF16
-    elif t.dtype == torch.float16:
-        code = GPTQ_F16
-    else:
-        raise TypeError(f"{name}: bfloat16 or float16 rows, got {t.dtype}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if cols is not None and t.shape[1] != cols:
-        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
+    if like is None:
+        if t.dtype not in _ROW_CODES:
+            raise TypeError(f"{name}: bfloat16 or float16 rows, got {t.dtype}")
+    elif t.dtype != like:
+        raise TypeError(f"{name} is {t.dtype}, expected {like}")
+    M, n = shape
+    if cols is not None and n != cols:
+        raise ValueError(f"{name} has {n} columns, expected {cols}")
+    if stride[1] != 1 and n > 1 and M > 0:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
     # the pitch of a single row is never used
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-    return _ptr(t, dev, name, rows=True), ld, code
+    return M, n, t.data_ptr(), stride[0] if M > 1 else max(stride[0], n)
 
 
 def _typed(t, dev, name, dtype, shape):
     """Pointer of a dense tensor of the given type and shape (None stays None)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a CUDA tensor")
+    _need(t, dev, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return _ptr(t, dev, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _packed(words, scales, bits, K, groupsize, g_idx, dev):
     """gptq_packed of words [E][N][>= nw] or [N][>= nw] with its scales and g_idx."""
-    if not isinstance(words, torch.Tensor) or words.dim() not in (2, 3):
+    if not isinstance(words, torch.Tensor):
+        raise ValueError("words must be a CUDA tensor")
+    shape, stride = words.shape, words.stride()
+    if len(shape) not in (2, 3):
         raise ValueError("words must be [N][words] or [experts][N][words]")
-    if words.dtype not in (torch.int32, torch.uint32):
+    if words.dtype != torch.int32 and words.dtype != torch.uint32:
         raise TypeError(f"words: int32 (bit patterns) or uint32, got {words.dtype}")
-    if words.shape[-1] < (K * bits + 31) // 32:
-        raise ValueError(f"words has {words.shape[-1]} words a row, {K} columns of {bits} bits need "
+    if shape[-1] < (K * bits + 31) // 32:
+        raise ValueError(f"words has {shape[-1]} words a row, {K} columns of {bits} bits need "
                          f"{(K * bits + 31) // 32}")
-    E, N = (1, words.shape[0]) if words.dim() == 2 else words.shape[:2]
-    ld = words.stride(-2) if E * N > 1 else words.shape[-1]
-    if words.dim() == 3 and N == 1 and E > 1:
-        ld = words.stride(0)
-    elif words.dim() == 3 and E > 1 and words.stride(0) != N * ld:
+    _need(words, dev, "words")
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise ValueError("words: the elements of a row must be contiguous")
+    lead = len(shape) == 3
+    E, N = shape[:2] if lead else (1, shape[0])
+    ld = stride[-2] if N > 1 else stride[0] if E > 1 else shape[-1]
+    if E > 1 and N > 1 and stride[0] != N * ld:
         raise ValueError("words: the experts' rows must follow one another at one pitch")
-    groups = (K + groupsize - 1) // groupsize if groupsize else 0
-    lead = () if words.dim() == 2 else (E,)
-    W = GPTQPacked()
-    W.words = _ptr(words, dev, "words", rows=True)
-    W.ld_words = ld
-    W.scales = _typed(scales, dev, "scales", torch.float32, lead + ((N, groups) if groupsize else (N,)))
     if g_idx is not None and not groupsize:
         raise ValueError("g_idx needs a groupsize")
-    W.g_idx = _typed(g_idx, dev, "g_idx", torch.int32, lead + (K,))
-    W.experts, W.N, W.K, W.bits, W.groupsize = E, N, K, bits, groupsize
-    return W
+    tail = (N, (K + groupsize - 1) // groupsize) if groupsize else (N,)
+    return GPTQPacked(words.data_ptr(), ld,
+                      _typed(scales, dev, "scales", torch.float32, (E, *tail) if lead else tail) or 0,
+                      _typed(g_idx, dev, "g_idx", torch.int32, (E, K) if lead else (K,)),
+                      E, N, K, bits, groupsize)
 
 
 def _offsets(offsets, dev, n):
     return _typed(offsets, dev, "offsets", torch.int32, (n + 1,))
 
 
-def _scratch(nbytes, dev, workspace, stream):
-    """The caller's workspace, or a new one that outlives the call on its stream."""
-    if workspace is None:
-        workspace = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+def _out(out, M, cols, like, dev, name, stream):
+    """(tensor, pointer, pitch) of a call's output rows: the caller's, or a new tensor."""
+    if out is None:
+        out = torch.empty((M, cols), dtype=like, device=dev)
         if stream is not None:
-            workspace.record_stream(stream)
-    return workspace, _ptr(workspace, dev, "workspace"), workspace.numel() * workspace.element_size()
+            out.record_stream(stream)
+        return out, out.data_ptr(), cols
+    rows, _, p, ld = _rows(out, dev, name, cols, like)
+    if rows != M:
+        raise ValueError(f"{name} has {rows} rows, the call has {M}")
+    return out, p, ld
 
 
 def _fresh(shape, dtype, dev, stream):
@@ -475,48 +497,58 @@ def _fresh(shape, dtype, dev, stream):
     return out
 
 
+def _scratch(nbytes, dev, workspace, stream):
+    """(tensor, pointer, bytes): the caller's workspace, or a new one that outlives the call on
+    its stream."""
+    if workspace is None:
+        workspace = _fresh((max(int(nbytes), 256),), torch.uint8, dev, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _need(workspace, dev, "workspace")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _enqueue(name, dev, args, status, stream):
+    """Call an entry point with the status word and the stream, its device current."""
+    fn = getattr(load_library(), name)
+    st = None if status is None else _typed(status, dev, "status", torch.int32, (1,))
+    if dev.type == "cuda" and torch.cuda.current_device() == dev.index:
+        code = fn(*args, st, _stream(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, st, _stream(stream, dev))
+    if code != GPTQ_OK:
+        raise GPTQError(code, name)
+
+
 def gptq_matmul_grouped(X, words, scales, bits, offsets=None, groupsize=0, g_idx=None, out=None,
                         status=None, stream=None):
     """out[t] = W^_e X[t] for offsets[e] <= t < offsets[e + 1] over packed layers (see
-    include/gptq_matmul.h). words [experts][N][..] or [N][..] (one layer; then scales and g_idx
-    have no leading dimension either). Without `out`, a new [M][N] tensor, whose rows
+    include/gptq_matmul.h). words [experts][N][..] or [N][..] (one layer; then scales and
+    g_idx have no leading dimension either). Without `out`, a new [M][N] tensor, whose rows
     outside the ranges are not initialised. Returns out."""
-    lib = load_library()
     dev = _device(X, "X")
-    x, ldx, code = _rows(X, dev, "X")
-    M, K = X.shape
+    M, K, x, ldx = _rows(X, dev, "X")
+    t = X.dtype
     W = _packed(words, scales, bits, K, groupsize, g_idx, dev)
-    if out is None:
-        out = _fresh((M, W.N), X.dtype, dev, stream)
-    y, ldy, _ = _rows(out, dev, "out", W.N, X.dtype)
-    if out.shape[0] != M:
-        raise ValueError(f"out has {out.shape[0]} rows, X has {M}")
-    args = (y, ldy, x, ldx, code, M, ctypes.byref(W), _offsets(offsets, dev, W.experts),
-            _ptr(status, dev, "status"), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        code = lib.gptq_matmul_grouped(*args)
-    _check(code, "gptq_matmul_grouped")
+    out, y, ldy = _out(out, M, W.N, t, dev, "out", stream)
+    _enqueue("gptq_matmul_grouped", dev,
+             (y, ldy, x, ldx, _ROW_CODES[t], M, W, _offsets(offsets, dev, W.experts)), status, stream)
     return out
 
 
 def gptq_matmul_grouped_dx(dY, words, scales, bits, K, offsets=None, groupsize=0, g_idx=None,
                            out=None, status=None, stream=None):
     """out[t] = W^_e^T dY[t]: the gradient of gptq_matmul_grouped's rows ([M][K])."""
-    lib = load_library()
     dev = _device(dY, "dY")
-    d, ldd, code = _rows(dY, dev, "dY", words.shape[-2] if isinstance(words, torch.Tensor) else None)
-    M = dY.shape[0]
+    M, N, d, ldd = _rows(dY, dev, "dY")
+    t = dY.dtype
     W = _packed(words, scales, bits, K, groupsize, g_idx, dev)
-    if out is None:
-        out = _fresh((M, K), dY.dtype, dev, stream)
-    y, ldy, _ = _rows(out, dev, "out", K, dY.dtype)
-    if out.shape[0] != M:
-        raise ValueError(f"out has {out.shape[0]} rows, dY has {M}")
-    args = (y, ldy, d, ldd, code, M, ctypes.byref(W), _offsets(offsets, dev, W.experts),
-            _ptr(status, dev, "status"), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        code = lib.gptq_matmul_grouped_dx(*args)
-    _check(code, "gptq_matmul_grouped_dx")
+    if W.N != N:
+        raise ValueError(f"dY has {N} columns, the layer has {W.N} channels")
+    out, y, ldy = _out(out, M, K, t, dev, "out", stream)
+    _enqueue("gptq_matmul_grouped_dx", dev,
+             (y, ldy, d, ldd, _ROW_CODES[t], M, W, _offsets(offsets, dev, W.experts)), status, stream)
     return out
 
 
@@ -524,25 +556,22 @@ def gptq_matmul_grouped_dw(dY, X, offsets=None, experts=None, out=None, accumula
                            status=None, stream=None):
     """out[e] = sum of dY[t]^T X[t] over the rows of expert e, fp32 [experts][N][K] (added to
     `out` with accumulate=True). experts: from `offsets` when not given; 1 without them."""
-    lib = load_library()
     dev = _device(dY, "dY")
-    d, ldd, code = _rows(dY, dev, "dY")
-    x, ldx, _ = _rows(X, dev, "X", None, dY.dtype)
-    if X.shape[0] != dY.shape[0]:
-        raise ValueError(f"X has {X.shape[0]} rows, dY has {dY.shape[0]}")
+    M, N, d, ldd = _rows(dY, dev, "dY")
+    t = dY.dtype
+    rows, K, x, ldx = _rows(X, dev, "X", None, t)
+    if rows != M:
+        raise ValueError(f"X has {rows} rows, dY has {M}")
     if experts is None:
         experts = 1 if offsets is None else offsets.shape[0] - 1
-    M, N, K = dY.shape[0], dY.shape[1], X.shape[1]
     if out is None:
         if accumulate:
             raise ValueError("accumulate=True needs `out`")
         out = _fresh((experts, N, K), torch.float32, dev, stream)
-    args = (_typed(out, dev, "out", torch.float32, (experts, N, K)), d, ldd, x, ldx, code, M, N, K,
-            experts, _offsets(offsets, dev, experts), int(bool(accumulate)),
-            _ptr(status, dev, "status"), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        code = lib.gptq_matmul_grouped_dw(*args)
-    _check(code, "gptq_matmul_grouped_dw")
+    _enqueue("gptq_matmul_grouped_dw", dev,
+             (_typed(out, dev, "out", torch.float32, (experts, N, K)), d, ldd, x, ldx, _ROW_CODES[t],
+              M, N, K, experts, _offsets(offsets, dev, experts), int(bool(accumulate))),
+             status, stream)
     return out
 
 
@@ -552,7 +581,7 @@ def _adapter_args(A, B, alpha, offsets, ids, dtype, N, K, dev):
         raise ValueError("A must be [adapters][rank][K]")
     if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
         raise ValueError("ids must be a 1-D int32 tensor")
-    L, r, R = A.shape[0], A.shape[1], ids.shape[0]
+    (L, r, _), R = A.shape, ids.shape[0]
     return (_typed(A, dev, "A", dtype, (L, r, K)), _typed(B, dev, "B", dtype, (L, N, r)),
             _typed(alpha, dev, "alpha", torch.float32, (L,)), L, r, _offsets(offsets, dev, R),
             _typed(ids, dev, "ids", torch.int32, (R,)), R)
@@ -566,24 +595,16 @@ def gptq_matmul_lora(X, words, scales, bits, A, B, alpha, offsets, ids, groupsiz
                      out=None, workspace=None, status=None, stream=None):
     """out[t] = W^ X[t] + alpha[a] B[a] A[a] X[t], a the adapter of t's request (ids[r] for
     offsets[r] <= t < offsets[r + 1], -1 none); see include/gptq_matmul.h. Returns out."""
-    lib = load_library()
     dev = _device(X, "X")
-    x, ldx, code = _rows(X, dev, "X")
-    M, K = X.shape
+    M, K, x, ldx = _rows(X, dev, "X")
+    t = X.dtype
     W = _packed(words, scales, bits, K, groupsize, g_idx, dev)
-    a = _adapter_args(A, B, alpha, offsets, ids, X.dtype, W.N, K, dev)
-    if out is None:
-        out = _fresh((M, W.N), X.dtype, dev, stream)
-    y, ldy, _ = _rows(out, dev, "out", W.N, X.dtype)
-    if out.shape[0] != M:
-        raise ValueError(f"out has {out.shape[0]} rows, X has {M}")
-    need = lib.gptq_lora_workspace_size(0, M, W.N, K, a[7], a[3], a[4])
-    workspace, ws, nbytes = _scratch(need, dev, workspace, stream)
-    args = (y, ldy, x, ldx, code, M, ctypes.byref(W), *a, ws, nbytes, _ptr(status, dev, "status"),
-            _stream(stream, dev))
-    with torch.cuda.device(dev):
-        code = lib.gptq_matmul_lora(*args)
-    _check(code, "gptq_matmul_lora")
+    a = _adapter_args(A, B, alpha, offsets, ids, t, W.N, K, dev)
+    out, y, ldy = _out(out, M, W.N, t, dev, "out", stream)
+    workspace, ws, nbytes = _scratch(gptq_lora_workspace_size(0, M, W.N, K, a[7], a[3], a[4]), dev,
+                                     workspace, stream)
+    _enqueue("gptq_matmul_lora", dev, (y, ldy, x, ldx, _ROW_CODES[t], M, W, *a, ws, nbytes), status,
+             stream)
     return out
 
 
@@ -592,35 +613,29 @@ def gptq_matmul_lora_backward(dY, X, words, scales, bits, A, B, alpha, offsets, 
                               workspace=None, status=None, stream=None):
     """(dX, dA, dB) of gptq_matmul_lora; `want` leaves out gradients (None in their place).
     dX is of dY's type, dA and dB fp32; see include/gptq_matmul.h."""
-    lib = load_library()
     dev = _device(dY, "dY")
-    d, ldd, code = _rows(dY, dev, "dY")
-    x, ldx, _ = _rows(X, dev, "X", None, dY.dtype)
-    (M, N), K = dY.shape, X.shape[1]
-    if X.shape[0] != M:
-        raise ValueError(f"X has {X.shape[0]} rows, dY has {M}")
+    M, N, d, ldd = _rows(dY, dev, "dY")
+    t = dY.dtype
+    rows, K, x, ldx = _rows(X, dev, "X", None, t)
+    if rows != M:
+        raise ValueError(f"X has {rows} rows, dY has {M}")
     W = _packed(words, scales, bits, K, groupsize, g_idx, dev)
     if W.N != N:
         raise ValueError(f"dY has {N} columns, the layer has {W.N} channels")
-    a = _adapter_args(A, B, alpha, offsets, ids, dY.dtype, N, K, dev)
+    a = _adapter_args(A, B, alpha, offsets, ids, t, N, K, dev)
     L, r = a[3], a[4]
-    dX = (_fresh((M, K), dY.dtype, dev, stream) if dX is None else dX) if want[0] else None
+    g, ldg = None, K
+    if want[0]:
+        dX, g, ldg = _out(dX, M, K, t, dev, "dX", stream)
     dA = (_fresh((L, r, K), torch.float32, dev, stream) if dA is None else dA) if want[1] else None
     dB = (_fresh((L, N, r), torch.float32, dev, stream) if dB is None else dB) if want[2] else None
-    g, ldg = None, K
-    if dX is not None:
-        g, ldg, _ = _rows(dX, dev, "dX", K, dY.dtype)
-        if dX.shape[0] != M:
-            raise ValueError(f"dX has {dX.shape[0]} rows, dY has {M}")
-    need = lib.gptq_lora_workspace_size(1, M, N, K, a[7], L, r)
-    workspace, ws, nbytes = _scratch(need, dev, workspace, stream)
-    args = (g, ldg, _typed(dA, dev, "dA", torch.float32, (L, r, K)),
-            _typed(dB, dev, "dB", torch.float32, (L, N, r)), d, ldd, x, ldx, code, M,
-            ctypes.byref(W), *a, ws, nbytes, _ptr(status, dev, "status"), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        code = lib.gptq_matmul_lora_backward(*args)
-    _check(code, "gptq_matmul_lora_backward")
-    return dX, dA, dB
+    workspace, ws, nbytes = _scratch(gptq_lora_workspace_size(1, M, N, K, a[7], L, r), dev, workspace,
+                                     stream)
+    _enqueue("gptq_matmul_lora_backward", dev,
+             (g, ldg, _typed(dA, dev, "dA", torch.float32, (L, r, K)),
+              _typed(dB, dev, "dB", torch.float32, (L, N, r)), d, ldd, x, ldx, _ROW_CODES[t], M, W, *a,
+              ws, nbytes), status, stream)
+    return dX if want[0] else None, dA, dB
 
 
 def gptq_first_order_shift(W, U, G, beta, gamma=None, workspace=None, status=None, stream=None):

@@ -63,6 +63,16 @@ struct Half2<__nv_bfloat16> {
         asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
         return d;
     }
+    // (128 + c 2^UP) / 2^UP - 128 / 2^UP - Z = c - Z, every step exact
+    template <int UP, int Z>
+    static __device__ __forceinline__ uint32_t scaled(uint32_t v) {
+        constexpr uint32_t inv = (127u - UP) << 7;                     // 2^-UP
+        constexpr float c = -(128.f / (1 << UP) + Z);
+        uint32_t d, cc;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(cc) : "f"(c));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(inv * 0x00010001u), "r"(cc));
+        return d;
+    }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t d;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -79,6 +89,16 @@ struct Half2<__half> {
     static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
         uint32_t d;
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    // (1024 + c 2^UP) / 2^UP - 1024 / 2^UP - Z = c - Z, every step exact
+    template <int UP, int Z>
+    static __device__ __forceinline__ uint32_t scaled(uint32_t v) {
+        constexpr uint32_t inv = (15u - UP) << 10;
+        constexpr float c = -(1024.f / (1 << UP) + Z);
+        uint32_t d, cc;
+        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(cc) : "f"(c));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(inv * 0x00010001u), "r"(cc));
         return d;
     }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -104,11 +124,34 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a) {
     return d;
 }
 
-// 32 codes (B words) -> c - z as 16 pairs in column order. Each code is placed under the
-// exponent bits of 128 (bf16) or 1024 (fp16), where its value is the number's low mantissa;
-// one packed subtraction then gives c - z exactly. Codes come out of a word two 16-bit lanes
-// at a time (code i with code i + 4, ...); byte permutes put neighbours together.
-template <int B, typename T>
+// 32 codes (B words) -> c - z as 16 pairs. Each code is placed under the exponent bits of 128
+// (bf16) or 1024 (fp16), where its value is the number's low mantissa; one packed operation then
+// gives c - z exactly: a subtraction, or, for a code masked in place a few bits up in the
+// mantissa (128 + 8 c), a multiply-add by the power of two, which saves the shift.
+// Codes come out of a word two 16-bit lanes at a time (code i with code i + 4, or i + 8 for 2
+// bits). NATURAL: byte permutes put neighbouring columns together; otherwise the pairs stay as
+// they come, in the order of pair_column, for a reader whose rows are in that order too.
+template <int B, bool NATURAL>
+__host__ __device__ constexpr int pair_column(int i, int h) {
+    return NATURAL || B == 8 ? 2 * i + h
+           : B == 2          ? (i / 8) * 16 + i % 8 + 8 * h
+                             : (i / 4) * 8 + i % 4 + 4 * h;
+}
+
+// q[J..]: codes J.. of both lanes of a field as c - z. Code J sits at bit B (J mod PER) of the
+// field shifted by whole runs of PER codes.
+template <int B, typename T, int J, int LANE, int PER, uint32_t MASK, int Z>
+__device__ __forceinline__ void pair_fields(uint32_t f, uint32_t (&q)[LANE]) {
+    if constexpr (J < LANE) {
+        constexpr int UP = B * (J % PER);
+        const uint32_t v = and_or<(MASK << UP), Half2<T>::kMagic>(f >> (B * (J - J % PER)));
+        if constexpr (UP == 0) q[J] = Half2<T>::sub(v, Half2<T>::kMagic + Z * 0x00010001u);
+        else q[J] = Half2<T>::template scaled<UP, Z>(v);
+        pair_fields<B, T, J + 1, LANE, PER, MASK, Z>(f, q);
+    }
+}
+
+template <int B, typename T, bool NATURAL = true>
 __device__ __forceinline__ void unpack32(const uint32_t (&w)[B], uint32_t (&out)[16]) {
     using H = Half2<T>;
     constexpr uint32_t M = H::kMagic;
@@ -130,52 +173,37 @@ __device__ __forceinline__ void unpack32(const uint32_t (&w)[B], uint32_t (&out)
                 }
             }
         }
-    } else if constexpr (B == 4) {
-        constexpr uint32_t Z = M + 0x00080008u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t v = w[i];
-            const uint32_t a = H::sub(and_or<0x000f000fu, M>(v), Z);           // c0 c4
-            const uint32_t b = H::sub(and_or<0x000f000fu, M>(v >> 4), Z);      // c1 c5
-            const uint32_t c = H::sub(and_or<0x000f000fu, M>(v >> 8), Z);      // c2 c6
-            const uint32_t d = H::sub(and_or<0x000f000fu, M>(v >> 12), Z);     // c3 c7
-            out[4 * i + 0] = __byte_perm(a, b, 0x5410);
-            out[4 * i + 1] = __byte_perm(c, d, 0x5410);
-            out[4 * i + 2] = __byte_perm(a, b, 0x7632);
-            out[4 * i + 3] = __byte_perm(c, d, 0x7632);
-        }
-    } else if constexpr (B == 2) {
-        constexpr uint32_t Z = M + 0x00020002u;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t q[8];                                                     // c_j c_(j+8)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = H::sub(and_or<0x00030003u, M>(w[i] >> (2 * j)), Z);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                out[8 * i + j] = __byte_perm(q[2 * j], q[2 * j + 1], 0x5410);
-                out[8 * i + 4 + j] = __byte_perm(q[2 * j], q[2 * j + 1], 0x7632);
-            }
-        }
     } else {
-        static_assert(B == 3, "bits");
-        constexpr uint32_t Z = M + 0x00040004u;
+        // fields of four (2 bits: eight) codes in each 16-bit lane, and a word's worth of them
+        constexpr int LANE = B == 2 ? 8 : 4, FIELDS = 16 / LANE;
+        constexpr uint32_t MASK = ((1u << B) - 1u) * 0x00010001u;
+        constexpr int z = 1 << (B - 1);
+        constexpr int MANT = H::kType == 1 ? 7 : 10;         // mantissa bits that hold codes
+        constexpr int PER = MANT / B;                        // codes read without a shift
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // the 24 bits of codes 8i .. 8i + 7, four codes to a 16-bit lane
-            const uint32_t g = i == 0 ? w[0]
-                               : i == 1 ? __funnelshift_r(w[0], w[1], 24)
-                               : i == 2 ? __funnelshift_r(w[1], w[2], 16)
-                                        : (w[2] >> 8);
-            const uint32_t h = (g & 0xfffu) | ((g << 4) & 0x0fff0000u);
-            const uint32_t a = H::sub(and_or<0x00070007u, M>(h), Z);
-            const uint32_t b = H::sub(and_or<0x00070007u, M>(h >> 3), Z);
-            const uint32_t c = H::sub(and_or<0x00070007u, M>(h >> 6), Z);
-            const uint32_t d = H::sub(and_or<0x00070007u, M>(h >> 9), Z);
-            out[4 * i + 0] = __byte_perm(a, b, 0x5410);
-            out[4 * i + 1] = __byte_perm(c, d, 0x5410);
-            out[4 * i + 2] = __byte_perm(a, b, 0x7632);
-            out[4 * i + 3] = __byte_perm(c, d, 0x7632);
+        for (int i = 0; i < FIELDS; ++i) {
+            uint32_t f;
+            if constexpr (B == 3) {
+                const uint32_t g = i == 0 ? w[0]
+                                   : i == 1 ? __funnelshift_r(w[0], w[1], 24)
+                                   : i == 2 ? __funnelshift_r(w[1], w[2], 16)
+                                            : (w[2] >> 8);
+                f = (g & 0xfffu) | ((g << 4) & 0x0fff0000u);
+            } else {
+                f = w[i];
+            }
+            uint32_t q[LANE];
+            pair_fields<B, T, 0, LANE, PER, MASK, z>(f, q);
+            if constexpr (NATURAL) {
+#pragma unroll
+                for (int j = 0; j < LANE / 2; ++j) {
+                    out[LANE * i + j] = __byte_perm(q[2 * j], q[2 * j + 1], 0x5410);
+                    out[LANE * i + LANE / 2 + j] = __byte_perm(q[2 * j], q[2 * j + 1], 0x7632);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < LANE; ++j) out[LANE * i + j] = q[j];
+            }
         }
     }
 }
@@ -204,17 +232,17 @@ __device__ __forceinline__ void scale32(uint32_t (&v)[16], float s) {
     }
 }
 
-// The 32 values of columns k0 .. k0 + 31, each times the scale of its column's group.
-template <typename T>
-__device__ __forceinline__ void scale32_by_index(uint32_t (&v)[16], const float *row_scales,
-                                                 const int32_t *g_idx, int k0, int K, int groups,
-                                                 int32_t *status) {
-#pragma unroll
+// The 32 values of columns k0 .. k0 + 31, each times the scale of its column's group. Out of
+// line: 64 dependent reads a chunk, whatever the registers around it.
+template <typename T, int B, bool NATURAL>
+__device__ __noinline__ void scale32_indexed(uint32_t *v, const float *row_scales, const int32_t *g_idx,
+                                             int k0, int K, int groups, int32_t *status) {
+#pragma unroll 4
     for (int i = 0; i < 16; ++i) {
         float s[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int k = k0 + 2 * i + h;
+            const int k = k0 + pair_column<B, NATURAL>(i, h);
             int g = k < K ? __ldg(g_idx + k) : 0;
             if ((unsigned)g >= (unsigned)groups) {
                 set_status(status, GPTQ_ERR_ARG);
@@ -225,6 +253,18 @@ __device__ __forceinline__ void scale32_by_index(uint32_t (&v)[16], const float 
         const float2 f = Half2<T>::unpack(v[i]);
         v[i] = Half2<T>::pack(f.x * s[0], f.y * s[1]);
     }
+}
+
+template <typename T, int B, bool NATURAL>
+__device__ __forceinline__ void scale32_by_index(uint32_t (&v)[16], const float *row_scales,
+                                                 const int32_t *g_idx, int k0, int K, int groups,
+                                                 int32_t *status) {
+    uint32_t t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i] = v[i];
+    scale32_indexed<T, B, NATURAL>(t, row_scales, g_idx, k0, K, groups, status);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = t[i];
 }
 
 // B words of chunk `chunk` of a row; words at or past the row's end read as zero. `row` NULL:

@@ -1,0 +1,844 @@
+// Packed-weight products on the tensor cores: Y[t] = W^_e X[t] (forward) and
+// dX[t] = W^_e^T dY[t] (input gradient) over row ranges of experts, with the low-rank
+// adapters of the rows' requests added in the same accumulators.
+//
+// One tile is 128 output channels (TMEM lanes) x up to 256 rows (TMEM columns): the weights
+// are the A operand, so a tile's row count is free (multiples of 16) and a short range of an
+// expert costs no more matrix work than it has rows. The contraction runs in steps of 128, one
+// stage of the operand rings and one round of barriers each (with steps of 64 the rounds, not the
+// MMAs, set the pace: the warp that issues the copies of X needed 690 clocks a round):
+//   forward         a thread unpacks 64 codes of its own channel (lane) and stores them into
+//                   TMEM, where the MMA reads A; only the rows X go through shared memory.
+//   input gradient  the contraction runs over the packed rows n, so a thread unpacks 64 codes
+//                   of one n into a [n][k] tile of shared memory, read as an MN-major A.
+// PAIR: two blocks share a tile of 256 channels (cta_group::2): each unpacks its own 128
+// channels and loads half of the rows' operand, which the pair's MMAs read from both, so the
+// operand traffic of an SM halves; that is what bounds the single-block form (one block's
+// MMAs alone, without unpacking, ran at 1.25 PFLOP/s on an 8,192 x 4,096 x 14,336 product).
+//
+// Scales: with one scale a channel the forward product multiplies exact integers c - z and the
+// scale enters in fp32 at the end. Where the scale changes along the contraction (input
+// groups, the input gradient) or adapters share the accumulators, each weight s (c - z) is
+// rounded once to the rows' 16-bit type, as a dequantised layer in that type would hold it.
+//
+// Adapters: after the steps of W^, each run of rows with one adapter adds
+// sum_j P_a[.][j] T[t][j] over the run's columns alone (runs are widened to the MMA's column borders,
+// the rows there that belong to others are zero in shared memory). T comes as a pair of 16-bit
+// halves, so the rank-space rows keep 16 bits.
+//
+// Order: the tiles of a range run rows first, so that blocks that work at the same time read
+// different rows of X and the same (few) words; with channels first every block asked the L2
+// for the same lines of X at once, and the pair's MMAs waited (54 % tensor-pipe cycles).
+//
+// Roles (512 threads): warps 0-7 unpack, four to each half of a step; warps 8-11 write the
+// outputs; warp 12 issues the tiled copies of X; warp 13 owns TMEM and issues the MMAs; warps
+// 14-15 bring the packed words, 128 rows x 128 codes (a step) at a time, through a ring of their
+// own that runs ahead across tiles. Tiles of at most 128 rows use two accumulators in turn, so a
+// tile's end costs the next one nothing.
+#pragma once
+
+#include <algorithm>
+
+#include "matmul.cuh"
+
+namespace gptq {
+
+constexpr int MM_LANES = 128;                       // output channels of a block's tile
+constexpr int MM_BK = 128;
+constexpr int MM_THREADS = 512;
+constexpr int MM_ROWS = 128;                        // rows of X that a block stages (a pair: 256)
+constexpr int MM_HALF = MM_ROWS * 64 * 2;           // 64 columns of them, 16 KB
+constexpr int MM_B_BYTES = 2 * MM_HALF;
+constexpr int MM_A_BYTES = MM_LANES * MM_BK * 2;    // 32 KB (input gradient)
+constexpr int MM_BOX = 128 * 64 * 2;                // A: 128 contraction rows x 64 columns
+constexpr int MM_TABLE = (MATMUL_MAX_EXPERTS + 4) * 4;
+constexpr uint32_t MM_TMEM = 512;
+constexpr int MM_MAX_STAGES = 4;                    // of 64 TMEM columns beside the accumulators
+
+// The ring of packed words: a stage is 128 rows x 128 codes (16 B bytes a row), as a tiled copy
+// with the swizzle of that width lays it out (48-byte rows of 3 bits have none).
+template <int B, int DIR>
+struct MmRing {
+    static constexpr int ROW = 16 * B;
+    static constexpr int STAGE = 128 * ROW;
+    // the input gradient's operand stages leave less room
+    static constexpr int STAGES = DIR == 1 ? (B == 2 ? 3 : 2) : B == 8 ? 3 : B == 4 ? 6 : B == 3 ? 7 : 8;
+    static constexpr int WORDS = STAGES * STAGE;
+    // two scales a thread and step, SCALES - 1 steps ahead
+    static constexpr int SCALES = DIR == 1 ? 2 : 4;
+    static constexpr int BYTES = WORDS + SCALES * 256 * 8;
+    // byte offset of 16-byte (3 bits: 8-byte) piece q of row r
+    static __device__ __forceinline__ int at(int r, int q) {
+        return B == 2   ? r * 32 + ((q ^ ((r >> 2) & 1)) << 4)
+               : B == 3 ? r * 48 + q * 8
+               : B == 4 ? r * 64 + ((q ^ ((r >> 1) & 3)) << 4)
+                        : r * 128 + ((q ^ (r & 7)) << 4);
+    }
+};
+
+struct MmTcArg {
+    MatmulArg m;
+    int out, inner;       // output channels and contraction length of this direction
+    int cols;             // most rows of a tile (multiple of 16)
+    int box_rows;         // rows of one tiled copy of X; 0: plain loads
+    int stages;           // of the operand ring
+    int accs, acc_cols;   // accumulators and their distance
+    int split;            // blocks of a cluster that share a tile's contraction
+    int fold;             // scales folded into the weights
+    int wtiled, yvec;     // packed rows by tiled copies; output rows start on 16-byte boundaries
+    int epi;              // bytes of the output staging (or of the partial sums)
+    int E;                // row ranges
+};
+
+gptq_status matmul_tc_bf16(const CUtensorMap &map, const CUtensorMap &wmap, const MmTcArg &p, int dir, int bits, bool pair, int blocks,
+                           size_t smem, cudaStream_t st);
+gptq_status matmul_tc_fp16(const CUtensorMap &map, const CUtensorMap &wmap, const MmTcArg &p, int dir, int bits, bool pair, int blocks,
+                           size_t smem, cudaStream_t st);
+
+// Rows [r0, r0 + rows) x columns [c0, c0 + 64) of X into the swizzled layout of a tiled copy,
+// zeros past row_end or col_end: the copy for layouts that tiled copies refuse.
+template <typename T>
+__device__ __forceinline__ void plain_box(uint8_t *dst, const T *x, int64_t ld, int64_t r0, int rows,
+                                          int64_t row_end, int c0, int col_end, int tid, int nthr) {
+    for (int i = tid; i < rows * 8; i += nthr) {
+        const int r = i >> 3, q = i & 7;
+        uint32_t v[4] = {0u, 0u, 0u, 0u};
+        if (r0 + r < row_end) {
+            const unsigned short *src =
+                reinterpret_cast<const unsigned short *>(x) + (r0 + r) * ld + c0 + 8 * q;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c0 + 8 * q + e < col_end) v[e >> 1] |= (uint32_t)__ldg(src + e) << (16 * (e & 1));
+        }
+        *reinterpret_cast<uint4 *>(dst + r * 128 + ((q ^ (r & 7)) << 4)) =
+            make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// 16 bytes (8 elements) of a row at p, `left` of them inside; whole pieces only when aligned.
+template <typename T>
+__device__ __forceinline__ uint4 load8(const T *p, int left, bool vec) {
+    if (left >= 8 && vec) return __ldg(reinterpret_cast<const uint4 *>(p));
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    const unsigned short *src = reinterpret_cast<const unsigned short *>(p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < left) v[e >> 1] |= (uint32_t)__ldg(src + e) << (16 * (e & 1));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// N bytes (4, 8 or 16) to shared memory, zeros when src is NULL.
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, const void *any) {
+    const int bytes = src ? N : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src ? src : any), "n"(N),
+                 "r"(bytes)
+                 : "memory");
+}
+
+struct MmTile {
+    int e, c0;            // range, first output channel of this block
+    int64_t t0;           // first row
+    int n, n16;           // rows, rounded up to the columns an MMA takes (16, a pair 32)
+};
+
+// Tile u -> (range, channels, rows), rows fastest.
+__device__ __forceinline__ MmTile mm_tile(const MmTcArg &p, const int *table, int tiles_out, int u,
+                                          int width, int first, int grain) {
+    MmTile t;
+    int lo = 0, hi = p.E - 1;                       // last range whose first tile is <= u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (table[mid] * tiles_out <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    t.e = lo;
+    int64_t begin = 0, end = p.m.M;
+    if (p.m.offsets) {
+        const bool one = p.m.lora.R > 0;            // with adapters the requests are one range
+        begin = __ldg(p.m.offsets + (one ? 0 : lo));
+        end = __ldg(p.m.offsets + (one ? p.m.lora.R : lo + 1));
+    }
+    const int cnt = (int)(end - begin);
+    const int nt = (cnt + p.cols - 1) / p.cols;
+    const int size = ((cnt + nt - 1) / nt + grain - 1) & -grain;
+    const int q = u - table[lo] * tiles_out, c = q / nt, j = q - c * nt;
+    t.c0 = c * width + first;
+    t.t0 = begin + (int64_t)j * size;
+    t.n = min(size, cnt - j * size);
+    t.n16 = (t.n + grain - 1) & -grain;
+    return t;
+}
+
+// A place in the ring of operand stages.
+struct RingPos {
+    int stage;
+    uint32_t phase;
+    __device__ __forceinline__ void advance(int stages) {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <typename T, int B, int DIR, bool IDX, bool PAIR>
+__global__ void __launch_bounds__(MM_THREADS, 1)
+    k_matmul_tc(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                const __grid_constant__ MmTcArg p) {
+    using Ring = MmRing<B, DIR>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    constexpr int stage_bytes = MM_B_BYTES + (DIR == 1 ? MM_A_BYTES : 0);
+    uint8_t *words = smem + p.stages * stage_bytes;             // the words' ring
+    uint8_t *epi = words + Ring::BYTES;
+    int *table = reinterpret_cast<int *>(epi + p.epi);
+    uint64_t *full = reinterpret_cast<uint64_t *>(epi + p.epi + MM_TABLE);
+    uint64_t *empty = full + MM_MAX_STAGES;
+    uint64_t *tfull = empty + MM_MAX_STAGES;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *ready = tempty + 2;                               // partial sums in place / read
+    uint64_t *done = ready + 1;
+    uint64_t *wfull = done + 1;
+    uint64_t *wempty = wfull + Ring::STAGES;
+    uint64_t *drain = wempty + Ring::STAGES;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *refuse = reinterpret_cast<int *>(tmem_slot + 2);
+
+    const MatmulArg &m = p.m;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int stages = p.stages;
+    const int split = PAIR ? 1 : p.split;
+    const int cluster = PAIR ? 2 : split;
+    const uint32_t rank = cluster > 1 ? tc::cluster_ctarank() : 0u;
+    const int group = blockIdx.x / cluster, ngroups = gridDim.x / cluster;
+    const bool tiled = p.box_rows > 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            tc::mbar_init(&full[s], (PAIR ? 16 : 8) + (tiled ? 1 : 0));
+            tc::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(&tfull[b], 1);
+            tc::mbar_init(&tempty[b], PAIR ? 8 : 4);
+        }
+        tc::mbar_init(ready, 4 * split);
+        tc::mbar_init(done, 4 * split);
+        for (int s = 0; s < Ring::STAGES; ++s) {
+            tc::mbar_init(&wfull[s], p.wtiled ? 1 : 64);
+            tc::mbar_init(&wempty[s], 8);
+        }
+        tc::mbar_init(drain, 1);
+        *abort = 0;
+        *refuse = 0;
+        tc::fence_mbar_init();
+        if (tiled) tc::prefetch_tmap(&xmap);
+        if (p.wtiled) tc::prefetch_tmap(&wmap);
+    }
+    if (warp == 13) {
+        if constexpr (PAIR) tc::tmem_alloc_pair(tmem_slot, MM_TMEM);
+        else tc::tmem_alloc(tmem_slot, MM_TMEM);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency();
+
+    // the ranges: refused as a whole when they are not ordered inside [0, M]
+    bool bad = false;
+    const int nranges = m.lora.R > 0 ? m.lora.R : p.E;
+    if (m.offsets) bad = offsets_bad(m.offsets, nranges, m.M, threadIdx.x, MM_THREADS);
+    if (m.lora.R > 0) bad |= ids_bad(m.lora.ids, m.lora.R, m.lora.L, threadIdx.x, MM_THREADS);
+    if (bad) *refuse = 1;
+    __syncthreads();
+    if (threadIdx.x == 0 && *refuse == 0 && failed(m.status)) *refuse = 2;
+    __syncthreads();
+    if (warp == 0) {
+        // table[e]: tiles of rows before range e
+        int base = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            int nt = 0;
+            if (e < p.E && *refuse != 1) {
+                int64_t cnt = m.M;
+                if (m.lora.R > 0) cnt = __ldg(m.offsets + m.lora.R) - __ldg(m.offsets);
+                else if (m.offsets) cnt = __ldg(m.offsets + e + 1) - __ldg(m.offsets + e);
+                nt = (int)((cnt + p.cols - 1) / p.cols);
+            }
+            int sum = nt;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(~0u, sum, d);
+                if (lane >= d) sum += v;
+            }
+            if (e < p.E) table[e] = base + sum - nt;
+            base += __shfl_sync(~0u, sum, 31);
+        }
+        if (lane == 0) table[p.E] = base;
+    }
+    __syncthreads();
+    if (cluster > 1) tc::cluster_sync();    // every block's barriers and refusal are in place
+    int skip = *refuse;
+    if (cluster > 1)                        // the blocks of a cluster go by the first one's reading
+        skip = (int)tc::ld_shared_cluster(tc::mapa_shared(tc::smem_u32(refuse), 0));
+    if (skip == 1 && threadIdx.x == 0) set_status(m.status, GPTQ_ERR_ARG);
+
+    constexpr int WIDTH = PAIR ? 2 * MM_LANES : MM_LANES;
+    constexpr int GRAIN = PAIR ? 32 : 16;           // column counts that an MMA takes
+    const int first = PAIR ? (int)rank * MM_LANES : 0;
+    const int tiles_out = (p.out + WIDTH - 1) / WIDTH;
+    const int tiles = skip ? 0 : table[p.E] * tiles_out;
+    const int steps = (p.inner + MM_BK - 1) / MM_BK;
+    const int part = PAIR ? 0 : (int)rank;
+    const int k0 = (int)((int64_t)steps * part / split), k1 = (int)((int64_t)steps * (part + 1) / split);
+    const int nmain = k1 - k0;
+    const bool adapters = m.lora.R > 0 && part == split - 1;
+    const int two_r = 2 * m.lora.rank;
+    const int rsteps = (two_r + MM_BK - 1) / MM_BK;
+    const T *X = static_cast<const T *>(m.X);
+    // the barrier of a stage that the MMA thread waits on (the first block's, in a pair)
+    auto arrive_full = [&](int stage) {
+        if (PAIR && rank != 0) tc::mbar_arrive_remote(tc::mapa_shared(tc::smem_u32(&full[stage]), 0));
+        else tc::mbar_arrive(&full[stage]);
+    };
+
+    if (warp < 8) {
+        const int set = warp >> 2, wq = warp & 3, tid = threadIdx.x;
+        // forward: channel = lane of the warp's TMEM quarter, half `set` of the step's columns.
+        // Input gradient: row n of the step and half of the block's 128 columns.
+        const int arow = (wq & 1) * 32 + lane + set * 64, ahalf = wq >> 1;
+        const uint32_t scale0 = tc::smem_u32(words) + Ring::WORDS + tid * 8;
+        // the row and first 16-byte (8-byte) piece of a words' stage that this thread unpacks
+        const int wrow = DIR == 0 ? wq * 32 + lane : arow;
+        const int wpiece = (DIR == 0 ? set : ahalf) * (B == 3 ? 3 : B / 2);
+
+        // Scales where they fold into the weights: this thread's next step to request, ahead of the
+        // unpacking and across tiles.
+        const bool scaled = !IDX && p.fold;
+        int fu = group, fi = 0, fslot = 0;
+        int64_t ferow = 0;
+        int fc0 = 0;
+        auto fetch_tile = [&]() {
+            if (fu >= tiles) return;
+            const MmTile t = mm_tile(p, table, tiles_out, fu, WIDTH, first, GRAIN);
+            ferow = (int64_t)t.e * m.w.N;
+            fc0 = t.c0;
+        };
+        auto fetch = [&]() {
+            if (fu < tiles) {
+                const int n = DIR == 0 ? fc0 + wq * 32 + lane : (k0 + fi) * MM_BK + arow;
+                const int k = DIR == 0 ? (k0 + fi) * MM_BK + set * 64 : fc0 + ahalf * 64;
+                const float *row = m.w.scales + (ferow + n) * (m.w.groups ? m.w.groups : 1);
+                const int g0 = m.w.groups ? k >> m.w.gshift : 0;
+                const int g1 = m.w.groups ? (k + 32) >> m.w.gshift : 0;
+                const uint32_t dst = scale0 + fslot * 256 * 8;
+                copy_async<4>(dst, n < m.w.N && k < m.w.K ? row + g0 : nullptr, m.w.scales);
+                if (m.w.gshift == 5) copy_async<4>(dst + 4, n < m.w.N && k + 32 < m.w.K ? row + g1 : nullptr, m.w.scales);
+                if (++fi == nmain) {
+                    fi = 0;
+                    fu += ngroups;
+                    fetch_tile();
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (++fslot == Ring::SCALES) fslot = 0;
+        };
+        if (scaled) {
+            fetch_tile();
+#pragma unroll 1
+            for (int d = 0; d < Ring::SCALES - 1; ++d) fetch();
+        }
+        int wstage = 0, slot = 0;
+        uint32_t wphase = 0;
+        RingPos pos{0, 0};
+        for (int u = group; u < tiles; u += ngroups) {
+            const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
+            const int64_t erow = (int64_t)t.e * m.w.N;
+            const int ch = t.c0 + wq * 32 + lane;       // forward: this thread's channel
+#pragma unroll 1
+            for (int i = 0; i < nmain; ++i) {
+                const int step = k0 + i;
+                if (scaled) {
+                    fetch();
+                    asm volatile("cp.async.wait_group %0;" ::"n"(Ring::SCALES - 1) : "memory");
+                }
+                uint32_t raw[2][B];
+                bool ok = tc::mbar_wait(&wfull[wstage], wphase, abort);
+                {
+                    const uint8_t *src = words + wstage * Ring::STAGE;
+                    if constexpr (B == 3) {
+#pragma unroll
+                        for (int q = 0; q < 3; ++q) {
+                            const uint2 y = *reinterpret_cast<const uint2 *>(src + Ring::at(wrow, wpiece + q));
+                            raw[(2 * q) / 3][(2 * q) % 3] = y.x;
+                            raw[(2 * q + 1) / 3][(2 * q + 1) % 3] = y.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < B / 2; ++q) {
+                            const uint4 y = *reinterpret_cast<const uint4 *>(src + Ring::at(wrow, wpiece + q));
+                            const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) raw[(4 * q + j) / B][(4 * q + j) % B] = z[j];
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&wempty[wstage]);
+                if (++wstage == Ring::STAGES) { wstage = 0; wphase ^= 1; }
+                float sc[2] = {1.f, 1.f};
+                if (scaled) {
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                                 : "=f"(sc[0]), "=f"(sc[1])
+                                 : "r"(scale0 + slot * 256 * 8));
+                    if (m.w.gshift != 5) sc[1] = sc[0];
+                    if (++slot == Ring::SCALES) slot = 0;
+                }
+                uint32_t v[2][16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    unpack32<B, T>(raw[h], v[h]);
+                    if constexpr (IDX) {
+                        const int n = DIR == 0 ? ch : step * MM_BK + arow;
+                        const int c = DIR == 0 ? step * MM_BK + set * 64 + 32 * h : t.c0 + ahalf * 64 + 32 * h;
+                        if (n < m.w.N && c < m.w.K)
+                            scale32_by_index<T, B, true>(v[h], m.w.scales + (erow + n) * m.w.groups,
+                                                         m.w.g_idx + (int64_t)t.e * m.w.K, c, m.w.K, m.w.groups,
+                                                         m.status);
+                    } else {
+                        if (p.fold) scale32<T>(v[h], sc[h]);
+                    }
+                }
+                ok = tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort) && ok;
+                ok = __all_sync(~0u, ok);
+                if (ok) {
+                    uint8_t *st = smem + pos.stage * stage_bytes;
+                    if constexpr (DIR == 0) {
+                        // the stage's last reader was an MMA that has completed
+                        tc::fence_after_sync();
+                        uint32_t r[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = v[j >> 4][j & 15];
+                        tc::tmem_st_32x32b_x32(tmem + 256 + pos.stage * 64 + set * 32 + ((uint32_t)(wq * 32) << 16), r);
+                        tc::tmem_st_wait();
+                    } else {
+                        uint8_t *a = st + MM_B_BYTES + ahalf * MM_BOX + arow * 128;
+                        const bool in = step * MM_BK + arow < m.w.N;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const uint32_t(&y)[16] = v[q >> 2];
+                            const int j = 4 * (q & 3);
+                            *reinterpret_cast<uint4 *>(a + ((q ^ (arow & 7)) << 4)) =
+                                in ? make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]) : make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    if (!tiled) {
+                        const int rows = PAIR ? t.n16 / 2 : t.n16;
+                        plain_box<T>(st + set * MM_HALF, X, m.ldx, t.t0 + (PAIR ? (int)rank * rows : 0), rows, t.t0 + t.n,
+                                     step * MM_BK + set * 64, p.inner, tid & 127, 128);
+                    }
+                    if (DIR == 1 || !tiled) tc::fence_async_shared();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) arrive_full(pos.stage);
+                }
+                pos.advance(stages);
+            }
+            if (adapters) {
+                const T *P = static_cast<const T *>(m.lora.P);
+                const T *T2 = static_cast<const T *>(m.lora.T2);
+                const int r = m.lora.rank;
+                RunWalk run(m.offsets, m.lora.ids, m.lora.R, (int)t.t0, (int)t.t0 + t.n);
+                while (run.next()) {
+                    const int b0 = (run.begin - (int)t.t0) & -GRAIN, b1 = ((run.end - (int)t.t0) + GRAIN - 1) & -GRAIN;
+                    const int rows = PAIR ? (b1 - b0) / 2 : b1 - b0;
+                    const int row0 = b0 + (PAIR ? (int)rank * rows : 0);
+                    for (int rs = 0; rs < rsteps; ++rs) {
+                        bool ok = tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort);
+                        ok = __all_sync(~0u, ok);
+                        if (ok) {
+                            uint8_t *st = smem + pos.stage * stage_bytes;
+                            if constexpr (DIR == 0) {
+                                // A: row n of B_a twice over, [hi part | lo part] of the contraction
+                                if (rs * MM_BK + set * 64 < two_r) {
+                                    uint32_t y[32];
+                                    const T *src = P + ((int64_t)run.id * m.w.N + ch) * r;
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) {
+                                        const int q = rs * MM_BK + set * 64 + j * 8;
+                                        const uint4 x = ch < m.w.N && q < two_r ? load8<T>(src + (q < r ? q : q - r), 8, true)
+                                                                                : make_uint4(0u, 0u, 0u, 0u);
+                                        y[4 * j] = x.x; y[4 * j + 1] = x.y; y[4 * j + 2] = x.z; y[4 * j + 3] = x.w;
+                                    }
+                                    tc::fence_after_sync();
+                                    tc::tmem_st_32x32b_x32(tmem + 256 + pos.stage * 64 + set * 32 +
+                                                               ((uint32_t)(wq * 32) << 16), y);
+                                    tc::tmem_st_wait();
+                                }
+                            } else {
+                                const int q = rs * MM_BK + arow;
+                                const int c = t.c0 + ahalf * 64;
+                                const T *src = P + ((int64_t)run.id * r + (q < r ? q : q - r)) * m.w.K + c;
+                                uint8_t *a = st + MM_B_BYTES + ahalf * MM_BOX + arow * 128;
+                                const bool v8 = (m.w.K & 7) == 0;
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    *reinterpret_cast<uint4 *>(a + ((j ^ (arow & 7)) << 4)) =
+                                        load8<T>(src + 8 * j, q < two_r ? m.w.K - c - 8 * j : 0, v8);
+                            }
+                            // the run's rows of [hi | lo], zeros for rows of others
+                            for (int j = tid; j < rows * 16; j += 256) {
+                                const int row = j >> 4, q = j & 15, col = rs * MM_BK + 8 * q;
+                                const int64_t tr = t.t0 + row0 + row;
+                                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                                if (tr >= run.begin && tr < run.end && col < two_r)
+                                    x = __ldg(reinterpret_cast<const uint4 *>(T2 + tr * two_r + col));
+                                *reinterpret_cast<uint4 *>(st + (q >> 3) * MM_HALF + row * 128 + (((q & 7) ^ (row & 7)) << 4)) = x;
+                            }
+                            tc::fence_async_shared();
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) arrive_full(pos.stage);
+                        }
+                        pos.advance(stages);
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp < 12) {
+        // outputs: lane = channel, register = row
+        const int wq = warp & 3, etid = threadIdx.x - 256;
+        int acc = 0;
+        uint32_t acc_phase = 0, sum_phase = 0;
+        T *Y = static_cast<T *>(m.Y);
+        for (int u = group; u < tiles; u += ngroups) {
+            const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
+            const int ch = t.c0 + wq * 32 + lane;
+            const bool per_channel = DIR == 0 && !p.fold;
+            const float s = per_channel && ch < p.out ? __ldg(m.w.scales + (int64_t)t.e * m.w.N + ch) : 1.f;
+            bool ok = tc::mbar_wait(&tfull[acc], acc_phase, abort);
+            ok = __all_sync(~0u, ok);
+            tc::fence_after_sync();
+            const uint32_t at = tmem + acc * p.acc_cols + ((uint32_t)(wq * 32) << 16);
+            auto release = [&]() {
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR && rank != 0) tc::mbar_arrive_remote(tc::mapa_shared(tc::smem_u32(&tempty[acc]), 0));
+                    else tc::mbar_arrive(&tempty[acc]);
+                }
+            };
+            if (split == 1) {
+                // through shared memory as [row][channel], `chunk` rows at a time
+                const int chunk = p.epi / 256;
+                T *stg = reinterpret_cast<T *>(epi);
+                for (int r0 = 0; r0 < t.n; r0 += chunk) {
+                    const int rows = min(chunk, t.n - r0);
+                    if (ok) {
+                        // `chunk` is a multiple of 32; the columns past the tile's rows are not written out
+                        uint16_t *d = reinterpret_cast<uint16_t *>(epi) + wq * 32 + lane;
+#pragma unroll 1
+                        for (int r = 0; r < rows; r += 32, d += 32 * MM_LANES) {
+                            uint32_t y[32];
+                            tc::tmem_ld_32x32b_x32(at + r0 + r, y);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                const uint32_t h = Half2<T>::pack(s * __uint_as_float(y[j]), s * __uint_as_float(y[j + 1]));
+                                d[j * MM_LANES] = (uint16_t)h;
+                                d[(j + 1) * MM_LANES] = (uint16_t)(h >> 16);
+                            }
+                        }
+                    }
+                    if (r0 + chunk >= t.n) release();
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (ok) {
+                        const int q = etid & 15, c = t.c0 + 8 * q;
+                        for (int r = etid >> 4; r < rows; r += 8) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(stg + r * MM_LANES + 8 * q);
+                            T *d = Y + (t.t0 + r0 + r) * m.ldy + c;
+                            if (p.yvec && c + 8 <= p.out) {
+                                *reinterpret_cast<uint4 *>(d) = x;
+                            } else {
+                                const uint32_t h[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    if (c + j < p.out)
+                                        reinterpret_cast<uint16_t *>(d)[j] = (uint16_t)(h[j >> 1] >> (16 * (j & 1)));
+                            }
+                        }
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                }
+            } else {
+                // partial sums of the cluster's blocks as [row][channel], summed in rank order by
+                // the block that writes the row
+                float *dump = reinterpret_cast<float *>(epi);
+                // the sums of the tile before have been read (first tile: passes at once)
+                ok = tc::mbar_wait_cluster(done, sum_phase ^ 1, abort) && ok;
+                ok = __all_sync(~0u, ok);
+                if (ok) {
+                    for (int r = 0; r < t.n16; r += 16) {
+                        uint32_t y[16];
+                        tc::tmem_ld_32x32b_x16(at + r, y);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            dump[(r + j) * MM_LANES + wq * 32 + lane] = __uint_as_float(y[j]);
+                    }
+                }
+                release();
+                if (lane < split)
+                    tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(ready), lane));
+                bool all = tc::mbar_wait_cluster(ready, sum_phase, abort);
+                all = __all_sync(~0u, all) && ok;
+                if (all) {
+                    for (int row = (int)rank; row < t.n; row += split) {
+                        float sum = 0.f;
+                        const uint32_t from = tc::smem_u32(dump + row * MM_LANES + wq * 32 + lane);
+                        for (int c = 0; c < split; ++c)
+                            sum += __uint_as_float(tc::ld_shared_cluster(tc::mapa_shared(from, c)));
+                        if (ch < p.out) Y[(t.t0 + row) * m.ldy + ch] = from_f32<T>(s * sum);
+                    }
+                }
+                __syncwarp();
+                if (lane < split)
+                    tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(done), lane));
+                sum_phase ^= 1;
+            }
+            if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
+        }
+    } else if (warp == 12) {
+        // the whole warp walks, one elected lane issues (as for the MMAs below)
+        if (tiled) {
+            RingPos pos{0, 0};
+            bool ok = true;
+            for (int u = group; u < tiles && ok; u += ngroups) {
+                const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
+                const int rows = PAIR ? t.n16 / 2 : t.n16;
+                const int row0 = (int)t.t0 + (PAIR ? (int)rank * rows : 0);
+                const int boxes = (rows + p.box_rows - 1) / p.box_rows;
+                const uint32_t bytes = boxes * p.box_rows * 256;
+#pragma unroll 1
+                for (int i = 0; i < nmain; ++i) {
+                    ok = __all_sync(~0u, tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort));
+                    if (!ok) break;
+                    uint8_t *st = smem + pos.stage * stage_bytes;
+                    const int x = (k0 + i) * MM_BK;
+                    if (tc::elect_one()) {
+                        if (!PAIR || rank == 0) tc::mbar_arrive_expect_tx(&full[pos.stage], PAIR ? 2 * bytes : bytes);
+                        for (int b = 0; b < boxes; ++b) {
+                            uint8_t *d = st + b * p.box_rows * 128;
+                            const int y = row0 + b * p.box_rows;
+                            if constexpr (PAIR) {
+                                const uint32_t fb = tc::mapa_shared(tc::smem_u32(&full[pos.stage]), 0);
+                                tc::tma_load_2d_pair(d, &xmap, fb, x, y);
+                                tc::tma_load_2d_pair(d + MM_HALF, &xmap, fb, x + 64, y);
+                            } else {
+                                tc::tma_load_2d(d, &xmap, &full[pos.stage], x, y);
+                                tc::tma_load_2d(d + MM_HALF, &xmap, &full[pos.stage], x + 64, y);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    pos.advance(stages);
+                }
+                if (ok && adapters) {
+                    RunWalk run(m.offsets, m.lora.ids, m.lora.R, (int)t.t0, (int)t.t0 + t.n);
+                    while (ok && run.next()) {
+                        for (int rs = 0; rs < rsteps; ++rs) {
+                            ok = __all_sync(~0u, tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort));
+                            if (!ok) break;
+                            if (lane == 0 && (!PAIR || rank == 0)) tc::mbar_arrive(&full[pos.stage]);
+                            pos.advance(stages);
+                        }
+                    }
+                }
+            }
+            if (!ok) {
+                // loads still in flight land before the block can exit
+                const long long from = clock64();
+                while (clock64() - from < 20000000ll) {
+                }
+            }
+        }
+    } else if (warp >= 14) {
+        // a stage: the block's channels x a step's columns (forward), or a step's rows x the block's
+        // columns
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        if (p.wtiled) {
+            if (warp == 14) {
+                for (int u = group; u < tiles && ok; u += ngroups) {
+                    const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
+                    const int erow = t.e * m.w.N;
+#pragma unroll 1
+                    for (int i = 0; i < nmain; ++i) {
+                        ok = __all_sync(~0u, tc::mbar_wait(&wempty[stage], phase ^ 1, abort));
+                        if (!ok) break;
+                        const int k = DIR == 0 ? (k0 + i) * MM_BK : t.c0;
+                        const int n = DIR == 0 ? t.c0 : (k0 + i) * MM_BK;
+                        if (tc::elect_one()) {
+                            tc::mbar_arrive_expect_tx(&wfull[stage], Ring::STAGE);
+                            tc::tma_load_2d(words + stage * Ring::STAGE, &wmap, &wfull[stage], (k >> 5) * B, erow + n);
+                        }
+                        __syncwarp();
+                        if (++stage == Ring::STAGES) { stage = 0; phase ^= 1; }
+                    }
+                }
+                if (!ok) {
+                    const long long from = clock64();
+                    while (clock64() - from < 20000000ll) {
+                    }
+                }
+            }
+        } else {
+            const int tid = threadIdx.x - 448;
+            const int nw = (int)(((int64_t)m.w.K * B + 31) / 32);
+            for (int u = group; u < tiles && ok; u += ngroups) {
+                const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
+                const int64_t erow = (int64_t)t.e * m.w.N;
+                for (int i = 0; i < nmain; ++i) {
+                    ok = tc::mbar_wait(&wempty[stage], phase ^ 1, abort);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    const int w0 = ((DIR == 0 ? (k0 + i) * MM_BK : t.c0) >> 5) * B;
+                    const int n0 = DIR == 0 ? t.c0 : (k0 + i) * MM_BK;
+                    const uint32_t dst = tc::smem_u32(words + stage * Ring::STAGE);
+                    constexpr int RW = 4 * B, PW = B == 3 ? 2 : 4;      // words of a row, of a piece
+#pragma unroll 4
+                    for (int j = tid; j < 128 * RW; j += 64) {
+                        const int r = j / RW, w = j - r * RW;
+                        const bool in = n0 + r < m.w.N && w0 + w < nw;
+                        copy_async<4>(dst + Ring::at(r, w / PW) + (w % PW) * 4,
+                                      in ? m.w.words + (erow + n0 + r) * m.w.ldw + w0 + w : nullptr, m.w.words);
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&wfull[stage]))
+                                 : "memory");
+                    if (++stage == Ring::STAGES) { stage = 0; phase ^= 1; }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+    } else {
+        // the whole warp walks the steps, so that what an MMA takes stays in uniform registers (with
+        // one lane walking, issuing an MMA took longer than the MMA); one elected lane issues
+        if (!PAIR || rank == 0) {
+            RingPos pos{0, 0};
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            constexpr int MROWS = PAIR ? 2 * MM_LANES : MM_LANES;
+            const uint32_t ring = tc::smem_u32(smem);
+            const uint64_t bdesc0 = tc::desc_sw128(ring, 16, 1024);
+            const uint64_t adesc0 = tc::desc_sw128(ring + MM_B_BYTES, MM_BOX, 1024);
+            // the MMAs of one step: kks of 16, into columns from d on, and the stage's release
+            auto issue = [&](uint32_t d, int stage, int kks, uint32_t id, uint32_t add) {
+                const uint64_t bd = bdesc0 + (uint32_t)(stage * stage_bytes >> 4);
+                const uint64_t ad = adesc0 + (uint32_t)(stage * stage_bytes >> 4);
+                const uint32_t at = tmem + 256 + stage * 64;
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < MM_BK / 16; ++kk) {
+                        if (kk >= kks) break;
+                        const uint64_t bk = bd + ((kk >> 2) * MM_HALF + (kk & 3) * 32 >> 4);
+                        const uint32_t on = kk > 0 ? 1u : add;
+                        if constexpr (DIR == 0) {
+                            if constexpr (PAIR) tc::mma_f16_ts_pair(d, at + kk * 8, bk, id, on);
+                            else tc::mma_f16_ts(d, at + kk * 8, bk, id, on);
+                        } else {
+                            if constexpr (PAIR) tc::mma_bf16_pair(d, ad + kk * 128, bk, id, on);
+                            else tc::mma_bf16(d, ad + kk * 128, bk, id, on);
+                        }
+                    }
+                    if constexpr (PAIR) tc::mma_commit_both(&empty[stage]);
+                    else tc::mma_commit(&empty[stage]);
+                }
+                __syncwarp();
+            };
+            for (int u = group; u < tiles && ok; u += ngroups) {
+                const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
+                const uint32_t id = tc::idesc_f16_f32(Half2<T>::kType, MROWS, t.n16, DIR, 0);
+                ok = __all_sync(~0u, tc::mbar_wait(&tempty[acc], acc_phase ^ 1, abort));
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t d = tmem + acc * p.acc_cols;
+                for (int i = 0; i < nmain; ++i) {
+                    ok = __all_sync(~0u, tc::mbar_wait(&full[pos.stage], pos.phase, abort));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    issue(d, pos.stage, MM_BK / 16, id, i > 0 ? 1u : 0u);
+                    pos.advance(stages);
+                }
+                if (ok && adapters) {
+                    RunWalk run(m.offsets, m.lora.ids, m.lora.R, (int)t.t0, (int)t.t0 + t.n);
+                    while (ok && run.next()) {
+                        const int b0 = (run.begin - (int)t.t0) & -GRAIN, b1 = ((run.end - (int)t.t0) + GRAIN - 1) & -GRAIN;
+                        const uint32_t rid = tc::idesc_f16_f32(Half2<T>::kType, MROWS, b1 - b0, DIR, 0);
+                        for (int rs = 0; rs < rsteps; ++rs) {
+                            ok = __all_sync(~0u, tc::mbar_wait(&full[pos.stage], pos.phase, abort));
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            issue(d + b0, pos.stage, (min(MM_BK, two_r - rs * MM_BK) + 15) / 16, rid, 1u);
+                            pos.advance(stages);
+                        }
+                    }
+                }
+                if (ok && tc::elect_one()) {
+                    if constexpr (PAIR) tc::mma_commit_both(&tfull[acc]);
+                    else tc::mma_commit(&tfull[acc]);
+                }
+                __syncwarp();
+                if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
+            }
+            // every MMA issued completes before TMEM is released
+            if (tc::elect_one()) {
+                if constexpr (PAIR) tc::mma_commit_pair(tc::mapa_shared(tc::smem_u32(drain), 0));
+                else tc::mma_commit(drain);
+                volatile int never = 0;
+                tc::mbar_wait(drain, 0, &never);
+            }
+        }
+    }
+
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (cluster > 1) tc::cluster_sync();    // no block leaves while others use its memory
+    if (*abort && threadIdx.x == 0) set_status(m.status, GPTQ_ERR_TIMEOUT);
+    if (warp == 13) {
+        tc::fence_after_sync();
+        if constexpr (PAIR) tc::tmem_dealloc_pair(tmem, MM_TMEM);
+        else tc::tmem_dealloc(tmem, MM_TMEM);
+    }
+}
+
+template <typename T, int B, int DIR>
+static gptq_status launch_tc(const CUtensorMap &map, const CUtensorMap &wmap, const MmTcArg &p, bool pair, int blocks, size_t smem,
+                             cudaStream_t st) {
+    const int cluster = pair ? 2 : p.split;
+    if (p.m.w.g_idx)
+        return pair ? launch_pdl(k_matmul_tc<T, B, DIR, true, true>, dim3(blocks), MM_THREADS, smem, cluster, st, map, wmap, p)
+                    : launch_pdl(k_matmul_tc<T, B, DIR, true, false>, dim3(blocks), MM_THREADS, smem, cluster, st, map, wmap, p);
+    return pair ? launch_pdl(k_matmul_tc<T, B, DIR, false, true>, dim3(blocks), MM_THREADS, smem, cluster, st, map, wmap, p)
+                : launch_pdl(k_matmul_tc<T, B, DIR, false, false>, dim3(blocks), MM_THREADS, smem, cluster, st, map, wmap, p);
+}
+
+template <typename T, int DIR>
+static gptq_status launch_tc_bits(const CUtensorMap &map, const CUtensorMap &wmap, const MmTcArg &p, int bits, bool pair, int blocks,
+                                  size_t smem, cudaStream_t st) {
+    switch (bits) {
+        case 2: return launch_tc<T, 2, DIR>(map, wmap, p, pair, blocks, smem, st);
+        case 3: return launch_tc<T, 3, DIR>(map, wmap, p, pair, blocks, smem, st);
+        case 4: return launch_tc<T, 4, DIR>(map, wmap, p, pair, blocks, smem, st);
+        default: return launch_tc<T, 8, DIR>(map, wmap, p, pair, blocks, smem, st);
+    }
+}
+
+}  // namespace gptq

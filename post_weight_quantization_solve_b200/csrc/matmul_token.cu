@@ -19,7 +19,6 @@ namespace gptq {
 
 namespace {
 constexpr int TK_WARPS = 8;
-constexpr int TK_CH = 32;                  // channels of a block (two 16-row fragments)
 }  // namespace
 
 struct TokenArg {
@@ -61,11 +60,39 @@ __device__ __forceinline__ void load_unit(const uint32_t *row, int chunk, int nw
     }
 }
 
-template <typename T, int B, int NT>
-__global__ void __launch_bounds__(TK_WARPS * 32)
+// Eight neighbouring values of a row in the pair order of unpack32<B, T, false>.
+template <int B>
+__device__ __forceinline__ void to_pair_order(uint32_t (&x)[16]) {
+    if constexpr (B == 3 || B == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a = x[4 * i], b = x[4 * i + 1], c = x[4 * i + 2], d = x[4 * i + 3];
+            x[4 * i] = __byte_perm(a, c, 0x5410);
+            x[4 * i + 1] = __byte_perm(a, c, 0x7632);
+            x[4 * i + 2] = __byte_perm(b, d, 0x5410);
+            x[4 * i + 3] = __byte_perm(b, d, 0x7632);
+        }
+    } else if constexpr (B == 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = x[8 * i + j];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[8 * i + 2 * j] = __byte_perm(y[j], y[j + 4], 0x5410);
+                x[8 * i + 2 * j + 1] = __byte_perm(y[j], y[j + 4], 0x7632);
+            }
+        }
+    }
+}
+
+// MT fragments of 16 channels, NT of 8 rows.
+template <typename T, int B, int NT, int MT>
+__global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
     k_matmul_token(const __grid_constant__ TokenArg p) {
     constexpr int U = B == 3 ? 4 : B == 2 ? 2 : 1;      // chunks that fill 16-byte pieces
-    constexpr int ROWS = 8 * NT;
+    constexpr int ROWS = 8 * NT, TK_CH = 16 * MT, NR = 2 * MT;
     __shared__ float part[TK_WARPS][ROWS][TK_CH + 1];
     __shared__ int found[4];
     const MatmulArg &m = p.m;
@@ -140,33 +167,47 @@ __global__ void __launch_bounds__(TK_WARPS * 32)
     const int K = m.w.K;
     const T *X = static_cast<const T *>(m.X);
     const int32_t *gi = m.w.g_idx ? m.w.g_idx + (int64_t)e * K : nullptr;
-    const uint32_t *rows[4];
+    const uint32_t *rows[NR];
+    const float *srow[NR];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NR; ++i) {
         const int ch = c0 + g + 8 * i;
-        rows[i] = ch < m.w.N ? m.w.words + (erow + ch) * m.w.ldw : nullptr;
+        const bool in = ch < m.w.N;
+        rows[i] = in ? m.w.words + (erow + ch) * m.w.ldw : nullptr;
+        srow[i] = in && p.fold ? m.w.scales + (erow + ch) * m.w.groups : nullptr;
     }
-    float acc[2][NT][4];
+    float acc[MT][NT][4];
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int a = 0; a < MT; ++a)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.f;
 
-    // a step: the warp's quads cover 4 U chunks of 32 columns
+    // a step: the warp's quads cover 4 U chunks of 32 columns. Words and scales of the next step
+    // are requested before this one's are used.
     const int steps = (K + 128 * U - 1) / (128 * U);
-    uint32_t cur[4][U * B], nxt[4][U * B];
+    uint32_t cur[NR][U * B], nxt[NR][U * B];
+    float sc[NR][U], sn[NR][U];
+    auto fetch = [&](int step, uint32_t (&w)[NR][U * B], float (&s)[NR][U]) {
+        const int chunk = (step * 4 + quad) * U;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_unit<B, U>(warp < steps ? rows[i] : nullptr, (warp * 4 + quad) * U, nw, p.vec, cur[i]);
+        for (int i = 0; i < NR; ++i) {
+            load_unit<B, U>(step < steps ? rows[i] : nullptr, chunk, nw, p.vec, w[i]);
+            if (p.fold && !gi) {
+#pragma unroll
+                for (int c = 0; c < U; ++c)
+                    s[i][c] = srow[i] && (chunk + c) * 32 < K ? __ldg(srow[i] + (((chunk + c) * 32) >> m.w.gshift)) : 0.f;
+            }
+        }
+    };
+    fetch(warp, cur, sc);
+#pragma unroll 1
     for (int step = warp; step < steps; step += TK_WARPS) {
-        const int ahead = step + TK_WARPS;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            load_unit<B, U>(ahead < steps ? rows[i] : nullptr, (ahead * 4 + quad) * U, nw, p.vec, nxt[i]);
+        if (step + TK_WARPS < steps) fetch(step + TK_WARPS, nxt, sn);
 #pragma unroll
         for (int c = 0; c < U; ++c) {
-            const int chunk = (step * 4 + quad) * U + c, k0 = chunk * 32;
+            const int k0 = ((step * 4 + quad) * U + c) * 32;
             uint32_t x[NT][16];
 #pragma unroll
             for (int b = 0; b < NT; ++b) {
@@ -181,29 +222,36 @@ __global__ void __launch_bounds__(TK_WARPS * 32)
                         v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
                     } else if (left > 0) {
                         const unsigned short *s = reinterpret_cast<const unsigned short *>(src + 8 * q);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i < left) v[i >> 1] |= (uint32_t)__ldg(s + i) << (16 * (i & 1));
+#pragma unroll 1
+                        for (int i = 0; i < 8 && i < left; ++i) {
+                            const uint32_t h = (uint32_t)__ldg(s + i) << (16 * (i & 1));
+                            v[0] |= i >> 1 == 0 ? h : 0u;
+                            v[1] |= i >> 1 == 1 ? h : 0u;
+                            v[2] |= i >> 1 == 2 ? h : 0u;
+                            v[3] |= i >> 1 == 3 ? h : 0u;
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[b][4 * q + i] = v[i];
                 }
+                to_pair_order<B>(x[b]);
             }
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
+            for (int a = 0; a < MT; ++a) {
                 uint32_t v[2][16];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    const int i = 2 * a + h;
                     uint32_t w[B];
 #pragma unroll
-                    for (int j = 0; j < B; ++j) w[j] = cur[2 * a + h][c * B + j];
-                    unpack32<B, T>(w, v[h]);
-                    if (p.fold && k0 < K) {
-                        const int ch = c0 + g + 8 * (2 * a + h);
-                        if (ch < m.w.N) {
-                            const float *sr = m.w.scales + (erow + ch) * m.w.groups;
-                            if (gi) scale32_by_index<T>(v[h], sr, gi, k0, K, m.w.groups, m.status);
-                            else scale32<T>(v[h], __ldg(sr + (k0 >> m.w.gshift)));
+                    for (int j = 0; j < B; ++j) w[j] = cur[i][c * B + j];
+                    unpack32<B, T, false>(w, v[h]);
+                    if (p.fold) {
+                        if (gi) {
+                            if (srow[i] && k0 < K)
+                                scale32_by_index<T, B, false>(v[h], srow[i], gi, k0, K, m.w.groups, m.status);
+                        } else {
+                            scale32<T>(v[h], sc[i][c]);
                         }
                     }
                 }
@@ -216,13 +264,16 @@ __global__ void __launch_bounds__(TK_WARPS * 32)
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < NR; ++i) {
 #pragma unroll
             for (int j = 0; j < U * B; ++j) cur[i][j] = nxt[i][j];
+#pragma unroll
+            for (int c = 0; c < U; ++c) sc[i][c] = sn[i][c];
+        }
     }
     // fragment (16 channels x 8 rows): channel g (+ 8), rows 2 quad, 2 quad + 1
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int a = 0; a < MT; ++a)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -267,13 +318,13 @@ __global__ void __launch_bounds__(TK_WARPS * 32)
     }
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int MT>
 static gptq_status launch_token(const TokenArg &p, int bits, dim3 grid, cudaStream_t st) {
     switch (bits) {
-        case 2: return launch_pdl(k_matmul_token<T, 2, NT>, grid, TK_WARPS * 32, 0, 1, st, p);
-        case 3: return launch_pdl(k_matmul_token<T, 3, NT>, grid, TK_WARPS * 32, 0, 1, st, p);
-        case 4: return launch_pdl(k_matmul_token<T, 4, NT>, grid, TK_WARPS * 32, 0, 1, st, p);
-        default: return launch_pdl(k_matmul_token<T, 8, NT>, grid, TK_WARPS * 32, 0, 1, st, p);
+        case 2: return launch_pdl(k_matmul_token<T, 2, NT, MT>, grid, TK_WARPS * 32, 0, 1, st, p);
+        case 3: return launch_pdl(k_matmul_token<T, 3, NT, MT>, grid, TK_WARPS * 32, 0, 1, st, p);
+        case 4: return launch_pdl(k_matmul_token<T, 4, NT, MT>, grid, TK_WARPS * 32, 0, 1, st, p);
+        default: return launch_pdl(k_matmul_token<T, 8, NT, MT>, grid, TK_WARPS * 32, 0, 1, st, p);
     }
 }
 
@@ -284,16 +335,17 @@ gptq_status matmul_token(const MatmulArg &m, int dtype, int bits, cudaStream_t s
     p.fold = m.w.groups > 0 ? 1 : 0;
     p.vec = aligned(m.w.words, 16) && m.w.ldw % 4 == 0;
     p.xvec = aligned(m.X, 16) && m.ldx % 8 == 0;
-    // one range: up to 16 rows at once; several: most have a few rows
+    // one range: up to 16 rows at once, which share the reading of X between 32 channels;
+    // several ranges: most have a few rows
     const bool wide = p.E == 1 && m.M > 8;
-    const int rows = wide ? 16 : 8;
-    const int64_t items = std::min<int64_t>(p.E, m.M) + m.M / rows;
-    const dim3 grid((m.w.N + TK_CH - 1) / TK_CH, (unsigned)std::max<int64_t>(1, p.E == 1 ? (m.M + rows - 1) / rows : items));
+    const int rows = wide ? 16 : 8, channels = wide ? 32 : 16;
+    const int64_t items = p.E == 1 ? (m.M + rows - 1) / rows : std::min<int64_t>(p.E, m.M) + m.M / rows;
+    const dim3 grid((m.w.N + channels - 1) / channels, (unsigned)items);
     if (dtype == GPTQ_BF16)
-        return wide ? launch_token<__nv_bfloat16, 2>(p, bits, grid, st)
-                    : launch_token<__nv_bfloat16, 1>(p, bits, grid, st);
-    return wide ? launch_token<__half, 2>(p, bits, grid, st)
-                : launch_token<__half, 1>(p, bits, grid, st);
+        return wide ? launch_token<__nv_bfloat16, 2, 2>(p, bits, grid, st)
+                    : launch_token<__nv_bfloat16, 1, 1>(p, bits, grid, st);
+    return wide ? launch_token<__half, 2, 2>(p, bits, grid, st)
+                : launch_token<__half, 1, 1>(p, bits, grid, st);
 }
 
 }  // namespace gptq

@@ -144,16 +144,9 @@ def host_calls(lib, monkeypatch):
                 return 0
             return fn
 
-    def host_ptr(t, dev=None, name="tensor", rows=False):
-        if t is None:
-            return None
-        gq._check_layout(t, name, rows)
-        return P(t.data_ptr())
-
     monkeypatch.setattr(gq, "_lib", FakeLib())
     monkeypatch.setattr(gq, "_device", lambda t, name: t.device)
     monkeypatch.setattr(gq, "_stream", lambda stream, dev=None: P(0))
-    monkeypatch.setattr(gq, "_ptr", host_ptr)
     monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
     return calls
 
