@@ -4,12 +4,17 @@
 //   T[t] = alpha_a A_a X[t]        (forward, and the gradient of B)
 //   U[t] = alpha_a B_a^T dY[t]     (gradients of X and A)
 //
-// Both are one kernel (k_rank_rows): a thin product rows x [rank][inner], bound by reading the
-// rows (long prompts) or the adapters (requests that decode, each with an adapter of its own).
-// Row and adapter fragments of mma.sync m16n8k16 are read straight from global memory: a lane
-// takes 16 bytes (8 neighbouring columns) of its row and of its adapter row, which permutes
-// the contraction index alike on both sides. The result leaves as a pair of 16-bit halves
-// [hi | lo], 16 bits of the fp32 sum, which the products that follow read as matrix operands.
+// Both are a thin product rows x [rank][inner], bound by reading the rows (long prompts) or the
+// adapters (requests that decode, each with an adapter of its own). The result leaves as a pair
+// of 16-bit halves [hi | lo], 16 bits of the fp32 sum, which the products that follow read as
+// matrix operands. Tiles of rows are cut inside each request, so a tile has one adapter.
+//   k_rank_tc    prompts: the adapter is the A operand of tcgen05 (rank lanes), 64 rows the B
+//                operand, both by tiled copies in steps of 128 columns.
+//   k_rank_rows  a few rows, or layouts that tiled copies refuse: fragments of mma.sync m16n8k16
+//                straight from global memory; a lane takes 16 bytes (8 neighbouring columns) of
+//                its row and of its adapter row, which permutes the contraction index alike on
+//                both sides.
+// A cluster of up to 8 blocks shares the contraction of a tile when there are few tiles.
 // B_a is stored [N][rank]; its gradient pass reads it transposed once (k_transpose).
 #include <algorithm>
 
@@ -67,44 +72,81 @@ __device__ __forceinline__ uint4 piece(const T *row, int c, int cols, bool vec) 
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// The b-th tile of `rows` rows: its first row, its rows and its adapter; none: false. Requests
+// without an adapter have no tiles. Offsets and ids are checked as a whole first (refused: status,
+// false). Called by every thread of the block; `found` is four ints of shared memory.
+__device__ __forceinline__ bool rank_tile(const RankArg &p, int64_t b, int rows, int *found, int &t, int &n,
+                                          int &id) {
+    if (threadIdx.x < 4) found[threadIdx.x] = 0;
+    __syncthreads();
+    bool bad = offsets_bad(p.offsets, p.R, p.M, threadIdx.x, blockDim.x);
+    bad |= ids_bad(p.ids, p.R, p.L, threadIdx.x, blockDim.x);
+    if (bad) found[3] = 1;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int64_t base = 0;
+        for (int s0 = 0; s0 < p.R && base <= b; s0 += 32) {
+            const int s = s0 + lane;
+            int begin = 0, len = 0, a = -1;
+            if (s < p.R) {
+                begin = __ldg(p.offsets + s);
+                len = __ldg(p.offsets + s + 1) - begin;
+                a = __ldg(p.ids + s);
+            }
+            const int nt = a >= 0 && len > 0 ? (len + rows - 1) / rows : 0;
+            int sum = nt;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(~0u, sum, d);
+                if (lane >= d) sum += v;
+            }
+            const int64_t j = b - (base + sum - nt);
+            if (j >= 0 && j < nt) {
+                found[0] = begin + (int)j * rows;
+                found[1] = min(rows, len - (int)j * rows);
+                found[2] = a;
+            }
+            base += __shfl_sync(~0u, sum, 31);
+        }
+    }
+    __syncthreads();
+    if (found[3]) {
+        if (threadIdx.x == 0) set_status(p.status, GPTQ_ERR_ARG);
+        return false;
+    }
+    t = found[0];
+    n = found[1];
+    id = found[2];
+    return n > 0;
+}
+
+// A rank-space value as its two halves.
+template <typename T>
+__device__ __forceinline__ void store_pair(T *d, int rank, float v) {
+    const T hi = from_f32<T>(v);
+    const float f = to_f32<T>(hi);
+    d[0] = hi;
+    d[rank] = from_f32<T>(isfinite(f) ? v - f : 0.f);      // an infinite half has no rest
+}
+
 // Block (row tile, part of the contraction): MW warps of 16 rows x KW warps of the contraction;
-// a cluster of `split` blocks shares a tile's contraction. Tiles are cut inside each request, so
-// a tile has one adapter; block b looks at row off[0] + b and works when a tile starts there.
+// a cluster of `split` blocks shares a tile's contraction.
 template <typename T, int NR, int MW, int KW>
 __global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constant__ RankArg p) {
     constexpr int THREADS = MW * KW * 32, ROWS = 16 * MW;
     __shared__ float part[KW][ROWS][NR * 8 + 1];
-    __shared__ int flag[2];
+    __shared__ int found[4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = lane & 3, g = lane >> 2;
     const int mw = warp % MW, kw = warp / MW;
     const uint32_t rank = p.split > 1 ? tc::cluster_ctarank() : 0u;
-    const int64_t tile = blockIdx.x / p.split;
     grid_dependency();
-    if (threadIdx.x < 2) flag[threadIdx.x] = 0;
-    __syncthreads();
-    bool bad = offsets_bad(p.offsets, p.R, p.M, threadIdx.x, THREADS);
-    bad |= ids_bad(p.ids, p.R, p.L, threadIdx.x, THREADS);
-    if (bad) flag[0] = 1;
-    // request of the row: the requests that end at or before it
-    const int64_t t = (int64_t)__ldg(p.offsets) + tile;
-    int before = 0;
-    for (int i = threadIdx.x; i < p.R; i += THREADS) before += (int64_t)__ldg(p.offsets + i + 1) <= t;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(~0u, before, d);
-    if (lane == 0 && before) atomicAdd(&flag[1], before);
-    __syncthreads();
-    // every block of a cluster sees the same offsets, so they agree on what follows
-    if (flag[0]) {
-        if (threadIdx.x == 0) set_status(p.status, GPTQ_ERR_ARG);
-        return;
-    }
-    const int s = flag[1];
-    if (s >= p.R) return;
-    const int begin = __ldg(p.offsets + s), end = __ldg(p.offsets + s + 1), id = __ldg(p.ids + s);
-    if (id < 0 || (t - begin) % ROWS != 0) return;
+    int t, n, id;
+    // every block of a cluster looks for the same tile, so they agree
+    if (!rank_tile(p, blockIdx.x / p.split, ROWS, found, t, n, id)) return;
+    const int end = t + n;
 
-    const int r0 = (int)t + mw * 16;
+    const int r0 = t + mw * 16;
     const T *X = static_cast<const T *>(p.X);
     const T *x0 = r0 + g < end ? X + (int64_t)(r0 + g) * p.ldx : nullptr;
     const T *x1 = r0 + g + 8 < end ? X + (int64_t)(r0 + g + 8) * p.ldx : nullptr;
@@ -117,7 +159,8 @@ __global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constan
     const int steps = (p.inner + 31) / 32;
     const int s0 = (int)((int64_t)steps * rank / p.split), s1 = (int)((int64_t)steps * (rank + 1) / p.split);
     const bool xv = p.xvec != 0, av = p.avec != 0;
-#pragma unroll 2
+    constexpr int AHEAD = NR <= 2 ? 4 : NR <= 4 ? 2 : 1;      // steps in flight
+#pragma unroll AHEAD
     for (int step = s0 + kw; step < s1; step += KW) {
         const int c = step * 32 + quad * 8;
         const uint4 a = piece<T>(x0, c, p.inner, xv), b = piece<T>(x1, c, p.inner, xv);
@@ -135,7 +178,7 @@ __global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constan
         for (int i = 0; i < 4; ++i)
             part[kw][mw * 16 + g + 8 * (i >> 1)][j * 8 + 2 * quad + (i & 1)] = acc[j][i];
     __syncthreads();
-    const int rows = min(ROWS, end - (int)t);
+    const int rows = n;
     for (int i = threadIdx.x; i < rows * NR * 8; i += THREADS) {
         const int row = i / (NR * 8), j = i % (NR * 8);
         float sum = part[0][row][j];
@@ -158,39 +201,195 @@ __global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constan
         } else {
             sum = part[0][row][j];
         }
-        if (j < p.rank) {
-            const float v = alpha * sum;
-            const T hi = from_f32<T>(v);
-            const float f = to_f32<T>(hi);
-            // an infinite half has no rest
-            const T lo = from_f32<T>(isfinite(f) ? v - f : 0.f);
-            T *d = out + ((int64_t)t + row) * 2 * p.rank + j;
-            d[0] = hi;
-            d[p.rank] = lo;
-        }
+        if (j < p.rank) store_pair<T>(out + ((int64_t)t + row) * 2 * p.rank + j, p.rank, alpha * sum);
     }
     if (p.split > 1) tc::cluster_sync();
 }
 
+// ---- prompts -------------------------------------------------------------------------------
+
+namespace {
+constexpr int RK_ROWS = 64, RK_BK = 128, RK_STAGES = 4;
+constexpr int RK_X = RK_ROWS * RK_BK * 2;               // 16 KB, two boxes of 64 columns
+constexpr int RK_A = 128 * RK_BK * 2;                   // 32 KB; only `rank` rows are filled
+constexpr int RK_STAGE = RK_X + RK_A;
+constexpr int RK_SMEM = RK_STAGES * RK_STAGE + 1024 + 256;
+constexpr int RK_THREADS = 192;
+}  // namespace
+
+// Roles: warp 0 tiled copies, warp 1 TMEM and MMAs, warps 2-5 outputs. The lanes past the rank
+// multiply what the stage happens to hold; nothing reads them.
+template <typename T>
+__global__ void __launch_bounds__(RK_THREADS, 1)
+    k_rank_tc(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
+              const __grid_constant__ RankArg p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + RK_STAGES * RK_STAGE);
+    uint64_t *empty = full + RK_STAGES;
+    uint64_t *tfull = empty + RK_STAGES;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tfull + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    __shared__ int found[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = p.split > 1 ? tc::cluster_ctarank() : 0u;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < RK_STAGES; ++s) {
+            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&empty[s], 1);
+        }
+        tc::mbar_init(tfull, 1);
+        *abort = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_tmap(&xmap);
+        tc::prefetch_tmap(&amap);
+    }
+    if (warp == 1) tc::tmem_alloc(tmem_slot, 64);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency();
+    int t = 0, n = 0, id = 0;
+    // every block of a cluster looks for the same tile, so they agree
+    const bool work = rank_tile(p, blockIdx.x / p.split, RK_ROWS, found, t, n, id);
+    const int steps = (p.inner + RK_BK - 1) / RK_BK;
+    const int s0 = (int)((int64_t)steps * rank / p.split), s1 = (int)((int64_t)steps * (rank + 1) / p.split);
+    const int n16 = (n + 15) & ~15;
+    float *sums = reinterpret_cast<float *>(smem);       // [row][rank] once the stages are done with
+    if (work) {
+        if (warp == 0) {
+            bool ok = true;
+            for (int s = s0; s < s1; ++s) {
+                const int i = s - s0, stage = i % RK_STAGES;
+                ok = __all_sync(~0u, tc::mbar_wait(&empty[stage], ((i / RK_STAGES) & 1) ^ 1, abort));
+                if (!ok) break;
+                uint8_t *x = smem + stage * RK_STAGE, *a = x + RK_X;
+                if (tc::elect_one()) {
+                    tc::mbar_arrive_expect_tx(&full[stage], RK_X + p.rank * 256);
+                    tc::tma_load_2d(x, &xmap, &full[stage], s * RK_BK, t);
+                    tc::tma_load_2d(x + RK_X / 2, &xmap, &full[stage], s * RK_BK + 64, t);
+                    tc::tma_load_2d(a, &amap, &full[stage], s * RK_BK, id * p.rank);
+                    tc::tma_load_2d(a + RK_A / 2, &amap, &full[stage], s * RK_BK + 64, id * p.rank);
+                }
+                __syncwarp();
+            }
+            if (!ok) {                      // loads still in flight land before the block exits
+                const long long from = clock64();
+                while (clock64() - from < 20000000ll) {
+                }
+            }
+        } else if (warp == 1) {
+            const uint32_t idesc = tc::idesc_f16_f32(Half2<T>::kType, 128, n16, 0, 0);
+            const uint64_t bd0 = tc::desc_sw128(tc::smem_u32(smem), 16, 1024);
+            const uint64_t ad0 = tc::desc_sw128(tc::smem_u32(smem) + RK_X, 16, 1024);
+            bool ok = true;
+            for (int s = s0; s < s1; ++s) {
+                const int i = s - s0, stage = i % RK_STAGES;
+                ok = __all_sync(~0u, tc::mbar_wait(&full[stage], (i / RK_STAGES) & 1, abort));
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t by = (uint32_t)(stage * RK_STAGE >> 4);
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < RK_BK / 16; ++kk)
+                        tc::mma_bf16(tmem, ad0 + by + ((kk >> 2) * (RK_A / 2) + (kk & 3) * 32 >> 4),
+                                     bd0 + by + ((kk >> 2) * (RK_X / 2) + (kk & 3) * 32 >> 4), idesc,
+                                     (i > 0 || kk > 0) ? 1u : 0u);
+                    tc::mma_commit(&empty[stage]);
+                }
+                __syncwarp();
+            }
+            // (also after a time-out: what was issued completes before TMEM is released)
+            if (tc::elect_one()) tc::mma_commit(tfull);
+            __syncwarp();
+            volatile int never = 0;
+            tc::mbar_wait(tfull, 0, &never);
+        } else {
+            // lane = rank index: into shared memory, over stages that the MMAs have read
+            const int quad = warp & 3, j = quad * 32 + lane;
+            volatile int never = 0;
+            const bool ok = __all_sync(~0u, tc::mbar_wait(tfull, 0, &never)) && !*abort;
+            tc::fence_after_sync();
+            if (ok && quad * 32 < p.rank) {
+                for (int c = 0; c < n16; c += 16) {
+                    uint32_t v[16];
+                    tc::tmem_ld_32x32b_x16(tmem + c + ((uint32_t)(quad * 32) << 16), v);
+                    tc::tmem_ld_wait();
+                    if (j < p.rank) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) sums[(c + q) * p.rank + j] = __uint_as_float(v[q]);
+                    }
+                }
+            }
+            tc::fence_before_sync();
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (p.split > 1) tc::cluster_sync();
+    // a cluster writes only when every block of it finished (the flags are read after the barrier)
+    bool all = work && !*abort;
+    if (p.split > 1 && work)
+        for (int c = 0; c < p.split; ++c)
+            all &= tc::ld_shared_cluster(tc::mapa_shared(tc::smem_u32(const_cast<int *>(abort)), c)) == 0;
+    if (all) {
+        const float alpha = __ldg(p.alpha + id);
+        T *out = static_cast<T *>(p.T2);
+        const int total = n * p.rank, per = (total + p.split - 1) / p.split;
+        for (int i = (int)rank * per + threadIdx.x; i < min(total, ((int)rank + 1) * per); i += RK_THREADS) {
+            const int row = i / p.rank, j = i - row * p.rank;
+            float sum = 0.f;
+            if (p.split > 1) {
+                const uint32_t at = tc::smem_u32(&sums[i]);
+                for (int c = 0; c < p.split; ++c)
+                    sum += __uint_as_float(tc::ld_shared_cluster(tc::mapa_shared(at, c)));
+            } else {
+                sum = sums[i];
+            }
+            store_pair<T>(out + ((int64_t)t + row) * 2 * p.rank + j, p.rank, alpha * sum);
+        }
+    }
+    if (p.split > 1) tc::cluster_sync();
+    if (*abort && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_TIMEOUT);
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 64);
+    }
+}
+
 template <typename T, int NR>
 static gptq_status launch_rank_nr(RankArg &p, cudaStream_t st) {
-    const int64_t rows = p.M;
-    if (rows >= 1024) {
-        // long prompts: bound by the rows; 64 rows a block share the adapter
+    if (p.M >= 1024) {
+        // many rows in a layout that tiled copies refuse: 64 rows a block share the adapter
         constexpr int KW = NR > 8 ? 1 : 2;
         p.split = 1;
-        return launch_pdl(k_rank_rows<T, NR, 4, KW>, dim3((unsigned)rows), 128 * KW, 0, 1, st, p);
+        return launch_pdl(k_rank_rows<T, NR, 4, KW>, dim3((unsigned)(p.R + p.M / 64)), 128 * KW, 0, 1, st, p);
     }
     constexpr int KW = NR > 8 ? 4 : 8;
     const int steps = (p.inner + 31) / 32;
     p.split = 1;
-    const int64_t tiles = std::min<int64_t>(rows, p.R + rows / 16);
+    const int64_t tiles = std::min<int64_t>(p.M, p.R + p.M / 16);
     while (p.split < 8 && tiles * p.split * 2 <= 2 * device_sms() && steps >= 4 * KW * p.split) p.split *= 2;
-    return launch_pdl(k_rank_rows<T, NR, 1, KW>, dim3((unsigned)(rows * p.split)), 32 * KW, 0, p.split, st, p);
+    return launch_pdl(k_rank_rows<T, NR, 1, KW>, dim3((unsigned)(tiles * p.split)), 32 * KW, 0, p.split, st, p);
 }
 
 template <typename T>
-static gptq_status launch_rank(RankArg &p, cudaStream_t st) {
+static gptq_status launch_rank(RankArg &p, int dtype, cudaStream_t st) {
+    // prompts: 64 rows a tile. The bound on short requests is that of tiles that a few rows fill.
+    if (p.M >= 256 && p.M >= 16 * (int64_t)p.R) {
+        CUtensorMap xm{}, am{};
+        if (rows_map(&xm, p.X, dtype, p.M, p.inner, p.ldx, RK_ROWS) &&
+            rows_map(&am, p.A, dtype, (int64_t)p.L * p.rank, p.inner, p.inner, p.rank)) {
+            const int64_t tiles = p.R + p.M / RK_ROWS;
+            const int steps = (p.inner + RK_BK - 1) / RK_BK;
+            p.split = 1;
+            while (p.split < 8 && tiles * p.split * 2 <= device_sms() && steps >= 4 * p.split) p.split *= 2;
+            return launch_pdl(k_rank_tc<T>, dim3((unsigned)(tiles * p.split)), RK_THREADS, RK_SMEM, p.split, st, xm,
+                              am, p);
+        }
+    }
     if (p.rank <= 8) return launch_rank_nr<T, 1>(p, st);
     if (p.rank <= 16) return launch_rank_nr<T, 2>(p, st);
     if (p.rank <= 32) return launch_rank_nr<T, 4>(p, st);
@@ -269,7 +468,7 @@ static gptq_status rank_rows(void *T2, const void *X, int64_t ldx, int64_t M, co
     p.xvec = aligned(X, 16) && ldx % 8 == 0;
     p.avec = aligned(A, 16) && inner % 8 == 0;
     p.status = status;
-    return dtype == GPTQ_BF16 ? launch_rank<__nv_bfloat16>(p, st) : launch_rank<__half>(p, st);
+    return dtype == GPTQ_BF16 ? launch_rank<__nv_bfloat16>(p, dtype, st) : launch_rank<__half>(p, dtype, st);
 }
 
 struct LoraSpace {

@@ -333,15 +333,21 @@ __device__ __forceinline__ int request_of(const int32_t *off, int R, int t) {
     return lo;
 }
 
+// Runs shorter than this are added by the outputs' threads, row by row; longer ones are matrix
+// operands of their own (an MMA takes 16 columns at least, and a round of barriers).
+constexpr int LORA_SHORT = 16;
+
 // Walks the rows [t0, t1) in runs of one adapter: neighbouring requests with the same adapter
-// make one run; rows without an adapter are skipped.
+// make one run; rows without an adapter are skipped, and runs of the other kind (shorter or not
+// shorter than LORA_SHORT inside [t0, t1)).
 struct RunWalk {
     const int32_t *off, *ids;
     int R, t1, s, t;
     int begin, end, id;       // the current run: rows [begin, end), its adapter
+    bool shorts;
     __device__ __forceinline__ RunWalk(const int32_t *off_, const int32_t *ids_, int R_, int t0,
-                                       int t1_)
-        : off(off_), ids(ids_), R(R_), t1(t1_), s(request_of(off_, R_, t0)), t(t0) {}
+                                       int t1_, bool shorts_ = false)
+        : off(off_), ids(ids_), R(R_), t1(t1_), s(request_of(off_, R_, t0)), t(t0), shorts(shorts_) {}
     __device__ __forceinline__ bool next() {
         while (s < R && t < t1) {
             const int e = min(__ldg(off + s + 1), t1);
@@ -357,11 +363,56 @@ struct RunWalk {
                 t = end;
                 ++s;
             }
-            if (a >= 0) return true;
+            if (a >= 0 && (end - begin < LORA_SHORT) == shorts) return true;
         }
         return false;
     }
 };
+
+// One row's adapter term of one output channel: sum_j P_a[ch][j] T[t][j] (forward, P = B) or
+// sum_j P_a[j][ch] T[t][j] (input gradient, P = A), fp32.
+template <typename T, int DIR>
+__device__ __forceinline__ float lora_term(const LoraArg &l, int id, int64_t t, int ch, int channels) {
+    const int r = l.rank;
+    const T *h = static_cast<const T *>(l.T2) + t * 2 * r;
+    float add = 0.f;
+    if constexpr (DIR == 0) {
+        const T *b = static_cast<const T *>(l.P) + ((int64_t)id * channels + ch) * r;
+#pragma unroll 2
+        for (int j = 0; j < r; j += 8) {
+            const uint4 bv = __ldg(reinterpret_cast<const uint4 *>(b + j));
+            const uint4 hv = __ldg(reinterpret_cast<const uint4 *>(h + j));
+            const uint4 lv = __ldg(reinterpret_cast<const uint4 *>(h + r + j));
+            const uint32_t bb[4] = {bv.x, bv.y, bv.z, bv.w}, hh[4] = {hv.x, hv.y, hv.z, hv.w},
+                           ll[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 fb = Half2<T>::unpack(bb[q]), fh = Half2<T>::unpack(hh[q]),
+                             fl = Half2<T>::unpack(ll[q]);
+                add = fmaf(fb.x, fh.x + fl.x, add);
+                add = fmaf(fb.y, fh.y + fl.y, add);
+            }
+        }
+    } else {
+        const unsigned short *a = reinterpret_cast<const unsigned short *>(l.P) + (int64_t)id * r * channels + ch;
+#pragma unroll 2
+        for (int j = 0; j < r; j += 8) {
+            const uint4 hv = __ldg(reinterpret_cast<const uint4 *>(h + j));
+            const uint4 lv = __ldg(reinterpret_cast<const uint4 *>(h + r + j));
+            const uint32_t hh[4] = {hv.x, hv.y, hv.z, hv.w}, ll[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 fh = Half2<T>::unpack(hh[q]), fl = Half2<T>::unpack(ll[q]);
+                const uint32_t w = __ldg(a + (int64_t)(j + 2 * q) * channels) |
+                                   ((uint32_t)__ldg(a + (int64_t)(j + 2 * q + 1) * channels) << 16);
+                const float2 fa = Half2<T>::unpack(w);
+                add = fmaf(fa.x, fh.x + fl.x, add);
+                add = fmaf(fa.y, fh.y + fl.y, add);
+            }
+        }
+    }
+    return add;
+}
 
 // ---- host ----------------------------------------------------------------------------------
 

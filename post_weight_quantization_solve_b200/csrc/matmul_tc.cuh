@@ -24,7 +24,8 @@
 // Adapters: after the steps of W^, each run of rows with one adapter adds
 // sum_j P_a[.][j] T[t][j] over the run's columns alone (runs are widened to the MMA's column borders,
 // the rows there that belong to others are zero in shared memory). T comes as a pair of 16-bit
-// halves, so the rank-space rows keep 16 bits.
+// halves, so the rank-space rows keep 16 bits. Runs of fewer than 16 rows (requests that decode)
+// are added by the threads that write the outputs: as matrix steps they cost about 1.3 us each.
 //
 // Order: the tiles of a range run rows first, so that blocks that work at the same time read
 // different rows of X and the same (few) words; with channels first every block asked the L2
@@ -51,7 +52,7 @@ constexpr int MM_HALF = MM_ROWS * 64 * 2;           // 64 columns of them, 16 KB
 constexpr int MM_B_BYTES = 2 * MM_HALF;
 constexpr int MM_A_BYTES = MM_LANES * MM_BK * 2;    // 32 KB (input gradient)
 constexpr int MM_BOX = 128 * 64 * 2;                // A: 128 contraction rows x 64 columns
-constexpr int MM_TABLE = (MATMUL_MAX_EXPERTS + 4) * 4;
+constexpr int MM_TABLE = (MATMUL_MAX_EXPERTS + 4 + 256) * 4;    // and the adapters of a tile's rows
 constexpr uint32_t MM_TMEM = 512;
 constexpr int MM_MAX_STAGES = 4;                    // of 64 TMEM columns beside the accumulators
 
@@ -458,37 +459,45 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     const int rows = PAIR ? (b1 - b0) / 2 : b1 - b0;
                     const int row0 = b0 + (PAIR ? (int)rank * rows : 0);
                     for (int rs = 0; rs < rsteps; ++rs) {
+                        // this thread's part of A, requested before the stage is free. Forward: row n
+                        // of B_a twice over, [hi part | lo part] of the contraction; input gradient:
+                        // rows of A_a, twice over too
+                        uint4 y[8];
+                        const int qa = rs * MM_BK + (DIR == 0 ? set * 64 : arow);
+                        if constexpr (DIR == 0) {
+                            const T *src = P + ((int64_t)run.id * m.w.N + ch) * r;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int q = qa + j * 8;
+                                y[j] = ch < m.w.N && q < two_r ? load8<T>(src + (q < r ? q : q - r), 8, true)
+                                                               : make_uint4(0u, 0u, 0u, 0u);
+                            }
+                        } else {
+                            const int c = t.c0 + ahalf * 64;
+                            const T *src = P + ((int64_t)run.id * r + (qa < r ? qa : qa - r)) * m.w.K + c;
+                            const bool v8 = (m.w.K & 7) == 0;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) y[j] = load8<T>(src + 8 * j, qa < two_r ? m.w.K - c - 8 * j : 0, v8);
+                        }
                         bool ok = tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort);
                         ok = __all_sync(~0u, ok);
                         if (ok) {
                             uint8_t *st = smem + pos.stage * stage_bytes;
                             if constexpr (DIR == 0) {
-                                // A: row n of B_a twice over, [hi part | lo part] of the contraction
-                                if (rs * MM_BK + set * 64 < two_r) {
-                                    uint32_t y[32];
-                                    const T *src = P + ((int64_t)run.id * m.w.N + ch) * r;
+                                uint32_t z[32];
 #pragma unroll
-                                    for (int j = 0; j < 8; ++j) {
-                                        const int q = rs * MM_BK + set * 64 + j * 8;
-                                        const uint4 x = ch < m.w.N && q < two_r ? load8<T>(src + (q < r ? q : q - r), 8, true)
-                                                                                : make_uint4(0u, 0u, 0u, 0u);
-                                        y[4 * j] = x.x; y[4 * j + 1] = x.y; y[4 * j + 2] = x.z; y[4 * j + 3] = x.w;
-                                    }
-                                    tc::fence_after_sync();
-                                    tc::tmem_st_32x32b_x32(tmem + 256 + pos.stage * 64 + set * 32 +
-                                                               ((uint32_t)(wq * 32) << 16), y);
-                                    tc::tmem_st_wait();
+                                for (int j = 0; j < 8; ++j) {
+                                    z[4 * j] = y[j].x; z[4 * j + 1] = y[j].y; z[4 * j + 2] = y[j].z; z[4 * j + 3] = y[j].w;
                                 }
+                                tc::fence_after_sync();
+                                tc::tmem_st_32x32b_x32(tmem + 256 + pos.stage * 64 + set * 32 +
+                                                           ((uint32_t)(wq * 32) << 16), z);
+                                tc::tmem_st_wait();
                             } else {
-                                const int q = rs * MM_BK + arow;
-                                const int c = t.c0 + ahalf * 64;
-                                const T *src = P + ((int64_t)run.id * r + (q < r ? q : q - r)) * m.w.K + c;
                                 uint8_t *a = st + MM_B_BYTES + ahalf * MM_BOX + arow * 128;
-                                const bool v8 = (m.w.K & 7) == 0;
 #pragma unroll
                                 for (int j = 0; j < 8; ++j)
-                                    *reinterpret_cast<uint4 *>(a + ((j ^ (arow & 7)) << 4)) =
-                                        load8<T>(src + 8 * j, q < two_r ? m.w.K - c - 8 * j : 0, v8);
+                                    *reinterpret_cast<uint4 *>(a + ((j ^ (arow & 7)) << 4)) = y[j];
                             }
                             // the run's rows of [hi | lo], zeros for rows of others
                             for (int j = tid; j < rows * 16; j += 256) {
@@ -521,6 +530,21 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             const int ch = t.c0 + wq * 32 + lane;
             const bool per_channel = DIR == 0 && !p.fold;
             const float s = per_channel && ch < p.out ? __ldg(m.w.scales + (int64_t)t.e * m.w.N + ch) : 1.f;
+            // adapters of the rows in short runs (-1: none), found while the products run
+            bool shorts = false;
+            int *row_ids = table + MATMUL_MAX_EXPERTS + 4;
+            if (m.lora.R > 0) {
+                asm volatile("bar.sync 1, 128;" ::: "memory");      // the tile before is done with them
+                for (int r = etid; r < t.n; r += 128) row_ids[r] = -1;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                RunWalk run(m.offsets, m.lora.ids, m.lora.R, (int)t.t0, (int)t.t0 + t.n, true);
+                while (run.next()) {
+                    shorts = true;
+                    if (warp == 8)
+                        for (int r = run.begin + lane; r < run.end; r += 32) row_ids[r - (int)t.t0] = run.id;
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
             bool ok = tc::mbar_wait(&tfull[acc], acc_phase, abort);
             ok = __all_sync(~0u, ok);
             tc::fence_after_sync();
@@ -534,6 +558,18 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
             };
             if (split == 1) {
+                if (shorts && ok) {
+                    // their terms into the accumulators
+                    for (int r = 0; r < t.n; ++r) {
+                        const int id = row_ids[r];
+                        if (id < 0) continue;
+                        const float add = ch < p.out ? lora_term<T, DIR>(m.lora, id, t.t0 + r, ch, p.out) : 0.f;
+                        const uint32_t y = tc::tmem_ld_32x32b_x1(at + r);
+                        tc::tmem_ld_wait();
+                        tc::tmem_st_32x32b_x1(at + r, __float_as_uint(__uint_as_float(y) + add));
+                    }
+                    tc::tmem_st_wait();
+                }
                 // through shared memory as [row][channel], `chunk` rows at a time
                 const int chunk = p.epi / 256;
                 T *stg = reinterpret_cast<T *>(epi);
@@ -598,8 +634,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 bool all = tc::mbar_wait_cluster(ready, sum_phase, abort);
                 all = __all_sync(~0u, all) && ok;
                 if (all) {
+#pragma unroll 2
                     for (int row = (int)rank; row < t.n; row += split) {
                         float sum = 0.f;
+                        if (shorts && row_ids[row] >= 0 && ch < p.out)
+                            sum = lora_term<T, DIR>(m.lora, row_ids[row], t.t0 + row, ch, p.out);
                         const uint32_t from = tc::smem_u32(dump + row * MM_LANES + wq * 32 + lane);
                         for (int c = 0; c < split; ++c)
                             sum += __uint_as_float(tc::ld_shared_cluster(tc::mapa_shared(from, c)));

@@ -292,27 +292,7 @@ __global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
             const int t = (int)t0 + row;
             const int s = request_of(m.offsets, m.lora.R, t);
             const int id = __ldg(m.lora.ids + s);
-            if (id >= 0) {
-                const int r = m.lora.rank;
-                const T *b = static_cast<const T *>(m.lora.P) + ((int64_t)id * m.w.N + ch) * r;
-                const T *h = static_cast<const T *>(m.lora.T2) + (int64_t)t * 2 * r;
-                float add = 0.f;
-                for (int j = 0; j < r; j += 8) {
-                    const uint4 bv = __ldg(reinterpret_cast<const uint4 *>(b + j));
-                    const uint4 hv = *reinterpret_cast<const uint4 *>(h + j);
-                    const uint4 lv = *reinterpret_cast<const uint4 *>(h + r + j);
-                    const uint32_t bb[4] = {bv.x, bv.y, bv.z, bv.w}, hh[4] = {hv.x, hv.y, hv.z, hv.w},
-                                   ll[4] = {lv.x, lv.y, lv.z, lv.w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float2 fb = Half2<T>::unpack(bb[q]), fh = Half2<T>::unpack(hh[q]),
-                                     fl = Half2<T>::unpack(ll[q]);
-                        add = fmaf(fb.x, fh.x + fl.x, add);
-                        add = fmaf(fb.y, fh.y + fl.y, add);
-                    }
-                }
-                sum += add;
-            }
+            if (id >= 0) sum += lora_term<T, 0>(m.lora, id, t, ch, m.w.N);
         }
         Y[(t0 + row) * m.ldy + ch] = from_f32<T>(sum);
     }
