@@ -29,7 +29,7 @@ extern "C" {
  *   g_idx      device int32 [experts][K], the group of each column (each in
  *              [0, ceil(K / groupsize)), else GPTQ_ERR_ARG in the status word), or NULL:
  *              column k in group k / groupsize (natural order and static groups).
- *   experts    1..1024; a plain projection is one expert.
+ *   experts    1..512; a plain projection is one expert.
  *   N, K       1..GPTQ_MAX_DIM.  bits 2, 3, 4 or 8.  groupsize 0, 32, 64 or 128.
  */
 typedef struct {

@@ -48,7 +48,7 @@ struct MatmulArg {
     int32_t *status;
 };
 
-constexpr int MATMUL_MAX_EXPERTS = 1024;
+constexpr int MATMUL_MAX_EXPERTS = 512;
 
 // ---- 16-bit types --------------------------------------------------------------------------
 

@@ -68,7 +68,7 @@ gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStre
     // staging: a whole tall tile where it holds the only accumulator, partial sums in fp32 when split
     p.epi = p.split > 1 ? p.cols * MM_LANES * 4 : p.accs == 1 ? p.cols * MM_LANES * 2 : 32 * MM_LANES * 2;
     const int stage = MM_B_BYTES + (dir == 1 ? MM_A_BYTES : 0);
-    const size_t fixed = ring_bytes(bits, dir) + p.epi + MM_TABLE + 1024 + 512;
+    const size_t fixed = ring_bytes(bits, dir) + p.epi + MM_TABLE + 1024 + 320;
     p.stages = (int)std::min<size_t>(MM_MAX_STAGES, (227 * 1024 - fixed) / stage);
     const size_t smem = fixed + (size_t)p.stages * stage;
     const int cluster = pair ? 2 : p.split;

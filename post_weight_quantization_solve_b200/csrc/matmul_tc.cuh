@@ -31,10 +31,11 @@
 // different rows of X and the same (few) words; with channels first every block asked the L2
 // for the same lines of X at once, and the pair's MMAs waited (54 % tensor-pipe cycles).
 //
-// Roles (512 threads): warps 0-7 unpack, four to each half of a step; warps 8-11 write the
-// outputs; warp 12 issues the tiled copies of X; warp 13 owns TMEM and issues the MMAs; warps
-// 14-15 bring the packed words, 128 rows x 128 codes (a step) at a time, through a ring of their
-// own that runs ahead across tiles. Tiles of at most 128 rows use two accumulators in turn, so a
+// Roles (640 threads): warps 0-11 unpack, in three sets of four that take the halves of the steps
+// in turn (integer operations issue every other clock, so two warps a scheduler spent most of a
+// step in one another's latencies; three do not); warps 12-15 write the outputs; warp 16 issues
+// the tiled copies of X; warp 17 owns TMEM and issues the MMAs; warps 18-19 bring the packed words,
+// 128 rows x 128 codes (a step) at a time, through a ring of their own that runs ahead across tiles. Tiles of at most 128 rows use two accumulators in turn, so a
 // tile's end costs the next one nothing.
 #pragma once
 
@@ -46,13 +47,16 @@ namespace gptq {
 
 constexpr int MM_LANES = 128;                       // output channels of a block's tile
 constexpr int MM_BK = 128;
-constexpr int MM_THREADS = 512;
+constexpr int MM_THREADS = 640;
+constexpr int MM_SETS = 3;
 constexpr int MM_ROWS = 128;                        // rows of X that a block stages (a pair: 256)
 constexpr int MM_HALF = MM_ROWS * 64 * 2;           // 64 columns of them, 16 KB
 constexpr int MM_B_BYTES = 2 * MM_HALF;
 constexpr int MM_A_BYTES = MM_LANES * MM_BK * 2;    // 32 KB (input gradient)
 constexpr int MM_BOX = 128 * 64 * 2;                // A: 128 contraction rows x 64 columns
-constexpr int MM_TABLE = (MATMUL_MAX_EXPERTS + 4 + 256) * 4;    // and the adapters of a tile's rows
+constexpr int MM_CACHED = 256;                       // offsets kept in shared memory
+// tiles before each range, the first offsets, and the adapters of a tile's rows (16 bits)
+constexpr int MM_TABLE = (MATMUL_MAX_EXPERTS + 4 + MM_CACHED + 4) * 4 + 256 * 2;
 constexpr uint32_t MM_TMEM = 512;
 constexpr int MM_MAX_STAGES = 4;                    // of 64 TMEM columns beside the accumulators
 
@@ -67,7 +71,7 @@ struct MmRing {
     static constexpr int WORDS = STAGES * STAGE;
     // two scales a thread and step, SCALES - 1 steps ahead
     static constexpr int SCALES = DIR == 1 ? 2 : 4;
-    static constexpr int BYTES = WORDS + SCALES * 256 * 8;
+    static constexpr int BYTES = WORDS + SCALES * MM_SETS * 128 * 8;
     // byte offset of 16-byte (3 bits: 8-byte) piece q of row r
     static __device__ __forceinline__ int at(int r, int q) {
         return B == 2   ? r * 32 + ((q ^ ((r >> 2) & 1)) << 4)
@@ -154,11 +158,14 @@ __device__ __forceinline__ MmTile mm_tile(const MmTcArg &p, const int *table, in
         else hi = mid - 1;
     }
     t.e = lo;
-    int64_t begin = 0, end = p.m.M;
-    if (p.m.offsets) {
-        const bool one = p.m.lora.R > 0;            // with adapters the requests are one range
-        begin = __ldg(p.m.offsets + (one ? 0 : lo));
-        end = __ldg(p.m.offsets + (one ? p.m.lora.R : lo + 1));
+    const int *cached = table + MATMUL_MAX_EXPERTS + 4;
+    int64_t begin, end;
+    if (lo < MM_CACHED) {
+        begin = cached[lo];
+        end = cached[lo + 1];
+    } else {
+        begin = __ldg(p.m.offsets + lo);
+        end = __ldg(p.m.offsets + lo + 1);
     }
     const int cnt = (int)(end - begin);
     const int nt = (cnt + p.cols - 1) / p.cols;
@@ -175,6 +182,11 @@ __device__ __forceinline__ MmTile mm_tile(const MmTcArg &p, const int *table, in
 struct RingPos {
     int stage;
     uint32_t phase;
+    __device__ __forceinline__ void jump(int n, int stages) {
+        const int s = stage + n, w = s / stages;
+        stage = s - w * stages;
+        phase ^= w & 1;
+    }
     __device__ __forceinline__ void advance(int stages) {
         if (++stage == stages) {
             stage = 0;
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         if (tiled) tc::prefetch_tmap(&xmap);
         if (p.wtiled) tc::prefetch_tmap(&wmap);
     }
-    if (warp == 13) {
+    if (warp == 17) {
         if constexpr (PAIR) tc::tmem_alloc_pair(tmem_slot, MM_TMEM);
         else tc::tmem_alloc(tmem_slot, MM_TMEM);
     }
@@ -280,6 +292,12 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             base += __shfl_sync(~0u, sum, 31);
         }
         if (lane == 0) table[p.E] = base;
+        // with adapters the requests are one range; without offsets all rows are
+        int *cached = table + MATMUL_MAX_EXPERTS + 4;
+        for (int i = lane; i <= min(p.E, MM_CACHED); i += 32)
+            cached[i] = !m.offsets         ? (i ? (int)m.M : 0)
+                        : m.lora.R > 0 ? __ldg(m.offsets + (i ? m.lora.R : 0))
+                                       : __ldg(m.offsets + i);
     }
     __syncthreads();
     if (cluster > 1) tc::cluster_sync();    // every block's barriers and refusal are in place
@@ -307,23 +325,27 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         else tc::mbar_arrive(&full[stage]);
     };
 
-    if (warp < 8) {
-        const int set = warp >> 2, wq = warp & 3, tid = threadIdx.x;
-        // forward: channel = lane of the warp's TMEM quarter, half `set` of the step's columns.
-        // Input gradient: row n of the step and half of the block's 128 columns.
-        const int arow = (wq & 1) * 32 + lane + set * 64, ahalf = wq >> 1;
+    if (warp < 4 * MM_SETS) {
+        const int set = warp >> 2, wq = warp & 3, tid = threadIdx.x, stid = tid & 127;
+        // forward: channel = lane of the warp's TMEM quarter, 64 of the step's columns. Input gradient:
+        // one of 64 rows n of the step and half of the block's 128 columns.
+        const int arow64 = (wq & 1) * 32 + lane, ahalf = wq >> 1;
         const uint32_t scale0 = tc::smem_u32(words) + Ring::WORDS + tid * 8;
-        // the row and first 16-byte (8-byte) piece of a words' stage that this thread unpacks
-        const int wrow = DIR == 0 ? wq * 32 + lane : arow;
-        const int wpiece = (DIR == 0 ? set : ahalf) * (B == 3 ? 3 : B / 2);
-
         // Scales where they fold into the weights: this thread's next step to request, ahead of the
         // unpacking and across tiles.
         const bool scaled = !IDX && p.fold;
-        int fu = group, fi = 0, fslot = 0;
+        // (halves of a tile's steps: h with (h + turn) % 3 == set, turn moving on with each tile)
+        auto first_half = [&](int turn) { return (set - turn + MM_SETS) % MM_SETS; };
+        const int turns = 2 * nmain % MM_SETS;
+        int fu = group, fturn = 0, fh = first_half(0), fslot = 0;
         int64_t ferow = 0;
         int fc0 = 0;
         auto fetch_tile = [&]() {
+            while (fu < tiles && fh >= 2 * nmain) {
+                fu += ngroups;
+                fturn = (fturn + turns) % MM_SETS;
+                fh = first_half(fturn);
+            }
             if (fu >= tiles) return;
             const MmTile t = mm_tile(p, table, tiles_out, fu, WIDTH, first, GRAIN);
             ferow = (int64_t)t.e * m.w.N;
@@ -331,19 +353,16 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         };
         auto fetch = [&]() {
             if (fu < tiles) {
-                const int n = DIR == 0 ? fc0 + wq * 32 + lane : (k0 + fi) * MM_BK + arow;
-                const int k = DIR == 0 ? (k0 + fi) * MM_BK + set * 64 : fc0 + ahalf * 64;
+                const int n = DIR == 0 ? fc0 + wq * 32 + lane : (2 * k0 + fh) * 64 + arow64;
+                const int k = DIR == 0 ? (2 * k0 + fh) * 64 : fc0 + ahalf * 64;
                 const float *row = m.w.scales + (ferow + n) * (m.w.groups ? m.w.groups : 1);
                 const int g0 = m.w.groups ? k >> m.w.gshift : 0;
                 const int g1 = m.w.groups ? (k + 32) >> m.w.gshift : 0;
-                const uint32_t dst = scale0 + fslot * 256 * 8;
+                const uint32_t dst = scale0 + fslot * MM_SETS * 128 * 8;
                 copy_async<4>(dst, n < m.w.N && k < m.w.K ? row + g0 : nullptr, m.w.scales);
                 if (m.w.gshift == 5) copy_async<4>(dst + 4, n < m.w.N && k + 32 < m.w.K ? row + g1 : nullptr, m.w.scales);
-                if (++fi == nmain) {
-                    fi = 0;
-                    fu += ngroups;
-                    fetch_tile();
-                }
+                fh += MM_SETS;
+                if (fh >= 2 * nmain) fetch_tile();
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             if (++fslot == Ring::SCALES) fslot = 0;
@@ -353,24 +372,34 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
 #pragma unroll 1
             for (int d = 0; d < Ring::SCALES - 1; ++d) fetch();
         }
-        int wstage = 0, slot = 0;
-        uint32_t wphase = 0;
-        RingPos pos{0, 0};
+        int slot = 0, turn = 0;
+        RingPos wbase{0, 0}, base{0, 0};            // ring places of the tile's first step
         for (int u = group; u < tiles; u += ngroups) {
             const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
             const int64_t erow = (int64_t)t.e * m.w.N;
             const int ch = t.c0 + wq * 32 + lane;       // forward: this thread's channel
+            RingPos wpos = wbase, pos = base;
+            int at = 0;                                 // the step that wpos and pos stand at
 #pragma unroll 1
-            for (int i = 0; i < nmain; ++i) {
-                const int step = k0 + i;
+            for (int h = first_half(turn); h < 2 * nmain; h += MM_SETS) {
+                const int side = h & 1;                 // which half of the step
+                for (; at < (h >> 1); ++at) {
+                    wpos.advance(Ring::STAGES);
+                    pos.advance(stages);
+                }
+                const int step = k0 + at;
+                const int arow = side * 64 + arow64;
                 if (scaled) {
                     fetch();
                     asm volatile("cp.async.wait_group %0;" ::"n"(Ring::SCALES - 1) : "memory");
                 }
                 uint32_t raw[2][B];
-                bool ok = tc::mbar_wait(&wfull[wstage], wphase, abort);
+                bool ok = tc::mbar_wait(&wfull[wpos.stage], wpos.phase, abort);
                 {
-                    const uint8_t *src = words + wstage * Ring::STAGE;
+                    const uint8_t *src = words + wpos.stage * Ring::STAGE;
+                    // the row and first 16-byte (8-byte) piece that this thread unpacks
+                    const int wrow = DIR == 0 ? wq * 32 + lane : arow;
+                    const int wpiece = (DIR == 0 ? side : ahalf) * (B == 3 ? 3 : B / 2);
                     if constexpr (B == 3) {
 #pragma unroll
                         for (int q = 0; q < 3; ++q) {
@@ -389,29 +418,28 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&wempty[wstage]);
-                if (++wstage == Ring::STAGES) { wstage = 0; wphase ^= 1; }
+                if (lane == 0) tc::mbar_arrive(&wempty[wpos.stage]);
                 float sc[2] = {1.f, 1.f};
                 if (scaled) {
                     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
                                  : "=f"(sc[0]), "=f"(sc[1])
-                                 : "r"(scale0 + slot * 256 * 8));
+                                 : "r"(scale0 + slot * MM_SETS * 128 * 8));
                     if (m.w.gshift != 5) sc[1] = sc[0];
                     if (++slot == Ring::SCALES) slot = 0;
                 }
                 uint32_t v[2][16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    unpack32<B, T>(raw[h], v[h]);
+                for (int q = 0; q < 2; ++q) {
+                    unpack32<B, T>(raw[q], v[q]);
                     if constexpr (IDX) {
                         const int n = DIR == 0 ? ch : step * MM_BK + arow;
-                        const int c = DIR == 0 ? step * MM_BK + set * 64 + 32 * h : t.c0 + ahalf * 64 + 32 * h;
+                        const int c = DIR == 0 ? step * MM_BK + side * 64 + 32 * q : t.c0 + ahalf * 64 + 32 * q;
                         if (n < m.w.N && c < m.w.K)
-                            scale32_by_index<T, B, true>(v[h], m.w.scales + (erow + n) * m.w.groups,
+                            scale32_by_index<T, B, true>(v[q], m.w.scales + (erow + n) * m.w.groups,
                                                          m.w.g_idx + (int64_t)t.e * m.w.K, c, m.w.K, m.w.groups,
                                                          m.status);
                     } else {
-                        if (p.fold) scale32<T>(v[h], sc[h]);
+                        if (p.fold) scale32<T>(v[q], sc[q]);
                     }
                 }
                 ok = tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort) && ok;
@@ -424,7 +452,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         uint32_t r[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[j] = v[j >> 4][j & 15];
-                        tc::tmem_st_32x32b_x32(tmem + 256 + pos.stage * 64 + set * 32 + ((uint32_t)(wq * 32) << 16), r);
+                        tc::tmem_st_32x32b_x32(tmem + 256 + pos.stage * 64 + side * 32 + ((uint32_t)(wq * 32) << 16), r);
                         tc::tmem_st_wait();
                     } else {
                         uint8_t *a = st + MM_B_BYTES + ahalf * MM_BOX + arow * 128;
@@ -439,17 +467,20 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     }
                     if (!tiled) {
                         const int rows = PAIR ? t.n16 / 2 : t.n16;
-                        plain_box<T>(st + set * MM_HALF, X, m.ldx, t.t0 + (PAIR ? (int)rank * rows : 0), rows, t.t0 + t.n,
-                                     step * MM_BK + set * 64, p.inner, tid & 127, 128);
+                        plain_box<T>(st + side * MM_HALF, X, m.ldx, t.t0 + (PAIR ? (int)rank * rows : 0), rows, t.t0 + t.n,
+                                     step * MM_BK + side * 64, p.inner, stid, 128);
                     }
                     if (DIR == 1 || !tiled) tc::fence_async_shared();
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) arrive_full(pos.stage);
                 }
-                pos.advance(stages);
             }
+            turn = (turn + turns) % MM_SETS;
+            wbase.jump(nmain, Ring::STAGES);
+            base.jump(nmain, stages);
             if (adapters) {
+                int half = 0;                           // halves of the adapters' steps, in turn too
                 const T *P = static_cast<const T *>(m.lora.P);
                 const T *T2 = static_cast<const T *>(m.lora.T2);
                 const int r = m.lora.rank;
@@ -458,12 +489,17 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     const int b0 = (run.begin - (int)t.t0) & -GRAIN, b1 = ((run.end - (int)t.t0) + GRAIN - 1) & -GRAIN;
                     const int rows = PAIR ? (b1 - b0) / 2 : b1 - b0;
                     const int row0 = b0 + (PAIR ? (int)rank * rows : 0);
-                    for (int rs = 0; rs < rsteps; ++rs) {
+                    for (int hs = 0; hs < 2 * rsteps; ++hs, ++half) {
+                        const int side = hs & 1, rs = hs >> 1;
+                        RingPos pos = base;
+                        if (side) base.advance(stages);
+                        if (half % MM_SETS != set) continue;
+                        const int arow = side * 64 + arow64;
                         // this thread's part of A, requested before the stage is free. Forward: row n
                         // of B_a twice over, [hi part | lo part] of the contraction; input gradient:
                         // rows of A_a, twice over too
                         uint4 y[8];
-                        const int qa = rs * MM_BK + (DIR == 0 ? set * 64 : arow);
+                        const int qa = rs * MM_BK + (DIR == 0 ? side * 64 : arow);
                         if constexpr (DIR == 0) {
                             const T *src = P + ((int64_t)run.id * m.w.N + ch) * r;
 #pragma unroll
@@ -490,7 +526,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                                     z[4 * j] = y[j].x; z[4 * j + 1] = y[j].y; z[4 * j + 2] = y[j].z; z[4 * j + 3] = y[j].w;
                                 }
                                 tc::fence_after_sync();
-                                tc::tmem_st_32x32b_x32(tmem + 256 + pos.stage * 64 + set * 32 +
+                                tc::tmem_st_32x32b_x32(tmem + 256 + pos.stage * 64 + side * 32 +
                                                            ((uint32_t)(wq * 32) << 16), z);
                                 tc::tmem_st_wait();
                             } else {
@@ -500,28 +536,27 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                                     *reinterpret_cast<uint4 *>(a + ((j ^ (arow & 7)) << 4)) = y[j];
                             }
                             // the run's rows of [hi | lo], zeros for rows of others
-                            for (int j = tid; j < rows * 16; j += 256) {
-                                const int row = j >> 4, q = j & 15, col = rs * MM_BK + 8 * q;
+                            for (int j = stid; j < rows * 8; j += 128) {
+                                const int row = j >> 3, q = j & 7, col = rs * MM_BK + side * 64 + 8 * q;
                                 const int64_t tr = t.t0 + row0 + row;
                                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
                                 if (tr >= run.begin && tr < run.end && col < two_r)
                                     x = __ldg(reinterpret_cast<const uint4 *>(T2 + tr * two_r + col));
-                                *reinterpret_cast<uint4 *>(st + (q >> 3) * MM_HALF + row * 128 + (((q & 7) ^ (row & 7)) << 4)) = x;
+                                *reinterpret_cast<uint4 *>(st + side * MM_HALF + row * 128 + ((q ^ (row & 7)) << 4)) = x;
                             }
                             tc::fence_async_shared();
                             tc::fence_before_sync();
                             __syncwarp();
                             if (lane == 0) arrive_full(pos.stage);
                         }
-                        pos.advance(stages);
                     }
                 }
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // outputs: lane = channel, register = row
-        const int wq = warp & 3, etid = threadIdx.x - 256;
+        const int wq = warp & 3, etid = threadIdx.x - 384;
         int acc = 0;
         uint32_t acc_phase = 0, sum_phase = 0;
         T *Y = static_cast<T *>(m.Y);
@@ -530,18 +565,18 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             const int ch = t.c0 + wq * 32 + lane;
             const bool per_channel = DIR == 0 && !p.fold;
             const float s = per_channel && ch < p.out ? __ldg(m.w.scales + (int64_t)t.e * m.w.N + ch) : 1.f;
-            // adapters of the rows in short runs (-1: none), found while the products run
+            // adapters of the rows in short runs (0xffff: none), found while the products run
             bool shorts = false;
-            int *row_ids = table + MATMUL_MAX_EXPERTS + 4;
+            uint16_t *row_ids = reinterpret_cast<uint16_t *>(table + MATMUL_MAX_EXPERTS + 4 + MM_CACHED + 4);
             if (m.lora.R > 0) {
                 asm volatile("bar.sync 1, 128;" ::: "memory");      // the tile before is done with them
-                for (int r = etid; r < t.n; r += 128) row_ids[r] = -1;
+                for (int r = etid; r < t.n; r += 128) row_ids[r] = 0xffff;
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 RunWalk run(m.offsets, m.lora.ids, m.lora.R, (int)t.t0, (int)t.t0 + t.n, true);
                 while (run.next()) {
                     shorts = true;
-                    if (warp == 8)
-                        for (int r = run.begin + lane; r < run.end; r += 32) row_ids[r - (int)t.t0] = run.id;
+                    if (warp == 12)
+                        for (int r = run.begin + lane; r < run.end; r += 32) row_ids[r - (int)t.t0] = (uint16_t)run.id;
                 }
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
@@ -562,7 +597,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     // their terms into the accumulators
                     for (int r = 0; r < t.n; ++r) {
                         const int id = row_ids[r];
-                        if (id < 0) continue;
+                        if (id == 0xffff) continue;
                         const float add = ch < p.out ? lora_term<T, DIR>(m.lora, id, t.t0 + r, ch, p.out) : 0.f;
                         const uint32_t y = tc::tmem_ld_32x32b_x1(at + r);
                         tc::tmem_ld_wait();
@@ -637,7 +672,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
 #pragma unroll 2
                     for (int row = (int)rank; row < t.n; row += split) {
                         float sum = 0.f;
-                        if (shorts && row_ids[row] >= 0 && ch < p.out)
+                        if (shorts && row_ids[row] != 0xffff && ch < p.out)
                             sum = lora_term<T, DIR>(m.lora, row_ids[row], t.t0 + row, ch, p.out);
                         const uint32_t from = tc::smem_u32(dump + row * MM_LANES + wq * 32 + lane);
                         for (int c = 0; c < split; ++c)
@@ -652,7 +687,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             }
             if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
         }
-    } else if (warp == 12) {
+    } else if (warp == 16) {
         // the whole warp walks, one elected lane issues (as for the MMAs below)
         if (tiled) {
             RingPos pos{0, 0};
@@ -706,14 +741,14 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
             }
         }
-    } else if (warp >= 14) {
+    } else if (warp >= 18) {
         // a stage: the block's channels x a step's columns (forward), or a step's rows x the block's
         // columns
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         if (p.wtiled) {
-            if (warp == 14) {
+            if (warp == 18) {
                 for (int u = group; u < tiles && ok; u += ngroups) {
                     const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
                     const int erow = t.e * m.w.N;
@@ -738,7 +773,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
             }
         } else {
-            const int tid = threadIdx.x - 448;
+            const int tid = threadIdx.x - 576;
             const int nw = (int)(((int64_t)m.w.K * B + 31) / 32);
             for (int u = group; u < tiles && ok; u += ngroups) {
                 const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
@@ -851,7 +886,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     __syncthreads();
     if (cluster > 1) tc::cluster_sync();    // no block leaves while others use its memory
     if (*abort && threadIdx.x == 0) set_status(m.status, GPTQ_ERR_TIMEOUT);
-    if (warp == 13) {
+    if (warp == 17) {
         tc::fence_after_sync();
         if constexpr (PAIR) tc::tmem_dealloc_pair(tmem, MM_TMEM);
         else tc::tmem_dealloc(tmem, MM_TMEM);

@@ -43,7 +43,7 @@ def packed(**kw):
 
 
 BAD_LAYERS = [dict(words=None), dict(scales=None), dict(words=FAKE + 2), dict(bits=5), dict(N=0), dict(K=0),
-              dict(N=65536), dict(K=65536, ld_words=1 << 20), dict(experts=0), dict(experts=1025), dict(groupsize=16),
+              dict(N=65536), dict(K=65536, ld_words=1 << 20), dict(experts=0), dict(experts=513), dict(groupsize=16),
               dict(ld_words=7), dict(g_idx=FAKE), dict(g_idx=FAKE + 1, groupsize=32), dict(experts=2)]
 
 
@@ -70,7 +70,7 @@ def test_row_checks(lib):
     assert lib.gptq_matmul_grouped(None, 0, None, 0, 0, 0, w, None, None, None) == gq.GPTQ_OK     # no rows
     dw = lib.gptq_matmul_grouped_dw
     ok = [f, f, 16, f, 64, 0, 4, 16, 64, 1, None, 0, None, None]
-    for at, v in ((0, None), (1, None), (2, 15), (4, 63), (5, 1), (6, -1), (7, 0), (8, 65536), (9, 0), (9, 1025), (9, 2),
+    for at, v in ((0, None), (1, None), (2, 15), (4, 63), (5, 1), (6, -1), (7, 0), (8, 65536), (9, 0), (9, 513), (9, 2),
                   (11, 2), (10, P(FAKE + 1)), (0, P(FAKE + 2))):
         args = list(ok)
         args[at] = v
