@@ -333,85 +333,55 @@ __device__ __forceinline__ int request_of(const int32_t *off, int R, int t) {
     return lo;
 }
 
-// Runs shorter than this are added by the outputs' threads, row by row; longer ones are matrix
-// operands of their own (an MMA takes 16 columns at least, and a round of barriers).
+// A run is neighbouring rows of one adapter inside a tile. Runs shorter than this are added by the
+// outputs' threads, row by row; longer ones are matrix operands of their own (an MMA takes 16
+// columns at least, and a round of barriers).
 constexpr int LORA_SHORT = 16;
 
-// Walks the rows [t0, t1) in runs of one adapter: neighbouring requests with the same adapter
-// make one run; rows without an adapter are skipped, and runs of the other kind (shorter or not
-// shorter than LORA_SHORT inside [t0, t1)).
-struct RunWalk {
-    const int32_t *off, *ids;
-    int R, t1, s, t;
-    int begin, end, id;       // the current run: rows [begin, end), its adapter
-    bool shorts;
-    __device__ __forceinline__ RunWalk(const int32_t *off_, const int32_t *ids_, int R_, int t0,
-                                       int t1_, bool shorts_ = false)
-        : off(off_), ids(ids_), R(R_), t1(t1_), s(request_of(off_, R_, t0)), t(t0), shorts(shorts_) {}
-    __device__ __forceinline__ bool next() {
-        while (s < R && t < t1) {
-            const int e = min(__ldg(off + s + 1), t1);
-            const int a = __ldg(ids + s);
-            if (e <= t) { ++s; continue; }
-            begin = t;
-            end = e;
-            id = a;
-            t = e;
-            ++s;
-            while (s < R && t < t1 && (__ldg(ids + s) == a || __ldg(off + s + 1) <= t)) {
-                end = max(end, min(__ldg(off + s + 1), t1));
-                t = end;
-                ++s;
-            }
-            if (a >= 0 && (end - begin < LORA_SHORT) == shorts) return true;
-        }
-        return false;
-    }
-};
-
-// One row's adapter term of one output channel: sum_j P_a[ch][j] T[t][j] (forward, P = B) or
-// sum_j P_a[j][ch] T[t][j] (input gradient, P = A), fp32.
-template <typename T, int DIR>
-__device__ __forceinline__ float lora_term(const LoraArg &l, int id, int64_t t, int ch, int channels) {
+// The adapter terms of one output channel for NROW rows t[i] with adapters id[i] (negative:
+// zero): sum_j P_a[ch][j] T[t][j] (forward, P = B) or sum_j P_a[j][ch] T[t][j] (input gradient,
+// P = A), fp32. The rows' reads are independent, so they overlap.
+template <typename T, int DIR, int NROW>
+__device__ __forceinline__ void lora_terms(const LoraArg &l, const int (&id)[NROW], const int64_t (&t)[NROW], int ch,
+                                           int channels, float (&add)[NROW]) {
     const int r = l.rank;
-    const T *h = static_cast<const T *>(l.T2) + t * 2 * r;
-    float add = 0.f;
-    if constexpr (DIR == 0) {
-        const T *b = static_cast<const T *>(l.P) + ((int64_t)id * channels + ch) * r;
-#pragma unroll 2
-        for (int j = 0; j < r; j += 8) {
-            const uint4 bv = __ldg(reinterpret_cast<const uint4 *>(b + j));
-            const uint4 hv = __ldg(reinterpret_cast<const uint4 *>(h + j));
-            const uint4 lv = __ldg(reinterpret_cast<const uint4 *>(h + r + j));
-            const uint32_t bb[4] = {bv.x, bv.y, bv.z, bv.w}, hh[4] = {hv.x, hv.y, hv.z, hv.w},
-                           ll[4] = {lv.x, lv.y, lv.z, lv.w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 fb = Half2<T>::unpack(bb[q]), fh = Half2<T>::unpack(hh[q]),
-                             fl = Half2<T>::unpack(ll[q]);
-                add = fmaf(fb.x, fh.x + fl.x, add);
-                add = fmaf(fb.y, fh.y + fl.y, add);
+    for (int i = 0; i < NROW; ++i) add[i] = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < r; j += 8) {
+        uint4 hv[NROW], lv[NROW], pv[NROW];
+#pragma unroll
+        for (int i = 0; i < NROW; ++i) {
+            hv[i] = lv[i] = pv[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (id[i] < 0) continue;
+            const T *h = static_cast<const T *>(l.T2) + t[i] * 2 * r + j;
+            hv[i] = __ldcg(reinterpret_cast<const uint4 *>(h));
+            lv[i] = __ldcg(reinterpret_cast<const uint4 *>(h + r));
+            if constexpr (DIR == 0) {
+                pv[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(l.P) +
+                                                              ((int64_t)id[i] * channels + ch) * r + j));
+            } else {
+                const unsigned short *a = reinterpret_cast<const unsigned short *>(l.P) +
+                                          ((int64_t)id[i] * r + j) * channels + ch;
+                uint32_t w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    w[q] = __ldg(a + (int64_t)(2 * q) * channels) | ((uint32_t)__ldg(a + (int64_t)(2 * q + 1) * channels) << 16);
+                pv[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-    } else {
-        const unsigned short *a = reinterpret_cast<const unsigned short *>(l.P) + (int64_t)id * r * channels + ch;
-#pragma unroll 2
-        for (int j = 0; j < r; j += 8) {
-            const uint4 hv = __ldg(reinterpret_cast<const uint4 *>(h + j));
-            const uint4 lv = __ldg(reinterpret_cast<const uint4 *>(h + r + j));
-            const uint32_t hh[4] = {hv.x, hv.y, hv.z, hv.w}, ll[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+        for (int i = 0; i < NROW; ++i) {
+            const uint32_t pp[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w}, hh[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w},
+                           ll[4] = {lv[i].x, lv[i].y, lv[i].z, lv[i].w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float2 fh = Half2<T>::unpack(hh[q]), fl = Half2<T>::unpack(ll[q]);
-                const uint32_t w = __ldg(a + (int64_t)(j + 2 * q) * channels) |
-                                   ((uint32_t)__ldg(a + (int64_t)(j + 2 * q + 1) * channels) << 16);
-                const float2 fa = Half2<T>::unpack(w);
-                add = fmaf(fa.x, fh.x + fl.x, add);
-                add = fmaf(fa.y, fh.y + fl.y, add);
+                const float2 fp = Half2<T>::unpack(pp[q]), fh = Half2<T>::unpack(hh[q]), fl = Half2<T>::unpack(ll[q]);
+                add[i] = fmaf(fp.x, fh.x + fl.x, add[i]);
+                add[i] = fmaf(fp.y, fh.y + fl.y, add[i]);
             }
         }
     }
-    return add;
 }
 
 // ---- host ----------------------------------------------------------------------------------
@@ -490,9 +460,11 @@ inline gptq_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, 
 }
 
 // Wait for the previous kernel of the stream, then let the next one set up.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void grid_dependency() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
+    grid_wait();
+    grid_release();
 }
 
 }  // namespace gptq

@@ -47,16 +47,25 @@ namespace gptq {
 
 constexpr int MM_LANES = 128;                       // output channels of a block's tile
 constexpr int MM_BK = 128;
-constexpr int MM_THREADS = 640;
-constexpr int MM_SETS = 3;
+constexpr int MM_SETS = 3;                          // of four unpacking warps
+constexpr int MM_WARP_OUT = 4 * MM_SETS, MM_WARP_X = MM_WARP_OUT + 4, MM_WARP_MMA = MM_WARP_X + 1,
+              MM_WARP_WORDS = MM_WARP_X + 2;
+constexpr int MM_THREADS = (MM_WARP_WORDS + 2) * 32;
 constexpr int MM_ROWS = 128;                        // rows of X that a block stages (a pair: 256)
 constexpr int MM_HALF = MM_ROWS * 64 * 2;           // 64 columns of them, 16 KB
 constexpr int MM_B_BYTES = 2 * MM_HALF;
 constexpr int MM_A_BYTES = MM_LANES * MM_BK * 2;    // 32 KB (input gradient)
 constexpr int MM_BOX = 128 * 64 * 2;                // A: 128 contraction rows x 64 columns
+// The runs of one adapter in a tile that are matrix operands, found by the outputs' warps for all.
+struct LoraRuns {
+    int count;
+    int begin[256 / LORA_SHORT], end[256 / LORA_SHORT], id[256 / LORA_SHORT];   // rows of the tile
+    uint32_t starts[8], longs[8];       // a bit a row: a run starts, a long one
+};
+
 constexpr int MM_CACHED = 256;                       // offsets kept in shared memory
 // tiles before each range, the first offsets, and the adapters of a tile's rows (16 bits)
-constexpr int MM_TABLE = (MATMUL_MAX_EXPERTS + 4 + MM_CACHED + 4) * 4 + 256 * 2;
+constexpr int MM_TABLE = ((MATMUL_MAX_EXPERTS + 4 + MM_CACHED + 4) * 4 + 256 * 2 + (int)sizeof(LoraRuns) + 15) / 16 * 16;
 constexpr uint32_t MM_TMEM = 512;
 constexpr int MM_MAX_STAGES = 4;                    // of 64 TMEM columns beside the accumulators
 
@@ -69,9 +78,7 @@ struct MmRing {
     // the input gradient's operand stages leave less room
     static constexpr int STAGES = DIR == 1 ? (B == 2 ? 3 : 2) : B == 8 ? 3 : B == 4 ? 6 : B == 3 ? 7 : 8;
     static constexpr int WORDS = STAGES * STAGE;
-    // two scales a thread and step, SCALES - 1 steps ahead
-    static constexpr int SCALES = DIR == 1 ? 2 : 4;
-    static constexpr int BYTES = WORDS + SCALES * MM_SETS * 128 * 8;
+    static constexpr int BYTES = WORDS;
     // byte offset of 16-byte (3 bits: 8-byte) piece q of row r
     static __device__ __forceinline__ int at(int r, int q) {
         return B == 2   ? r * 32 + ((q ^ ((r >> 2) & 1)) << 4)
@@ -215,7 +222,9 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     uint64_t *done = ready + 1;
     uint64_t *wfull = done + 1;
     uint64_t *wempty = wfull + Ring::STAGES;
-    uint64_t *drain = wempty + Ring::STAGES;
+    uint64_t *lfull = wempty + Ring::STAGES;                    // the tile's run list
+    uint64_t *lempty = lfull + 1;
+    uint64_t *drain = lempty + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *refuse = reinterpret_cast<int *>(tmem_slot + 2);
@@ -244,6 +253,9 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             tc::mbar_init(&wfull[s], p.wtiled ? 1 : 64);
             tc::mbar_init(&wempty[s], 8);
         }
+        tc::mbar_init(lfull, 4);
+        // its readers: the unpacking warps, the X warp where it copies, the MMA warp where it issues
+        tc::mbar_init(lempty, MM_WARP_OUT + (tiled ? 1 : 0) + (!PAIR || rank == 0 ? 1 : 0));
         tc::mbar_init(drain, 1);
         *abort = 0;
         *refuse = 0;
@@ -251,7 +263,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         if (tiled) tc::prefetch_tmap(&xmap);
         if (p.wtiled) tc::prefetch_tmap(&wmap);
     }
-    if (warp == 17) {
+    if (warp == MM_WARP_MMA) {
         if constexpr (PAIR) tc::tmem_alloc_pair(tmem_slot, MM_TMEM);
         else tc::tmem_alloc(tmem_slot, MM_TMEM);
     }
@@ -259,28 +271,43 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    grid_dependency();
+    // With adapters the kernel before this one makes T or follows the one that does; all else that
+    // is read was there before it began, so only T waits for it.
+    if (m.lora.R == 0) grid_wait();
+    grid_release();
 
-    // the ranges: refused as a whole when they are not ordered inside [0, M]
-    bool bad = false;
+    // the ranges: refused as a whole when they are not ordered inside [0, M]. With adapters the
+    // requests are one range; without offsets all rows are.
+    int *cached = table + MATMUL_MAX_EXPERTS + 4;
     const int nranges = m.lora.R > 0 ? m.lora.R : p.E;
-    if (m.offsets) bad = offsets_bad(m.offsets, nranges, m.M, threadIdx.x, MM_THREADS);
+    bool bad = false;
+    if (threadIdx.x == MM_THREADS - 1 && failed(m.status)) *refuse = 2;
+    if (m.offsets) {
+        for (int i = threadIdx.x; i <= nranges; i += MM_THREADS) {
+            const int v = __ldg(m.offsets + i);
+            bad |= v < 0 || (int64_t)v > m.M || (i > 0 && v < __ldg(m.offsets + i - 1));
+            if (m.lora.R > 0) {
+                if (i == 0) cached[0] = v;
+                if (i == nranges) cached[1] = v;
+            } else if (i <= MM_CACHED) {
+                cached[i] = v;
+            }
+        }
+    } else if (threadIdx.x < 2) {
+        cached[threadIdx.x] = threadIdx.x ? (int)m.M : 0;
+    }
     if (m.lora.R > 0) bad |= ids_bad(m.lora.ids, m.lora.R, m.lora.L, threadIdx.x, MM_THREADS);
-    if (bad) *refuse = 1;
-    __syncthreads();
-    if (threadIdx.x == 0 && *refuse == 0 && failed(m.status)) *refuse = 2;
-    __syncthreads();
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0 && bad) *refuse = 1;
     if (warp == 0) {
         // table[e]: tiles of rows before range e
         int base = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
             int nt = 0;
-            if (e < p.E && *refuse != 1) {
-                int64_t cnt = m.M;
-                if (m.lora.R > 0) cnt = __ldg(m.offsets + m.lora.R) - __ldg(m.offsets);
-                else if (m.offsets) cnt = __ldg(m.offsets + e + 1) - __ldg(m.offsets + e);
-                nt = (int)((cnt + p.cols - 1) / p.cols);
+            if (e < p.E && !bad) {
+                const int cnt = e < MM_CACHED ? cached[e + 1] - cached[e] : __ldg(m.offsets + e + 1) - __ldg(m.offsets + e);
+                nt = (cnt + p.cols - 1) / p.cols;
             }
             int sum = nt;
 #pragma unroll
@@ -292,12 +319,6 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             base += __shfl_sync(~0u, sum, 31);
         }
         if (lane == 0) table[p.E] = base;
-        // with adapters the requests are one range; without offsets all rows are
-        int *cached = table + MATMUL_MAX_EXPERTS + 4;
-        for (int i = lane; i <= min(p.E, MM_CACHED); i += 32)
-            cached[i] = !m.offsets         ? (i ? (int)m.M : 0)
-                        : m.lora.R > 0 ? __ldg(m.offsets + (i ? m.lora.R : 0))
-                                       : __ldg(m.offsets + i);
     }
     __syncthreads();
     if (cluster > 1) tc::cluster_sync();    // every block's barriers and refusal are in place
@@ -319,27 +340,36 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     const int two_r = 2 * m.lora.rank;
     const int rsteps = (two_r + MM_BK - 1) / MM_BK;
     const T *X = static_cast<const T *>(m.X);
+    LoraRuns *runs = reinterpret_cast<LoraRuns *>(table + MATMUL_MAX_EXPERTS + 4 + MM_CACHED + 4 + 128);
+    uint32_t lphase = 0;
+    // the tile's run list is there; done with it
+    auto runs_wait = [&]() { return (bool)__all_sync(~0u, tc::mbar_wait(lfull, lphase, abort)); };
+    auto runs_done = [&]() {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(lempty);
+        lphase ^= 1;
+    };
     // the barrier of a stage that the MMA thread waits on (the first block's, in a pair)
     auto arrive_full = [&](int stage) {
         if (PAIR && rank != 0) tc::mbar_arrive_remote(tc::mapa_shared(tc::smem_u32(&full[stage]), 0));
         else tc::mbar_arrive(&full[stage]);
     };
 
-    if (warp < 4 * MM_SETS) {
+    if (warp < MM_WARP_OUT) {
         const int set = warp >> 2, wq = warp & 3, tid = threadIdx.x, stid = tid & 127;
         // forward: channel = lane of the warp's TMEM quarter, 64 of the step's columns. Input gradient:
         // one of 64 rows n of the step and half of the block's 128 columns.
         const int arow64 = (wq & 1) * 32 + lane, ahalf = wq >> 1;
-        const uint32_t scale0 = tc::smem_u32(words) + Ring::WORDS + tid * 8;
-        // Scales where they fold into the weights: this thread's next step to request, ahead of the
-        // unpacking and across tiles.
-        const bool scaled = !IDX && p.fold;
         // (halves of a tile's steps: h with (h + turn) % 3 == set, turn moving on with each tile)
         auto first_half = [&](int turn) { return (set - turn + MM_SETS) % MM_SETS; };
         const int turns = 2 * nmain % MM_SETS;
-        int fu = group, fturn = 0, fh = first_half(0), fslot = 0;
-        int64_t ferow = 0;
-        int fc0 = 0;
+
+        // Scales where they fold into the weights: requested one of this thread's steps ahead of the
+        // unpacking, across tiles.
+        const bool scaled = !IDX && p.fold;
+        int fu = group, fturn = 0, fh = first_half(0), fc0 = 0;
+        const float *frow = nullptr;                // scales of the channel (forward), of the range
+        float ahead[2] = {0.f, 0.f};
         auto fetch_tile = [&]() {
             while (fu < tiles && fh >= 2 * nmain) {
                 fu += ngroups;
@@ -348,31 +378,27 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             }
             if (fu >= tiles) return;
             const MmTile t = mm_tile(p, table, tiles_out, fu, WIDTH, first, GRAIN);
-            ferow = (int64_t)t.e * m.w.N;
             fc0 = t.c0;
+            const int n = DIR == 0 ? t.c0 + wq * 32 + lane : 0;
+            frow = n < m.w.N ? m.w.scales + ((int64_t)t.e * m.w.N + n) * max(m.w.groups, 1) : nullptr;
         };
         auto fetch = [&]() {
-            if (fu < tiles) {
-                const int n = DIR == 0 ? fc0 + wq * 32 + lane : (2 * k0 + fh) * 64 + arow64;
-                const int k = DIR == 0 ? (2 * k0 + fh) * 64 : fc0 + ahalf * 64;
-                const float *row = m.w.scales + (ferow + n) * (m.w.groups ? m.w.groups : 1);
-                const int g0 = m.w.groups ? k >> m.w.gshift : 0;
-                const int g1 = m.w.groups ? (k + 32) >> m.w.gshift : 0;
-                const uint32_t dst = scale0 + fslot * MM_SETS * 128 * 8;
-                copy_async<4>(dst, n < m.w.N && k < m.w.K ? row + g0 : nullptr, m.w.scales);
-                if (m.w.gshift == 5) copy_async<4>(dst + 4, n < m.w.N && k + 32 < m.w.K ? row + g1 : nullptr, m.w.scales);
-                fh += MM_SETS;
-                if (fh >= 2 * nmain) fetch_tile();
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (++fslot == Ring::SCALES) fslot = 0;
+            if (fu >= tiles) return;
+            const int half = 2 * k0 + fh;           // 64 columns (forward) or rows of the contraction
+            const int n = half * 64 + arow64, k = DIR == 0 ? half * 64 : fc0 + ahalf * 64;
+            const float *row = DIR == 0 ? frow : n < m.w.N ? frow + (int64_t)n * max(m.w.groups, 1) : nullptr;
+            const bool in = row && k < m.w.K, in2 = row && k + 32 < m.w.K;
+            const int g = m.w.groups ? k >> m.w.gshift : 0;
+            ahead[0] = in ? __ldg(row + g) : 0.f;
+            ahead[1] = m.w.gshift == 5 && m.w.groups ? (in2 ? __ldg(row + g + 1) : 0.f) : ahead[0];
+            fh += MM_SETS;
+            if (fh >= 2 * nmain) fetch_tile();
         };
         if (scaled) {
             fetch_tile();
-#pragma unroll 1
-            for (int d = 0; d < Ring::SCALES - 1; ++d) fetch();
+            fetch();
         }
-        int slot = 0, turn = 0;
+        int turn = 0;
         RingPos wbase{0, 0}, base{0, 0};            // ring places of the tile's first step
         for (int u = group; u < tiles; u += ngroups) {
             const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
@@ -389,10 +415,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
                 const int step = k0 + at;
                 const int arow = side * 64 + arow64;
-                if (scaled) {
-                    fetch();
-                    asm volatile("cp.async.wait_group %0;" ::"n"(Ring::SCALES - 1) : "memory");
-                }
+                const float sc[2] = {ahead[0], ahead[1]};
+                if (scaled) fetch();
                 uint32_t raw[2][B];
                 bool ok = tc::mbar_wait(&wfull[wpos.stage], wpos.phase, abort);
                 {
@@ -419,14 +443,6 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&wempty[wpos.stage]);
-                float sc[2] = {1.f, 1.f};
-                if (scaled) {
-                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                                 : "=f"(sc[0]), "=f"(sc[1])
-                                 : "r"(scale0 + slot * MM_SETS * 128 * 8));
-                    if (m.w.gshift != 5) sc[1] = sc[0];
-                    if (++slot == Ring::SCALES) slot = 0;
-                }
                 uint32_t v[2][16];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -480,13 +496,15 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             wbase.jump(nmain, Ring::STAGES);
             base.jump(nmain, stages);
             if (adapters) {
+                grid_wait();
                 int half = 0;                           // halves of the adapters' steps, in turn too
                 const T *P = static_cast<const T *>(m.lora.P);
                 const T *T2 = static_cast<const T *>(m.lora.T2);
                 const int r = m.lora.rank;
-                RunWalk run(m.offsets, m.lora.ids, m.lora.R, (int)t.t0, (int)t.t0 + t.n);
-                while (run.next()) {
-                    const int b0 = (run.begin - (int)t.t0) & -GRAIN, b1 = ((run.end - (int)t.t0) + GRAIN - 1) & -GRAIN;
+                const int count = runs_wait() ? runs->count : 0;
+                for (int run = 0; run < count; ++run) {
+                    const int run_begin = runs->begin[run], run_end = runs->end[run], run_id = runs->id[run];
+                    const int b0 = run_begin & -GRAIN, b1 = (run_end + GRAIN - 1) & -GRAIN;
                     const int rows = PAIR ? (b1 - b0) / 2 : b1 - b0;
                     const int row0 = b0 + (PAIR ? (int)rank * rows : 0);
                     for (int hs = 0; hs < 2 * rsteps; ++hs, ++half) {
@@ -501,7 +519,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         uint4 y[8];
                         const int qa = rs * MM_BK + (DIR == 0 ? side * 64 : arow);
                         if constexpr (DIR == 0) {
-                            const T *src = P + ((int64_t)run.id * m.w.N + ch) * r;
+                            const T *src = P + ((int64_t)run_id * m.w.N + ch) * r;
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const int q = qa + j * 8;
@@ -510,7 +528,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                             }
                         } else {
                             const int c = t.c0 + ahalf * 64;
-                            const T *src = P + ((int64_t)run.id * r + (qa < r ? qa : qa - r)) * m.w.K + c;
+                            const T *src = P + ((int64_t)run_id * r + (qa < r ? qa : qa - r)) * m.w.K + c;
                             const bool v8 = (m.w.K & 7) == 0;
 #pragma unroll
                             for (int j = 0; j < 8; ++j) y[j] = load8<T>(src + 8 * j, qa < two_r ? m.w.K - c - 8 * j : 0, v8);
@@ -538,10 +556,10 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                             // the run's rows of [hi | lo], zeros for rows of others
                             for (int j = stid; j < rows * 8; j += 128) {
                                 const int row = j >> 3, q = j & 7, col = rs * MM_BK + side * 64 + 8 * q;
-                                const int64_t tr = t.t0 + row0 + row;
+                                const int tr = row0 + row;
                                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                                if (tr >= run.begin && tr < run.end && col < two_r)
-                                    x = __ldg(reinterpret_cast<const uint4 *>(T2 + tr * two_r + col));
+                                if (tr >= run_begin && tr < run_end && col < two_r)
+                                    x = __ldcg(reinterpret_cast<const uint4 *>(T2 + (t.t0 + tr) * two_r + col));
                                 *reinterpret_cast<uint4 *>(st + side * MM_HALF + row * 128 + ((q ^ (row & 7)) << 4)) = x;
                             }
                             tc::fence_async_shared();
@@ -551,12 +569,12 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         }
                     }
                 }
+                runs_done();
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp < 16) {
+    } else if (warp < MM_WARP_X) {
         // outputs: lane = channel, register = row
-        const int wq = warp & 3, etid = threadIdx.x - 384;
+        const int wq = warp & 3, etid = threadIdx.x - MM_WARP_OUT * 32;
         int acc = 0;
         uint32_t acc_phase = 0, sum_phase = 0;
         T *Y = static_cast<T *>(m.Y);
@@ -569,18 +587,104 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             bool shorts = false;
             uint16_t *row_ids = reinterpret_cast<uint16_t *>(table + MATMUL_MAX_EXPERTS + 4 + MM_CACHED + 4);
             if (m.lora.R > 0) {
-                asm volatile("bar.sync 1, 128;" ::: "memory");      // the tile before is done with them
-                for (int r = etid; r < t.n; r += 128) row_ids[r] = 0xffff;
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                RunWalk run(m.offsets, m.lora.ids, m.lora.R, (int)t.t0, (int)t.t0 + t.n, true);
-                while (run.next()) {
-                    shorts = true;
-                    if (warp == 12)
-                        for (int r = run.begin + lane; r < run.end; r += 32) row_ids[r - (int)t.t0] = (uint16_t)run.id;
+                grid_wait();
+                // a bit for each row that starts a run, from its request's adapter and its neighbour's
+                bool free = true;
+                if (adapters) free = __all_sync(~0u, tc::mbar_wait(lempty, lphase ^ 1, abort));
+                asm volatile("bar.sync 1, 128;" ::: "memory");      // the tile before is done with row_ids
+                for (int r = etid; r < 256; r += 128) {
+                    int id = -1;
+                    if (r < t.n) id = __ldg(m.lora.ids + request_of(m.offsets, m.lora.R, (int)t.t0 + r));
+                    row_ids[r] = (uint16_t)id;                      // -1 is 0xffff
                 }
                 asm volatile("bar.sync 1, 128;" ::: "memory");
+                for (int r = etid; r < 256; r += 128) {
+                    const unsigned b = __ballot_sync(~0u, r >= t.n || r == 0 || row_ids[r] != row_ids[r - 1]);
+                    if (lane == 0) runs->starts[r >> 5] = b;
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                int id2[2], begin2[2], len2[2];
+                for (int i = 0; i < 2; ++i) {
+                    // this row's run: the last start at or before it, the first behind it
+                    const int r = etid + 128 * i;
+                    int w = r >> 5;
+                    uint32_t v = runs->starts[w] & (0xffffffffu >> (31 - (r & 31)));
+                    while (v == 0u) v = runs->starts[--w];
+                    begin2[i] = w * 32 + 31 - __clz(v);
+                    w = r >> 5;
+                    v = (r & 31) == 31 ? 0u : runs->starts[w] & (0xfffffffeu << (r & 31));
+                    while (v == 0u && w < 7) v = runs->starts[++w];
+                    len2[i] = (v ? w * 32 + __ffs(v) - 1 : 256) - begin2[i];
+                    id2[i] = r < t.n ? row_ids[r] : 0xffff;
+                    const bool some = id2[i] != 0xffff;
+                    const unsigned b = __ballot_sync(~0u, some && len2[i] >= LORA_SHORT && begin2[i] == r);
+                    if (lane == 0) runs->longs[r >> 5] = b;
+                    shorts |= some && len2[i] < LORA_SHORT;
+                }
+                // (a named barrier that also tells whether any thread saw a short run)
+                {
+                    int any;
+                    asm volatile(
+                        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+                        "bar.red.or.pred q, 1, 128, p;\n\t"
+                        "selp.s32 %0, 1, 0, q;\n\t}"
+                        : "=r"(any)
+                        : "r"((int)shorts)
+                        : "memory");
+                    shorts = any != 0;
+                }
+                int before[2] = {0, 0}, count = 0;
+                for (int w = 0; w < 8; ++w) {
+                    const uint32_t v = runs->longs[w];
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = etid + 128 * i;
+                        before[i] += w < (r >> 5) ? __popc(v) : w == (r >> 5) ? __popc(v & ((1u << (r & 31)) - 1u)) : 0;
+                    }
+                    count += __popc(v);
+                }
+                for (int i = 0; i < 2; ++i) {
+                    const int r = etid + 128 * i;
+                    if (id2[i] != 0xffff && len2[i] >= LORA_SHORT) {
+                        if (begin2[i] == r && free) {
+                            runs->begin[before[i]] = r;
+                            runs->end[before[i]] = min(r + len2[i], t.n);
+                            runs->id[before[i]] = id2[i];
+                        }
+                        row_ids[r] = 0xffff;            // its term is a matrix step's
+                    }
+                }
+                if (etid == 0) runs->count = free ? count : 0;      // (a time-out leaves no list)
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (adapters) {
+                    if (lane == 0) tc::mbar_arrive(lfull);
+                    lphase ^= 1;
+                }
             }
-            bool ok = tc::mbar_wait(&tfull[acc], acc_phase, abort);
+            float *dump = reinterpret_cast<float *>(epi);
+            bool ok = true;
+            if (split > 1) {
+                // the partial sums of the tile before have been read (first tile: passes at once); the
+                // rows that this block will write take their adapter terms while the products run
+                ok = __all_sync(~0u, tc::mbar_wait_cluster(done, sum_phase ^ 1, abort));
+                if (shorts && ok) {
+                    for (int row = (int)rank; row < t.n; row += 4 * split) {
+                        int id[4];
+                        int64_t ts[4];
+                        float add[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = row + i * split;
+                            id[i] = r < t.n && ch < p.out && row_ids[r] != 0xffff ? (int)row_ids[r] : -1;
+                            ts[i] = t.t0 + r;
+                        }
+                        lora_terms<T, DIR, 4>(m.lora, id, ts, ch, p.out, add);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (row + i * split < t.n) dump[(row + i * split) * MM_LANES + wq * 32 + lane] = add[i];
+                    }
+                }
+            }
+            ok = tc::mbar_wait(&tfull[acc], acc_phase, abort) && ok;
             ok = __all_sync(~0u, ok);
             tc::fence_after_sync();
             const uint32_t at = tmem + acc * p.acc_cols + ((uint32_t)(wq * 32) << 16);
@@ -595,13 +699,26 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             if (split == 1) {
                 if (shorts && ok) {
                     // their terms into the accumulators
-                    for (int r = 0; r < t.n; ++r) {
-                        const int id = row_ids[r];
-                        if (id == 0xffff) continue;
-                        const float add = ch < p.out ? lora_term<T, DIR>(m.lora, id, t.t0 + r, ch, p.out) : 0.f;
-                        const uint32_t y = tc::tmem_ld_32x32b_x1(at + r);
-                        tc::tmem_ld_wait();
-                        tc::tmem_st_32x32b_x1(at + r, __float_as_uint(__uint_as_float(y) + add));
+                    for (int r = 0; r < t.n; r += 4) {
+                        int id[4];
+                        int64_t ts[4];
+                        float add[4];
+                        bool some = false;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            id[i] = r + i < t.n && row_ids[r + i] != 0xffff ? (int)row_ids[r + i] : -1;
+                            some |= id[i] >= 0;
+                            if (ch >= p.out) id[i] = -1;
+                            ts[i] = t.t0 + r + i;
+                        }
+                        if (!some) continue;
+                        lora_terms<T, DIR, 4>(m.lora, id, ts, ch, p.out, add);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t y = tc::tmem_ld_32x32b_x1(at + r + i);
+                            tc::tmem_ld_wait();
+                            tc::tmem_st_32x32b_x1(at + r + i, __float_as_uint(__uint_as_float(y) + add[i]));
+                        }
                     }
                     tc::tmem_st_wait();
                 }
@@ -649,18 +766,17 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             } else {
                 // partial sums of the cluster's blocks as [row][channel], summed in rank order by
                 // the block that writes the row
-                float *dump = reinterpret_cast<float *>(epi);
-                // the sums of the tile before have been read (first tile: passes at once)
-                ok = tc::mbar_wait_cluster(done, sum_phase ^ 1, abort) && ok;
-                ok = __all_sync(~0u, ok);
                 if (ok) {
                     for (int r = 0; r < t.n16; r += 16) {
                         uint32_t y[16];
                         tc::tmem_ld_32x32b_x16(at + r, y);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            dump[(r + j) * MM_LANES + wq * 32 + lane] = __uint_as_float(y[j]);
+                        for (int j = 0; j < 16; ++j) {
+                            float *d = dump + (r + j) * MM_LANES + wq * 32 + lane;
+                            const bool mine = shorts && (r + j) % split == (int)rank && r + j < t.n;
+                            *d = mine ? *d + __uint_as_float(y[j]) : __uint_as_float(y[j]);
+                        }
                     }
                 }
                 release();
@@ -672,8 +788,6 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
 #pragma unroll 2
                     for (int row = (int)rank; row < t.n; row += split) {
                         float sum = 0.f;
-                        if (shorts && row_ids[row] != 0xffff && ch < p.out)
-                            sum = lora_term<T, DIR>(m.lora, row_ids[row], t.t0 + row, ch, p.out);
                         const uint32_t from = tc::smem_u32(dump + row * MM_LANES + wq * 32 + lane);
                         for (int c = 0; c < split; ++c)
                             sum += __uint_as_float(tc::ld_shared_cluster(tc::mapa_shared(from, c)));
@@ -687,7 +801,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             }
             if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
         }
-    } else if (warp == 16) {
+    } else if (warp == MM_WARP_X) {
         // the whole warp walks, one elected lane issues (as for the MMAs below)
         if (tiled) {
             RingPos pos{0, 0};
@@ -723,8 +837,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     pos.advance(stages);
                 }
                 if (ok && adapters) {
-                    RunWalk run(m.offsets, m.lora.ids, m.lora.R, (int)t.t0, (int)t.t0 + t.n);
-                    while (ok && run.next()) {
+                    const int count = runs_wait() ? runs->count : 0;
+                    for (int run = 0; run < count && ok; ++run) {
                         for (int rs = 0; rs < rsteps; ++rs) {
                             ok = __all_sync(~0u, tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort));
                             if (!ok) break;
@@ -732,6 +846,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                             pos.advance(stages);
                         }
                     }
+                    runs_done();
                 }
             }
             if (!ok) {
@@ -741,14 +856,14 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
             }
         }
-    } else if (warp >= 18) {
+    } else if (warp >= MM_WARP_WORDS) {
         // a stage: the block's channels x a step's columns (forward), or a step's rows x the block's
         // columns
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         if (p.wtiled) {
-            if (warp == 18) {
+            if (warp == MM_WARP_WORDS) {
                 for (int u = group; u < tiles && ok; u += ngroups) {
                     const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
                     const int erow = t.e * m.w.N;
@@ -773,7 +888,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
             }
         } else {
-            const int tid = threadIdx.x - 576;
+            const int tid = threadIdx.x - MM_WARP_WORDS * 32;
             const int nw = (int)(((int64_t)m.w.K * B + 31) / 32);
             for (int u = group; u < tiles && ok; u += ngroups) {
                 const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
@@ -851,9 +966,9 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     pos.advance(stages);
                 }
                 if (ok && adapters) {
-                    RunWalk run(m.offsets, m.lora.ids, m.lora.R, (int)t.t0, (int)t.t0 + t.n);
-                    while (ok && run.next()) {
-                        const int b0 = (run.begin - (int)t.t0) & -GRAIN, b1 = ((run.end - (int)t.t0) + GRAIN - 1) & -GRAIN;
+                    const int count = runs_wait() ? runs->count : 0;
+                    for (int run = 0; run < count && ok; ++run) {
+                        const int b0 = runs->begin[run] & -GRAIN, b1 = (runs->end[run] + GRAIN - 1) & -GRAIN;
                         const uint32_t rid = tc::idesc_f16_f32(Half2<T>::kType, MROWS, b1 - b0, DIR, 0);
                         for (int rs = 0; rs < rsteps; ++rs) {
                             ok = __all_sync(~0u, tc::mbar_wait(&full[pos.stage], pos.phase, abort));
@@ -863,6 +978,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                             pos.advance(stages);
                         }
                     }
+                    runs_done();
                 }
                 if (ok && tc::elect_one()) {
                     if constexpr (PAIR) tc::mma_commit_both(&tfull[acc]);
@@ -881,12 +997,13 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         }
     }
 
+    if (m.lora.R > 0) grid_wait();          // whatever came before is done before this kernel is
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     if (cluster > 1) tc::cluster_sync();    // no block leaves while others use its memory
     if (*abort && threadIdx.x == 0) set_status(m.status, GPTQ_ERR_TIMEOUT);
-    if (warp == 17) {
+    if (warp == MM_WARP_MMA) {
         tc::fence_after_sync();
         if constexpr (PAIR) tc::tmem_dealloc_pair(tmem, MM_TMEM);
         else tc::tmem_dealloc(tmem, MM_TMEM);

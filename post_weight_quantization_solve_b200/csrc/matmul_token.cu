@@ -98,7 +98,10 @@ __global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
     const MatmulArg &m = p.m;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = lane & 3, g = lane >> 2;
-    grid_dependency();
+    // With adapters the kernel before this one is the one that makes T; all that is read up to the
+    // sums was there before that one began, so only the sums wait for it.
+    if (m.lora.R == 0) grid_wait();
+    grid_release();
 
     // which range, and which of its rows
     int e = 0;
@@ -118,9 +121,13 @@ __global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
         __syncthreads();
         if (found[3]) {
             if (threadIdx.x == 0) set_status(m.status, GPTQ_ERR_ARG);
+            grid_wait();
             return;
         }
-        if (failed(m.status)) return;
+        if (failed(m.status)) {
+            grid_wait();
+            return;
+        }
         if (m.lora.R > 0) {
             const int begin = __ldg(m.offsets), end = __ldg(m.offsets + m.lora.R);
             t0 = begin + (int64_t)blockIdx.y * ROWS;
@@ -159,7 +166,10 @@ __global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
             n = found[2];
         }
     }
-    if (n <= 0) return;
+    if (n <= 0) {
+        grid_wait();
+        return;
+    }
 
     const int c0 = blockIdx.x * TK_CH;
     const int64_t erow = (int64_t)e * m.w.N;
@@ -280,6 +290,7 @@ __global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
             for (int i = 0; i < 4; ++i)
                 part[warp][b * 8 + 2 * quad + (i & 1)][a * 16 + g + 8 * (i >> 1)] = acc[a][b][i];
     __syncthreads();
+    if (m.lora.R > 0) grid_wait();
     T *Y = static_cast<T *>(m.Y);
     for (int i = threadIdx.x; i < ROWS * TK_CH; i += TK_WARPS * 32) {
         const int row = i / TK_CH, c = i % TK_CH, ch = c0 + c;
@@ -292,7 +303,13 @@ __global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
             const int t = (int)t0 + row;
             const int s = request_of(m.offsets, m.lora.R, t);
             const int id = __ldg(m.lora.ids + s);
-            if (id >= 0) sum += lora_term<T, 0>(m.lora, id, t, ch, m.w.N);
+            if (id >= 0) {
+                const int ids[1] = {id};
+                const int64_t ts[1] = {t};
+                float add[1];
+                lora_terms<T, 0, 1>(m.lora, ids, ts, ch, m.w.N, add);
+                sum += add[0];
+            }
         }
         Y[(t0 + row) * m.ldy + ch] = from_f32<T>(sum);
     }

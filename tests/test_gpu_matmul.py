@@ -113,6 +113,13 @@ def test_forward_row_pitch(rows, xpad):
     forward_case("bf16", 4, 64, False, [rows], 96, 128, xpad=xpad)
 
 
+@pytest.mark.parametrize("K,N", [(256, 2560), (201, 2571)])
+@pytest.mark.parametrize("counts", [[1500, 0, 2500], [200] * 20, [60] * 20])
+def test_forward_many_tiles_a_block(K, N, counts):
+    forward_case("bf16", 4, 64, False, counts, N, K, pad=3)
+    forward_case("fp16", 3, 0, False, counts, N, K, first=2)
+
+
 def test_forward_long_contraction_and_wide_layer():
     forward_case("bf16", 4, 128, False, [24], 64, 14336)     # clusters share the contraction
     forward_case("bf16", 2, 0, False, [2], 5000, 640)
@@ -277,6 +284,36 @@ def test_lora_backward(counts, ids, dtype, bits, groupsize, rank, N, K):
     assert only[0] is None and only[2] is None and torch.equal(only[1], dA)
     only = gq.gptq_matmul_lora_backward(c["dY"], c["X"], *c["args"], want=(False, False, True))
     assert torch.equal(only[2], dB)
+
+
+@pytest.mark.parametrize("dtype,K,N,rank", [("bf16", 256, 2560, 64), ("fp16", 200, 2568, 16), ("bf16", 129, 2571, 8)])
+def test_many_tiles_a_block(dtype, K, N, rank):
+    # pairs of blocks that walk several tiles each, tiles with several long and short runs, and
+    # layouts with and without tiled copies
+    rng = gen(K)
+    counts, ids = [], []
+    while sum(counts) < 4000:
+        counts.append(int(rng.choice([0, 1, 3, 15, 16, 17, 60, 300])))
+        ids.append(int(rng.integers(-1, 4)))
+    c = lora_case(5, dtype, 4, 32, counts, ids, 4, rank, N, K, first=1, pad=2)
+    out = torch.full((c["M"], N), 7.0, dtype=c["t"], device="cuda")
+    status = gq.new_status()
+    gq.gptq_matmul_lora(c["X"], *c["args"], out=out, status=status)
+    gq.raise_on_status(status)
+    check_lora(c, out, 7.0)
+    # the input gradient of a layer as wide (its channels are K there)
+    c = lora_case(6, dtype, 4, 32, counts, ids, 4, rank, K, N, first=1, pad=2)
+    dX = torch.full((c["M"], N), 7.0, dtype=c["t"], device="cuda")
+    status = gq.new_status()
+    gq.gptq_matmul_lora_backward(c["dY"], c["X"], *c["args"], dX=dX, want=(True, False, False), status=status)
+    gq.raise_on_status(status)
+    arrays = [f64(c["dY"]), f64(c["X"]), c["L"]["W"][0], f64(c["A"]), f64(c["B"])]
+    al = c["alpha"].astype(np.float64)
+    want = ref.lora_backward(*arrays, al, c["o"], c["ids"], np.full((c["M"], N), 7.0))[0]
+    S = ref.lora_backward(*map(np.abs, arrays), al, c["o"], c["ids"], np.zeros((c["M"], N)))[0]
+    floor = 2.0 ** -24 if c["t"] == torch.float16 else 0.0
+    check(f64(dX), want, limit(want, S, K + 2 * rank, c["t"], 1) + 2 * pair_eps(c["t"]) * S
+          + floor * rank * np.abs(arrays[3]).max())
 
 
 def test_lora_gradients_against_differences():
