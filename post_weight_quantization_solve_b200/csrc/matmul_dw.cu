@@ -4,18 +4,22 @@
 // halves [hi | lo], whose two products are added in the epilogue.
 //
 // Both operands come straight from row-major matrices: rows are the contraction, so a box of
-// 64 rows x 64 columns in the 128-byte swizzle is an MN-major operand. A tile is 128 columns
-// of P (TMEM lanes) x up to 256 columns of Q; the 64-row steps of a range are accumulated in
-// TMEM. Range ends do not fall on step borders: the rows of the last step that belong to
-// others are set to zero in shared memory, in both operands, before the MMAs read it.
+// 128 rows x 64 columns in the 128-byte swizzle is an MN-major operand. The 128-row steps of a
+// range are accumulated in TMEM. Range ends do not fall on step borders: a step that a range ends
+// in lands on a barrier of its own, a warp sets the rows that belong to others to zero in shared
+// memory, in both operands (infinities in one would meet zeros of the other), and passes it on.
+//
+// PAIR: two blocks share a tile of 256 columns of P (128 TMEM lanes each) x 256 of Q
+// (cta_group::2): each loads its own columns of P and half of Q's, 64 KB a step. Single blocks
+// take 128 columns of P x up to 256 of Q: narrow Q (adapters), and products with few tiles.
 //
 // The tensor core's fp32 accumulation rounds each step the same way, so a chain is at most
 // 2,048 rows (128 MMAs); longer ranges swap accumulators and the epilogue adds the next chain
 // to the stored sum in fp32 to nearest. The same thread adds every chain of an element, in
 // order, so results do not change from run to run.
 //
-// Roles (320 threads): warp 0 tiled copies, warp 1 TMEM, row ends and MMAs, warps 2-5 epilogue,
-// warps 6-9 plain copies where the layout refuses tiled ones.
+// Roles (384 threads): warp 0 tiled copies, warp 1 TMEM and MMAs, warp 2 range ends, warps 4-7
+// epilogue, warps 8-11 plain copies where the layout refuses tiled ones.
 #include <algorithm>
 
 #include "matmul.cuh"
@@ -23,13 +27,12 @@
 namespace gptq {
 
 namespace {
-constexpr int DW_LANES = 128, DW_COLS = 256, DW_BK = 64, DW_STAGES = 4;
-constexpr int DW_BOX = 64 * 64 * 2;
-constexpr int DW_STAGE = (DW_LANES + DW_COLS) * DW_BK * 2;      // 48 KB
+constexpr int DW_LANES = 128, DW_COLS = 256, DW_BK = 128, DW_MAX_STAGES = 4;
+constexpr int DW_BOX = 128 * 64 * 2;                            // 16 KB
 constexpr int DW_EPI = 4 * 32 * 33 * 4;
-constexpr int DW_SMEM = DW_STAGES * DW_STAGE + DW_EPI + 1024 + 256;
-constexpr int DW_THREADS = 320;
-constexpr int DW_CHAIN = 32;                                    // steps of one accumulator
+constexpr int DW_FIXED = DW_EPI + 1024 + 256;
+constexpr int DW_THREADS = 384;
+constexpr int DW_CHAIN = 16;                                    // steps of one accumulator
 }  // namespace
 
 struct DwArg {
@@ -47,6 +50,7 @@ struct DwArg {
     int accumulate;
     float *out;               // [split][groups][np][nq'] (or [nq'][np])
     int tiled, vec;
+    int stages, boxes;        // operand ring; boxes of a stage (P's two, then Q's)
     int32_t *status;
 };
 
@@ -98,11 +102,11 @@ struct StepWalk {
     }
 };
 
-// 64 rows x 64 columns from (r0, c0) into a swizzled box; zeros past `rows` or `cols`.
+// 128 rows x 64 columns from (r0, c0) into a swizzled box; zeros past `rows` or `cols`.
 template <typename T>
 __device__ __forceinline__ void dw_plain_box(uint8_t *dst, const T *x, int64_t ld, int64_t r0, int rows,
                                              int c0, int cols, bool vec, int tid, int nthr) {
-    for (int i = tid; i < 64 * 8; i += nthr) {
+    for (int i = tid; i < DW_BK * 8; i += nthr) {
         const int r = i >> 3, q = i & 7, c = c0 + 8 * q;
         uint32_t v[4] = {0u, 0u, 0u, 0u};
         if (r < rows && c < cols) {
@@ -121,17 +125,19 @@ __device__ __forceinline__ void dw_plain_box(uint8_t *dst, const T *x, int64_t l
     }
 }
 
-template <typename T>
+template <typename T, bool PAIR>
 __global__ void __launch_bounds__(DW_THREADS, 1)
     k_matmul_dw(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ DwArg p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *epi = reinterpret_cast<float *>(smem + DW_STAGES * DW_STAGE);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + DW_STAGES * DW_STAGE + DW_EPI);
-    uint64_t *empty = full + DW_STAGES;
-    uint64_t *tfull = empty + DW_STAGES;
+    const int stages = p.stages, stage_bytes = p.boxes * DW_BOX;
+    float *epi = reinterpret_cast<float *>(smem + stages * stage_bytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + stages * stage_bytes + DW_EPI);
+    uint64_t *empty = full + DW_MAX_STAGES;
+    uint64_t *tail = empty + DW_MAX_STAGES;     // copies of steps that a range ends in
+    uint64_t *tfull = tail + DW_MAX_STAGES;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
@@ -139,14 +145,17 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     int *refuse = reinterpret_cast<int *>(tmem_slot + 2);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? tc::cluster_ctarank() : 0u;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < DW_STAGES; ++s) {
-            tc::mbar_init(&full[s], p.tiled ? 1 : 4);
+        // tiled: the copies' warp of each block, or its warp for range ends; plain: four warps each
+        for (int s = 0; s < stages; ++s) {
+            tc::mbar_init(&full[s], (p.tiled ? 1 : 4) * (PAIR ? 2 : 1));
             tc::mbar_init(&empty[s], 1);
+            tc::mbar_init(&tail[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&tfull[b], 1);
-            tc::mbar_init(&tempty[b], 128);
+            tc::mbar_init(&tempty[b], PAIR ? 8 : 4);
         }
         tc::mbar_init(drain, 1);
         *abort = 0;
@@ -157,157 +166,217 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
             tc::prefetch_tmap(&qmap);
         }
     }
-    if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+    if (warp == 1) {
+        if constexpr (PAIR) tc::tmem_alloc_pair(tmem_slot, 512);
+        else tc::tmem_alloc(tmem_slot, 512);
+    }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     grid_dependency();
+    if (threadIdx.x == DW_THREADS - 1 && failed(p.status)) *refuse = 2;
     bool bad = p.offsets && offsets_bad(p.offsets, p.R, p.M, threadIdx.x, DW_THREADS);
     if (p.ids) bad |= ids_bad(p.ids, p.R, p.L, threadIdx.x, DW_THREADS);
-    if (bad) *refuse = 1;
-    if (threadIdx.x == 0 && failed(p.status)) *refuse = 2;
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) {
+        *refuse = 1;
+        set_status(p.status, GPTQ_ERR_ARG);
+    }
     __syncthreads();
-    if (*refuse == 1 && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_ARG);
+    if constexpr (PAIR) tc::cluster_sync();     // both blocks' barriers and refusal are in place
+    int skip = *refuse;
+    if constexpr (PAIR) skip = (int)tc::ld_shared_cluster(tc::mapa_shared(tc::smem_u32(refuse), 0));
 
-    const int tp = (p.np + DW_LANES - 1) / DW_LANES, tq = (p.nq + DW_COLS - 1) / DW_COLS;
+    constexpr int PW = PAIR ? 2 * DW_LANES : DW_LANES;
+    const int tp = (p.np + PW - 1) / PW, tq = (p.nq + DW_COLS - 1) / DW_COLS;
     const int per_group = tp * tq * p.split;
-    const int64_t units = *refuse ? 0 : (int64_t)p.groups * per_group;
-    const int qboxes = (min(p.nq, DW_COLS) + 63) / 64;
-    // unit -> group, part, tile of P fastest
-    auto decode = [&](int64_t u, int &g, int &part, int &pt, int &qt) {
-        g = (int)(u / per_group);
-        int r = (int)(u - (int64_t)g * per_group);
-        part = r / (tp * tq);
-        r -= part * tp * tq;
-        qt = r / tp;
-        pt = r - qt * tp;
+    const int64_t units = skip ? 0 : (int64_t)p.groups * per_group;
+    const int64_t first = blockIdx.x / (PAIR ? 2 : 1), by = gridDim.x / (PAIR ? 2 : 1);
+    // unit -> group, part of its steps, this block's first columns of P and Q (operand) and of the
+    // tile's Q columns, tiles of P fastest
+    struct Unit {
+        int g, s0, s1, pc, qc, qb, cols;        // qb boxes of Q from qc; the tile's columns
+        int qt;
     };
-    auto steps_of = [&](int g, int part, int &s0, int &s1) {
-        const int n = StepWalk::total(p, g);
-        s0 = (int)((int64_t)n * part / p.split);
-        s1 = (int)((int64_t)n * (part + 1) / p.split);
+    auto unit = [&](int64_t u) {
+        Unit t;
+        t.g = (int)(u / per_group);
+        int r = (int)(u - (int64_t)t.g * per_group);
+        const int part = r / (tp * tq);
+        r -= part * tp * tq;
+        t.qt = r / tp;
+        t.pc = (r - t.qt * tp) * PW + (int)rank * DW_LANES;
+        const int n = StepWalk::total(p, t.g);
+        t.s0 = (int)((int64_t)n * part / p.split);
+        t.s1 = (int)((int64_t)n * (part + 1) / p.split);
+        // columns that the MMAs take: multiples of 16 (a pair: all 256, zeros past Q's end)
+        t.cols = PAIR ? DW_COLS : min(DW_COLS, (p.nq - t.qt * DW_COLS + 15) & ~15);
+        t.qc = t.qt * DW_COLS + (PAIR ? (int)rank * (DW_COLS / 2) : 0);
+        t.qb = PAIR ? 2 : (t.cols + 63) / 64;
+        return t;
+    };
+    auto arrive_full = [&](int stage) {
+        if (PAIR && rank != 0) tc::mbar_arrive_remote(tc::mapa_shared(tc::smem_u32(&full[stage]), 0));
+        else tc::mbar_arrive(&full[stage]);
     };
 
     if (warp == 0 && p.tiled) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                int g, part, pt, qt, s0, s1, n;
-                int64_t r;
-                decode(u, g, part, pt, qt);
-                steps_of(g, part, s0, s1);
-                StepWalk walk(p, g, s0, s1);
-                const int pb = min(2, (p.np - pt * DW_LANES + 63) / 64);
-                const int qb = min(qboxes, (p.nq - qt * DW_COLS + 63) / 64);
-                while (walk.next(r, n)) {
-                    if (!tc::mbar_wait(&empty[stage], phase ^ 1, abort)) { ok = false; break; }
-                    tc::mbar_arrive_expect_tx(&full[stage], (pb + qb) * DW_BOX);
-                    uint8_t *a = smem + stage * DW_STAGE, *b = a + 2 * DW_BOX;
-                    for (int i = 0; i < pb; ++i)
-                        tc::tma_load_2d(a + i * DW_BOX, &pmap, &full[stage], pt * DW_LANES + 64 * i, (int)r);
-                    for (int i = 0; i < qb; ++i)
-                        tc::tma_load_2d(b + i * DW_BOX, &qmap, &full[stage], qt * DW_COLS + 64 * i, (int)r);
-                    if (++stage == DW_STAGES) { stage = 0; phase ^= 1; }
+        // the whole warp walks, one elected lane issues
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int64_t u = first; u < units && ok; u += by) {
+            const Unit t = unit(u);
+            StepWalk walk(p, t.g, t.s0, t.s1);
+            int64_t r;
+            int n;
+            const uint32_t bytes = (2 + t.qb) * DW_BOX;
+            while (walk.next(r, n)) {
+                ok = __all_sync(~0u, tc::mbar_wait(&empty[stage], phase ^ 1, abort));
+                if (!ok) break;
+                uint8_t *a = smem + stage * stage_bytes, *b = a + 2 * DW_BOX;
+                const int x0 = t.pc, x1 = t.qc, y = (int)r;
+                const bool ends = n < DW_BK;
+                if (tc::elect_one()) {
+                    if (ends || !PAIR) {
+                        uint64_t *bar = ends ? &tail[stage] : &full[stage];
+                        tc::mbar_arrive_expect_tx(bar, bytes);
+                        for (int i = 0; i < 2; ++i) tc::tma_load_2d(a + i * DW_BOX, &pmap, bar, x0 + 64 * i, y);
+                        for (int i = 0; i < t.qb; ++i) tc::tma_load_2d(b + i * DW_BOX, &qmap, bar, x1 + 64 * i, y);
+                    } else {
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+                        const uint32_t fb = tc::mapa_shared(tc::smem_u32(&full[stage]), 0);
+                        for (int i = 0; i < 2; ++i) tc::tma_load_2d_pair(a + i * DW_BOX, &pmap, fb, x0 + 64 * i, y);
+                        for (int i = 0; i < 2; ++i) tc::tma_load_2d_pair(b + i * DW_BOX, &qmap, fb, x1 + 64 * i, y);
+                        if (rank != 0) tc::mbar_arrive_remote(fb);
+                    }
                 }
-            }
-            if (!ok) {                      // loads still in flight land before the block exits
-                const long long from = clock64();
-                while (clock64() - from < 20000000ll) {
-                }
+                __syncwarp();
+                if (++stage == stages) { stage = 0; phase ^= 1; }
             }
         }
-    } else if (warp == 1) {
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
+        if (!ok) {                          // loads still in flight land before the block exits
+            const long long from = clock64();
+            while (clock64() - from < 20000000ll) {
+            }
+        }
+    } else if (warp == 2 && p.tiled) {
+        // steps that a range ends in: rows n .. the next multiple of 16 belong to others
+        int stage = 0;
+        uint32_t phases = 0;                // of the tail barriers, a bit a stage
         bool ok = true;
-        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            int g, part, pt, qt, s0, s1, n;
+        for (int64_t u = first; u < units && ok; u += by) {
+            const Unit t = unit(u);
+            StepWalk walk(p, t.g, t.s0, t.s1);
             int64_t r;
-            decode(u, g, part, pt, qt);
-            steps_of(g, part, s0, s1);
-            StepWalk walk(p, g, s0, s1);
-            const int cols = min(DW_COLS, (p.nq - qt * DW_COLS + 15) & ~15);
-            const int qb = (cols + 63) / 64, pb = min(2, (p.np - pt * DW_LANES + 63) / 64);
-            const uint32_t id = tc::idesc_f16_f32(Half2<T>::kType, DW_LANES, cols, 1, 1);
-            int chain = 0;
+            int n;
             while (ok && walk.next(r, n)) {
-                if (chain == 0) {
-                    ok = tc::mbar_wait(&tempty[acc], acc_phase ^ 1, abort);
-                    ok = __all_sync(~0u, ok);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                }
-                ok = tc::mbar_wait(&full[stage], phase, abort);
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
-                uint8_t *a = smem + stage * DW_STAGE;
                 if (n < DW_BK) {
-                    // rows n .. the next multiple of 16 belong to others: zero in both operands
-                    const int zero = ((n + 15) & ~15) - n;
-                    for (int i = lane; i < zero * 8 * 6; i += 32) {
+                    ok = __all_sync(~0u, tc::mbar_wait(&tail[stage], (phases >> stage) & 1u, abort));
+                    if (!ok) break;
+                    phases ^= 1u << stage;
+                    uint8_t *a = smem + stage * stage_bytes;
+                    const int zero = ((n + 15) & ~15) - n, boxes = 2 + t.qb;
+                    for (int i = lane; i < zero * 8 * boxes; i += 32) {
                         const int box = i / (zero * 8), j = i - box * zero * 8;
-                        if (box < 2 ? box < pb : box - 2 < qb)
-                            *reinterpret_cast<uint4 *>(a + box * DW_BOX + (n + (j >> 3)) * 128 + ((j & 7) << 4)) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(a + box * DW_BOX + (n + (j >> 3)) * 128 + ((j & 7) << 4)) =
+                            make_uint4(0u, 0u, 0u, 0u);
                     }
                     tc::fence_async_shared();
                     __syncwarp();
+                    if (lane == 0) arrive_full(stage);
                 }
-                if (lane == 0) {
-                    tc::fence_after_sync();
-                    const uint32_t sa = tc::smem_u32(a), sb = sa + 2 * DW_BOX;
-                    const int kks = (n + 15) / 16;
-                    for (int kk = 0; kk < kks; ++kk)
-                        tc::mma_bf16(tmem + acc * DW_COLS, tc::desc_sw128(sa + kk * 2048, DW_BOX, 1024),
-                                     tc::desc_sw128(sb + kk * 2048, DW_BOX, 1024), id, (chain > 0 || kk > 0) ? 1u : 0u);
-                    tc::mma_commit(&empty[stage]);
+                if (++stage == stages) stage = 0;
+            }
+        }
+    } else if (warp == 1) {
+        if (!PAIR || rank == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            const uint64_t ad0 = tc::desc_sw128(tc::smem_u32(smem), DW_BOX, 1024);
+            const uint64_t bd0 = tc::desc_sw128(tc::smem_u32(smem) + 2 * DW_BOX, DW_BOX, 1024);
+            auto commit = [&](uint64_t *bar) {
+                if (tc::elect_one()) {
+                    if constexpr (PAIR) tc::mma_commit_both(bar);
+                    else tc::mma_commit(bar);
                 }
                 __syncwarp();
-                if (++stage == DW_STAGES) { stage = 0; phase ^= 1; }
-                if (++chain == DW_CHAIN) {
-                    if (lane == 0) tc::mma_commit(&tfull[acc]);
-                    chain = 0;
+            };
+            for (int64_t u = first; u < units && ok; u += by) {
+                const Unit t = unit(u);
+                StepWalk walk(p, t.g, t.s0, t.s1);
+                int64_t r;
+                int n;
+                const uint32_t id = tc::idesc_f16_f32(Half2<T>::kType, PW, t.cols, 1, 1);
+                int chain = 0;
+                while (ok && walk.next(r, n)) {
+                    if (chain == 0) {
+                        ok = __all_sync(~0u, tc::mbar_wait(&tempty[acc], acc_phase ^ 1, abort));
+                        if (!ok) break;
+                    }
+                    ok = __all_sync(~0u, tc::mbar_wait(&full[stage], phase, abort));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint64_t ad = ad0 + (uint32_t)(stage * stage_bytes >> 4);
+                    const uint64_t bd = bd0 + (uint32_t)(stage * stage_bytes >> 4);
+                    const uint32_t d = tmem + acc * DW_COLS;
+                    const int kks = (n + 15) / 16;
+                    if (tc::elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < DW_BK / 16; ++kk) {
+                            if (kk >= kks) break;
+                            const uint32_t add = (chain > 0 || kk > 0) ? 1u : 0u;
+                            if constexpr (PAIR) tc::mma_bf16_pair(d, ad + kk * 128, bd + kk * 128, id, add);
+                            else tc::mma_bf16(d, ad + kk * 128, bd + kk * 128, id, add);
+                        }
+                    }
+                    __syncwarp();
+                    commit(&empty[stage]);
+                    if (++stage == stages) { stage = 0; phase ^= 1; }
+                    if (++chain == DW_CHAIN) {
+                        commit(&tfull[acc]);
+                        chain = 0;
+                        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                    }
+                }
+                if (ok && chain > 0) {
+                    commit(&tfull[acc]);
                     if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                 }
             }
-            if (ok && chain > 0) {
-                if (lane == 0) tc::mma_commit(&tfull[acc]);
-                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            if (tc::elect_one()) {
+                if constexpr (PAIR) tc::mma_commit_pair(tc::mapa_shared(tc::smem_u32(drain), 0));
+                else tc::mma_commit(drain);
+                volatile int never = 0;
+                tc::mbar_wait(drain, 0, &never);
             }
         }
-        if (lane == 0) {
-            tc::mma_commit(drain);
-            volatile int never = 0;
-            tc::mbar_wait(drain, 0, &never);
-        }
-    } else if (warp >= 2 && warp < 6) {
+    } else if (warp >= 4 && warp < 8) {
         const int quad = warp & 3;
-        float *buf = epi + (warp - 2) * 32 * 33;
+        float *buf = epi + quad * 32 * 33;
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
         const int half = p.pair ? p.nq / 2 : 0, nout = p.pair ? half : p.nq;
-        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            int g, part, pt, qt, s0, s1;
-            decode(u, g, part, pt, qt);
-            steps_of(g, part, s0, s1);
-            float *out = p.out + ((int64_t)part * p.groups + g) * p.np * nout;
-            const int r0 = pt * DW_LANES + quad * 32;
-            const int chains = max(1, (s1 - s0 + DW_CHAIN - 1) / DW_CHAIN);
+        for (int64_t u = first; u < units && ok; u += by) {
+            const Unit t = unit(u);
+            const int part = (int)(u / (tp * tq)) % p.split;
+            float *out = p.out + ((int64_t)part * p.groups + t.g) * p.np * nout;
+            const int r0 = t.pc + quad * 32;
+            const int chains = max(1, (t.s1 - t.s0 + DW_CHAIN - 1) / DW_CHAIN);
             for (int c = 0; c < chains && ok; ++c) {
-                const bool none = s1 == s0;             // a range without rows: zeros
+                const bool none = t.s1 == t.s0;         // a range without rows: zeros
                 if (!none) {
-                    ok = tc::mbar_wait(&tfull[acc], acc_phase, abort);
-                    ok = __all_sync(~0u, ok);
+                    ok = __all_sync(~0u, tc::mbar_wait(&tfull[acc], acc_phase, abort));
                     if (!ok) break;
                     tc::fence_after_sync();
                 }
                 const bool add = p.accumulate || c > 0;
-                const int qn = min(DW_COLS, nout - qt * DW_COLS);
+                const int qn = min(DW_COLS, nout - t.qt * DW_COLS);
                 if (!(none && add)) {
+#pragma unroll 1
                     for (int cb = 0; cb < qn; cb += 32) {
                         uint32_t v[32];
 #pragma unroll
@@ -325,7 +394,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                                     v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
                             }
                         }
-                        const int q0 = qt * DW_COLS + cb;
+                        const int q0 = t.qt * DW_COLS + cb;
                         if (p.transposed) {
                             if (r0 + lane < p.np) {
 #pragma unroll
@@ -341,11 +410,13 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                             __syncwarp();
                             const int rows = min(32, p.np - r0);
                             if (cb + lane < qn) {
+                                float *d = out + (int64_t)r0 * nout + q0 + lane;
+                                if (add) {
 #pragma unroll 8
-                                for (int i = 0; i < rows; ++i) {
-                                    float *d = out + (int64_t)(r0 + i) * nout + q0 + lane;
-                                    const float x = buf[i * 33 + lane];
-                                    *d = add ? *d + x : x;
+                                    for (int i = 0; i < rows; ++i) d[(int64_t)i * nout] += buf[i * 33 + lane];
+                                } else {
+#pragma unroll 8
+                                    for (int i = 0; i < rows; ++i) d[(int64_t)i * nout] = buf[i * 33 + lane];
                                 }
                             }
                             __syncwarp();
@@ -354,38 +425,38 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                 }
                 if (!none) {
                     tc::fence_before_sync();
-                    tc::mbar_arrive(&tempty[acc]);
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR && rank != 0) tc::mbar_arrive_remote(tc::mapa_shared(tc::smem_u32(&tempty[acc]), 0));
+                        else tc::mbar_arrive(&tempty[acc]);
+                    }
                     if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                 }
             }
         }
-    } else if (warp >= 6 && !p.tiled) {
-        const int tid = threadIdx.x - 192;
+    } else if (warp >= 8 && !p.tiled) {
+        const int tid = threadIdx.x - 256;
         const T *P = static_cast<const T *>(p.P), *Q = static_cast<const T *>(p.Q);
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            int g, part, pt, qt, s0, s1, n;
+        for (int64_t u = first; u < units && ok; u += by) {
+            const Unit t = unit(u);
+            StepWalk walk(p, t.g, t.s0, t.s1);
             int64_t r;
-            decode(u, g, part, pt, qt);
-            steps_of(g, part, s0, s1);
-            StepWalk walk(p, g, s0, s1);
-            const int pb = min(2, (p.np - pt * DW_LANES + 63) / 64);
-            const int qb = min(qboxes, (p.nq - qt * DW_COLS + 63) / 64);
+            int n;
             while (ok && walk.next(r, n)) {
-                ok = tc::mbar_wait(&empty[stage], phase ^ 1, abort);
-                ok = __all_sync(~0u, ok);
+                ok = __all_sync(~0u, tc::mbar_wait(&empty[stage], phase ^ 1, abort));
                 if (!ok) break;
-                uint8_t *a = smem + stage * DW_STAGE, *b = a + 2 * DW_BOX;
-                for (int i = 0; i < pb; ++i)
-                    dw_plain_box<T>(a + i * DW_BOX, P, p.ldp, r, n, pt * DW_LANES + 64 * i, p.np, (p.vec & 1) != 0, tid, 128);
-                for (int i = 0; i < qb; ++i)
-                    dw_plain_box<T>(b + i * DW_BOX, Q, p.ldq, r, n, qt * DW_COLS + 64 * i, p.nq, (p.vec & 2) != 0, tid, 128);
+                uint8_t *a = smem + stage * stage_bytes, *b = a + 2 * DW_BOX;
+                for (int i = 0; i < 2; ++i)
+                    dw_plain_box<T>(a + i * DW_BOX, P, p.ldp, r, n, t.pc + 64 * i, p.np, (p.vec & 1) != 0, tid, 128);
+                for (int i = 0; i < t.qb; ++i)
+                    dw_plain_box<T>(b + i * DW_BOX, Q, p.ldq, r, n, t.qc + 64 * i, p.nq, (p.vec & 2) != 0, tid, 128);
                 tc::fence_async_shared();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&full[stage]);
-                if (++stage == DW_STAGES) { stage = 0; phase ^= 1; }
+                if (lane == 0) arrive_full(stage);
+                if (++stage == stages) { stage = 0; phase ^= 1; }
             }
         }
     }
@@ -393,10 +464,12 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
+    if constexpr (PAIR) tc::cluster_sync();     // neither block leaves while the pair uses its memory
     if (*abort && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_TIMEOUT);
     if (warp == 1) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, 512);
+        if constexpr (PAIR) tc::tmem_dealloc_pair(tmem, 512);
+        else tc::tmem_dealloc(tmem, 512);
     }
 }
 
@@ -417,12 +490,21 @@ static gptq_status launch_dw(DwArg &p, int dtype, cudaStream_t st) {
     p.tiled = rows_map(&pm, p.P, dtype, p.M, p.np, p.ldp, DW_BK) &&
               rows_map(&qm, p.Q, dtype, p.M, p.nq, p.ldq, DW_BK);
     p.vec = (aligned(p.P, 16) && p.ldp % 8 == 0 ? 1 : 0) | (aligned(p.Q, 16) && p.ldq % 8 == 0 ? 2 : 0);
-    const int64_t tiles = (int64_t)((p.np + DW_LANES - 1) / DW_LANES) * ((p.nq + DW_COLS - 1) / DW_COLS);
-    const int64_t units = tiles * p.groups * p.split;
-    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(units, device_sms()));
+    auto units = [&](int pw) {
+        return (int64_t)((p.np + pw - 1) / pw) * ((p.nq + DW_COLS - 1) / DW_COLS) * p.groups * p.split;
+    };
+    // pairs where both operands fill their tiles and there are pairs enough for the machine
+    const bool pair = !p.pair && p.np > DW_LANES && p.nq > DW_COLS / 2 && 2 * units(2 * DW_LANES) >= device_sms();
+    p.boxes = pair ? 4 : 2 + (std::min(p.nq, DW_COLS) + 63) / 64;
+    p.stages = std::min(DW_MAX_STAGES, (227 * 1024 - DW_FIXED) / (p.boxes * DW_BOX));
+    const size_t smem = (size_t)p.stages * p.boxes * DW_BOX + DW_FIXED;
+    const int blocks = pair ? (int)std::min<int64_t>(units(2 * DW_LANES), device_sms() / 2) * 2
+                            : (int)std::max<int64_t>(1, std::min<int64_t>(units(DW_LANES), device_sms()));
     if (dtype == GPTQ_BF16)
-        return launch_pdl(k_matmul_dw<__nv_bfloat16>, dim3(blocks), DW_THREADS, DW_SMEM, 1, st, pm, qm, p);
-    return launch_pdl(k_matmul_dw<__half>, dim3(blocks), DW_THREADS, DW_SMEM, 1, st, pm, qm, p);
+        return pair ? launch_pdl(k_matmul_dw<__nv_bfloat16, true>, dim3(blocks), DW_THREADS, smem, 2, st, pm, qm, p)
+                    : launch_pdl(k_matmul_dw<__nv_bfloat16, false>, dim3(blocks), DW_THREADS, smem, 1, st, pm, qm, p);
+    return pair ? launch_pdl(k_matmul_dw<__half, true>, dim3(blocks), DW_THREADS, smem, 2, st, pm, qm, p)
+                : launch_pdl(k_matmul_dw<__half, false>, dim3(blocks), DW_THREADS, smem, 1, st, pm, qm, p);
 }
 
 // G[e] (+)= dY^T X over the rows of range e.

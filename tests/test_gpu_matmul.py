@@ -181,7 +181,9 @@ def test_input_gradient(dtype, bits, groupsize, indexed, counts, N, K):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("counts,N,K", [([1], 8, 8), ([0, 65, 1, 130], 200, 264), ([4200], 128, 64),
-                                        ([31, 47], 77, 301), ([2048, 2049], 64, 320)])
+                                        ([31, 47], 77, 301), ([2048, 2049], 64, 320),
+                                        ([130, 0, 300, 17, 64, 128, 255, 1, 16], 1100, 1000), ([2100, 140], 1200, 2200),
+                                        ([90, 33], 1201, 2203)])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_weight_gradient(dtype, counts, N, K, accumulate):
     rng, t = gen(K), TYPES[dtype]
