@@ -15,8 +15,10 @@
 //
 // The tensor core's fp32 accumulation rounds each step the same way, so a chain is at most
 // 2,048 rows (128 MMAs); longer ranges swap accumulators and the epilogue adds the next chain
-// to the stored sum in fp32 to nearest. The same thread adds every chain of an element, in
-// order, so results do not change from run to run.
+// to the stored sum in fp32 to nearest, in order, so results do not change from run to run.
+// Outputs leave through shared memory as tiled stores of 32 x 32 boxes (a later chain as tiled
+// adds, after the one before has completed): row by row from registers they took 25,000 clocks a
+// tile, three times its products. Layouts that tiled stores refuse go row by row.
 //
 // Roles (384 threads): warp 0 tiled copies, warp 1 TMEM and MMAs, warp 2 range ends, warps 4-7
 // epilogue, warps 8-11 plain copies where the layout refuses tiled ones.
@@ -29,7 +31,7 @@ namespace gptq {
 namespace {
 constexpr int DW_LANES = 128, DW_COLS = 256, DW_BK = 128, DW_MAX_STAGES = 4;
 constexpr int DW_BOX = 128 * 64 * 2;                            // 16 KB
-constexpr int DW_EPI = 4 * 32 * 33 * 4;
+constexpr int DW_EPI = 4 * 2 * 32 * 32 * 4;                     // two boxes a warp
 constexpr int DW_FIXED = DW_EPI + 1024 + 256;
 constexpr int DW_THREADS = 384;
 constexpr int DW_CHAIN = 16;                                    // steps of one accumulator
@@ -50,6 +52,7 @@ struct DwArg {
     int accumulate;
     float *out;               // [split][groups][np][nq'] (or [nq'][np])
     int tiled, vec;
+    int tstore;               // outputs by tiled stores
     int stages, boxes;        // operand ring; boxes of a stage (P's two, then Q's)
     int32_t *status;
 };
@@ -128,7 +131,7 @@ __device__ __forceinline__ void dw_plain_box(uint8_t *dst, const T *x, int64_t l
 template <typename T, bool PAIR>
 __global__ void __launch_bounds__(DW_THREADS, 1)
     k_matmul_dw(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
-                const __grid_constant__ DwArg p) {
+                const __grid_constant__ CUtensorMap omap, const __grid_constant__ DwArg p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -355,7 +358,9 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         }
     } else if (warp >= 4 && warp < 8) {
         const int quad = warp & 3;
-        float *buf = epi + quad * 32 * 33;
+        uint8_t *boxes = reinterpret_cast<uint8_t *>(epi) + quad * 8192;
+        float *buf = reinterpret_cast<float *>(boxes);      // or [32][33]
+        int box = 0;
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
@@ -395,7 +400,24 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                             }
                         }
                         const int q0 = t.qt * DW_COLS + cb;
-                        if (p.transposed) {
+                        if (p.tstore) {
+                            // row = lane, 16-byte piece q at q ^ (lane & 7); the box two stores ago is free
+                            uint8_t *to = boxes + box * 4096;
+                            box ^= 1;
+                            if (lane == 0) tc::bulk_wait_read<1>();
+                            __syncwarp();
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                *reinterpret_cast<uint4 *>(to + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                                    make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                            tc::fence_async_shared();
+                            __syncwarp();
+                            if (lane == 0 && r0 < p.np) {
+                                if (add) tc::tma_reduce_add_3d(&omap, to, q0, r0, t.g);
+                                else tc::tma_store_3d(&omap, to, q0, r0, t.g);
+                                tc::bulk_commit();
+                            }
+                        } else if (p.transposed) {
                             if (r0 + lane < p.np) {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
@@ -423,6 +445,8 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                         }
                     }
                 }
+                // the next chain adds to what this one stored
+                if (p.tstore && chains > 1 && lane == 0) tc::bulk_wait_all();
                 if (!none) {
                     tc::fence_before_sync();
                     __syncwarp();
@@ -434,6 +458,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                 }
             }
         }
+        if (lane == 0) tc::bulk_wait_all();
     } else if (warp >= 8 && !p.tiled) {
         const int tid = threadIdx.x - 256;
         const T *P = static_cast<const T *>(p.P), *Q = static_cast<const T *>(p.Q);
@@ -485,8 +510,21 @@ __global__ void __launch_bounds__(256) k_sum_parts(const float *__restrict__ par
     out[i] = s;
 }
 
+// The outputs [groups][np][nq] as boxes of 32 x 32 of one group.
+static bool out_map(CUtensorMap *map, const DwArg &p) {
+    EncodeTiled enc = encode_tiled();
+    if (!enc || p.pair || p.split != 1 || !aligned(p.out, 16) || p.nq % 4 != 0) return false;
+    const cuuint64_t dim[3] = {(cuuint64_t)p.nq, (cuuint64_t)p.np, (cuuint64_t)p.groups};
+    const cuuint64_t stride[2] = {(cuuint64_t)p.nq * 4, (cuuint64_t)p.nq * 4 * p.np};
+    const cuuint32_t box[3] = {32, 32, 1}, step[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.out, dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static gptq_status launch_dw(DwArg &p, int dtype, cudaStream_t st) {
-    CUtensorMap pm{}, qm{};
+    CUtensorMap pm{}, qm{}, om{};
+    p.tstore = out_map(&om, p);
     p.tiled = rows_map(&pm, p.P, dtype, p.M, p.np, p.ldp, DW_BK) &&
               rows_map(&qm, p.Q, dtype, p.M, p.nq, p.ldq, DW_BK);
     p.vec = (aligned(p.P, 16) && p.ldp % 8 == 0 ? 1 : 0) | (aligned(p.Q, 16) && p.ldq % 8 == 0 ? 2 : 0);
@@ -501,10 +539,10 @@ static gptq_status launch_dw(DwArg &p, int dtype, cudaStream_t st) {
     const int blocks = pair ? (int)std::min<int64_t>(units(2 * DW_LANES), device_sms() / 2) * 2
                             : (int)std::max<int64_t>(1, std::min<int64_t>(units(DW_LANES), device_sms()));
     if (dtype == GPTQ_BF16)
-        return pair ? launch_pdl(k_matmul_dw<__nv_bfloat16, true>, dim3(blocks), DW_THREADS, smem, 2, st, pm, qm, p)
-                    : launch_pdl(k_matmul_dw<__nv_bfloat16, false>, dim3(blocks), DW_THREADS, smem, 1, st, pm, qm, p);
-    return pair ? launch_pdl(k_matmul_dw<__half, true>, dim3(blocks), DW_THREADS, smem, 2, st, pm, qm, p)
-                : launch_pdl(k_matmul_dw<__half, false>, dim3(blocks), DW_THREADS, smem, 1, st, pm, qm, p);
+        return pair ? launch_pdl(k_matmul_dw<__nv_bfloat16, true>, dim3(blocks), DW_THREADS, smem, 2, st, pm, qm, om, p)
+                    : launch_pdl(k_matmul_dw<__nv_bfloat16, false>, dim3(blocks), DW_THREADS, smem, 1, st, pm, qm, om, p);
+    return pair ? launch_pdl(k_matmul_dw<__half, true>, dim3(blocks), DW_THREADS, smem, 2, st, pm, qm, om, p)
+                : launch_pdl(k_matmul_dw<__half, false>, dim3(blocks), DW_THREADS, smem, 1, st, pm, qm, om, p);
 }
 
 // G[e] (+)= dY^T X over the rows of range e.

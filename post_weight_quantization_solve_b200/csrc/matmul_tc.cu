@@ -1,4 +1,6 @@
 // Which tiles a packed-weight product on the tensor cores takes (the kernel is in matmul_tc.cuh).
+#include <atomic>
+
 #include "matmul_tc.cuh"
 
 namespace gptq {
@@ -30,6 +32,21 @@ static bool words_map(CUtensorMap *map, const PackedArg &w, int bits) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of `size` blocks that run at once, one block an SM: SMs that a processing cluster has left
+// over stay idle (33 of 4 and 15 of 8 on the 148 SMs of a B200), and a cluster that waits for others
+// to end would double the time. Asked once a device.
+static int matmul_tc_clusters(int size) {
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || size < 1 || size > 8) return 1;
+    int n = known[dev][size].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    n = size == 1 ? device_sms() : matmul_tc_occupancy(size);
+    if (n < 1) n = std::max(1, device_sms() / size);
+    known[dev][size].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // dir 0: Y = X W^T, 1: dX = dY W.
 gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStream_t st) {
     MmTcArg p{};
@@ -53,7 +70,8 @@ gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStre
     p.cols = pair ? 256 : 128;
     p.split = 1;
     if (!pair)
-        while (p.split < 8 && tiles(MM_LANES, p.cols) * p.split * 2 <= sms && steps >= 4 * p.split) p.split *= 2;
+        while (p.split < 8 && tiles(MM_LANES, p.cols) <= matmul_tc_clusters(2 * p.split) && steps >= 4 * p.split)
+            p.split *= 2;
     // the partial sums of 128 rows would leave the input gradient one operand stage
     if (p.split > 1 && dir == 1) p.cols = 64;
     // large boxes of X (few copies to issue), smaller ones where most ranges have a few rows
@@ -72,7 +90,7 @@ gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStre
     p.stages = (int)std::min<size_t>(MM_MAX_STAGES, (227 * 1024 - fixed) / stage);
     const size_t smem = fixed + (size_t)p.stages * stage;
     const int cluster = pair ? 2 : p.split;
-    const int64_t groups = std::min<int64_t>(tiles(pair ? 2 * MM_LANES : MM_LANES, p.cols), sms / cluster);
+    const int64_t groups = std::min<int64_t>(tiles(pair ? 2 * MM_LANES : MM_LANES, p.cols), matmul_tc_clusters(cluster));
     const int blocks = (int)std::max<int64_t>(1, groups) * cluster;
     return dtype == GPTQ_BF16 ? matmul_tc_bf16(map, wmap, p, dir, bits, pair, blocks, smem, st)
                               : matmul_tc_fp16(map, wmap, p, dir, bits, pair, blocks, smem, st);

@@ -107,6 +107,8 @@ gptq_status matmul_tc_bf16(const CUtensorMap &map, const CUtensorMap &wmap, cons
 gptq_status matmul_tc_fp16(const CUtensorMap &map, const CUtensorMap &wmap, const MmTcArg &p, int dir, int bits, bool pair, int blocks,
                            size_t smem, cudaStream_t st);
 
+int matmul_tc_occupancy(int cluster);
+
 // Rows [r0, r0 + rows) x columns [c0, c0 + 64) of X into the swizzled layout of a tiled copy,
 // zeros past row_end or col_end: the copy for layouts that tiled copies refuse.
 template <typename T>

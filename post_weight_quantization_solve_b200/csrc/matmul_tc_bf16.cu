@@ -8,4 +8,28 @@ gptq_status matmul_tc_bf16(const CUtensorMap &map, const CUtensorMap &wmap, cons
     return dir == 0 ? launch_tc_bits<__nv_bfloat16, 0>(map, wmap, p, bits, pair, blocks, smem, st)
                     : launch_tc_bits<__nv_bfloat16, 1>(map, wmap, p, bits, pair, blocks, smem, st);
 }
+
+// Clusters of `cluster` blocks that fit the current device at once (0: the question failed).
+int matmul_tc_occupancy(int cluster) {
+    constexpr int smem = 200 * 1024;
+    auto kernel = k_matmul_tc<__nv_bfloat16, 4, 0, false, false>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(MM_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
 }  // namespace gptq
