@@ -52,6 +52,13 @@ constexpr int MATMUL_MAX_EXPERTS = 512;
 
 // ---- 16-bit types --------------------------------------------------------------------------
 
+// The bits of -v (an integer of at most mantissa + 1 bits) in a 16-bit floating type.
+__host__ __device__ constexpr uint32_t negative_bits(int v, int mantissa, int bias) {
+    int e = 0;
+    while ((v >> e) > 1) ++e;
+    return 0x8000u | (uint32_t)((bias + e) << mantissa) | ((((uint32_t)v << mantissa) >> e) & ((1u << mantissa) - 1u));
+}
+
 template <typename T>
 struct Half2;
 template <>
@@ -67,9 +74,8 @@ struct Half2<__nv_bfloat16> {
     template <int UP, int Z>
     static __device__ __forceinline__ uint32_t scaled(uint32_t v) {
         constexpr uint32_t inv = (127u - UP) << 7;                     // 2^-UP
-        constexpr float c = -(128.f / (1 << UP) + Z);
-        uint32_t d, cc;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(cc) : "f"(c));
+        constexpr uint32_t cc = negative_bits((128 >> UP) + Z, 7, 127) * 0x00010001u;
+        uint32_t d;
         asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(inv * 0x00010001u), "r"(cc));
         return d;
     }
@@ -95,9 +101,8 @@ struct Half2<__half> {
     template <int UP, int Z>
     static __device__ __forceinline__ uint32_t scaled(uint32_t v) {
         constexpr uint32_t inv = (15u - UP) << 10;
-        constexpr float c = -(1024.f / (1 << UP) + Z);
-        uint32_t d, cc;
-        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(cc) : "f"(c));
+        constexpr uint32_t cc = negative_bits((1024 >> UP) + Z, 10, 15) * 0x00010001u;
+        uint32_t d;
         asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(inv * 0x00010001u), "r"(cc));
         return d;
     }
@@ -435,7 +440,8 @@ inline int device_sms() {
 template <typename... KArgs, typename... Args>
 inline gptq_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
                               int cluster, cudaStream_t st, Args... args) {
-    if (smem > 48 * 1024 &&
+    // (kernels with dynamic shared memory have less than 24 KB of static)
+    if (smem > 24 * 1024 &&
         cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
         cudaGetLastError();

@@ -5,9 +5,11 @@
 // its rows; its 8 warps split the contraction, and each lane reads whole chunks of 32 codes,
 // several requests in flight. Four lanes of a quad hold four neighbouring chunks of one row,
 // which is the m16n8k16 fragment layout with the contraction index permuted: a sum does not
-// care, as long as the rows X are read in the same order, and they are (a lane reads the 32
-// values of its own chunk). The matrix instruction adds in fp32; the warps' partial sums meet
-// in shared memory in warp order.
+// care, as long as the rows X are read in the same order. X is put into shared memory once a
+// block, in the order in which codes leave a word, so a fragment is four 16-byte reads and the
+// unpacking needs no permutes (read from global memory per fragment, with its bounds and
+// permutes, X cost as many instructions as the codes: 5.2 a code against 2.6). The matrix
+// instruction adds in fp32; the warps' partial sums meet in shared memory in warp order.
 //
 // Scales: one scale a channel enters in fp32 at the end (the codes are exact); with input
 // groups each weight is rounded once to the rows' 16-bit type, as in the tiled kernel.
@@ -19,11 +21,15 @@ namespace gptq {
 
 namespace {
 constexpr int TK_WARPS = 8;
+constexpr int TK_CH = 32;                  // channels of a block (two 16-row fragments)
+constexpr int TK_SPAN = TK_WARPS * 128;    // columns that the warps cover in one step each
+constexpr int TK_SMEM = 64 * 1024;         // most of X that is staged at a time
 }  // namespace
 
 struct TokenArg {
     MatmulArg m;
     int fold, vec, xvec, E;
+    int rows, span;       // rows of X that a block stages at most, columns at a time (multiple of TK_SPAN)
 };
 
 template <typename T>
@@ -43,24 +49,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// U chunks (32 U codes) of a row in whole 16-byte pieces, or word by word.
-template <int B, int U>
-__device__ __forceinline__ void load_unit(const uint32_t *row, int chunk, int nw, bool vec,
-                                          uint32_t (&w)[U * B]) {
-    const int at = chunk * B;
-    if (row != nullptr && vec && at + U * B <= nw) {
-#pragma unroll
-        for (int j = 0; j < U * B; j += 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + at + j));
-            w[j] = v.x; w[j + 1] = v.y; w[j + 2] = v.z; w[j + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < U * B; ++j) w[j] = row != nullptr && at + j < nw ? __ldg(row + at + j) : 0u;
-    }
-}
-
-// Eight neighbouring values of a row in the pair order of unpack32<B, T, false>.
+// 32 neighbouring values of a row in the pair order of unpack32<B, T, false>.
 template <int B>
 __device__ __forceinline__ void to_pair_order(uint32_t (&x)[16]) {
     if constexpr (B == 3 || B == 4) {
@@ -87,12 +76,13 @@ __device__ __forceinline__ void to_pair_order(uint32_t (&x)[16]) {
     }
 }
 
-// MT fragments of 16 channels, NT of 8 rows.
-template <typename T, int B, int NT, int MT>
-__global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
+// NT fragments of 8 rows; IDX: groups by g_idx.
+template <typename T, int B, int NT, bool IDX>
+__global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 ? 2 : 1)
     k_matmul_token(const __grid_constant__ TokenArg p) {
-    constexpr int U = B == 3 ? 4 : B == 2 ? 2 : 1;      // chunks that fill 16-byte pieces
-    constexpr int ROWS = 8 * NT, TK_CH = 16 * MT, NR = 2 * MT;
+    constexpr int ROWS = 8 * NT, NR = 4;
+    constexpr int AHEAD = IDX || B == 8 ? 1 : B == 4 ? 2 : 3;     // steps of words in flight
+    extern __shared__ uint8_t xs[];                     // [row][chunk of 64 bytes], padded rows
     __shared__ float part[TK_WARPS][ROWS][TK_CH + 1];
     __shared__ int found[4];
     const MatmulArg &m = p.m;
@@ -176,7 +166,7 @@ __global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
     const int nw = (int)(((int64_t)m.w.K * B + 31) / 32);
     const int K = m.w.K;
     const T *X = static_cast<const T *>(m.X);
-    const int32_t *gi = m.w.g_idx ? m.w.g_idx + (int64_t)e * K : nullptr;
+    const int32_t *gi = IDX ? m.w.g_idx + (int64_t)e * K : nullptr;
     const uint32_t *rows[NR];
     const float *srow[NR];
 #pragma unroll
@@ -186,83 +176,99 @@ __global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
         rows[i] = in ? m.w.words + (erow + ch) * m.w.ldw : nullptr;
         srow[i] = in && p.fold ? m.w.scales + (erow + ch) * m.w.groups : nullptr;
     }
-    float acc[MT][NT][4];
+    float acc[2][NT][4];
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.f;
 
-    // a step: the warp's quads cover 4 U chunks of 32 columns. Words and scales of the next step
-    // are requested before this one's are used.
-    const int steps = (K + 128 * U - 1) / (128 * U);
-    uint32_t cur[NR][U * B], nxt[NR][U * B];
-    float sc[NR][U], sn[NR][U];
-    auto fetch = [&](int step, uint32_t (&w)[NR][U * B], float (&s)[NR][U]) {
-        const int chunk = (step * 4 + quad) * U;
+    // a step: the warp's quads cover 4 chunks of 32 columns; the warps take steps in turn
+    const int steps = (K + 127) / 128, mine = (steps - warp + TK_WARPS - 1) / TK_WARPS;
+    uint32_t w[AHEAD][NR][B];
+    float sc[AHEAD][NR];
+    auto fetch = [&](int j, uint32_t (&w)[NR][B], float (&s)[NR]) {
+        const int chunk = (warp + j * TK_WARPS) * 4 + quad;
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-            load_unit<B, U>(step < steps ? rows[i] : nullptr, chunk, nw, p.vec, w[i]);
-            if (p.fold && !gi) {
-#pragma unroll
-                for (int c = 0; c < U; ++c)
-                    s[i][c] = srow[i] && (chunk + c) * 32 < K ? __ldg(srow[i] + (((chunk + c) * 32) >> m.w.gshift)) : 0.f;
-            }
+            load_chunk<B>(j < mine ? rows[i] : nullptr, chunk, nw, p.vec, w[i]);
+            if (!IDX && p.fold)
+                s[i] = srow[i] && chunk * 32 < K ? __ldg(srow[i] + ((chunk * 32) >> m.w.gshift)) : 0.f;
         }
     };
-    fetch(warp, cur, sc);
-#pragma unroll 1
-    for (int step = warp; step < steps; step += TK_WARPS) {
-        if (step + TK_WARPS < steps) fetch(step + TK_WARPS, nxt, sn);
 #pragma unroll
-        for (int c = 0; c < U; ++c) {
-            const int k0 = ((step * 4 + quad) * U + c) * 32;
+    for (int d = 0; d < AHEAD; ++d) fetch(d, w[d], sc[d]);
+
+    // X by spans of columns. Piece q of chunk c stands at q ^ (c >> 1 & 1), rows 32 bytes apart
+    // modulo 128: the eight lanes that read together then meet eight different 16-byte banks.
+    const int pitch = p.span * 2 + 32;
+    const int rounds = (steps + TK_WARPS - 1) / TK_WARPS, per_span = p.span / TK_SPAN;
+    auto stage = [&](int round) {
+        const int k0 = round * TK_SPAN, chunks = min(p.span, (K - k0 + 127) & ~127) / 32;
+        if (round > 0) __syncthreads();                 // everyone is done with the span before
+        for (int i = threadIdx.x; i < n * chunks; i += TK_WARPS * 32) {
+            const int row = i / chunks, c = i - row * chunks, k = k0 + c * 32;
+            const T *src = X + (t0 + row) * m.ldx + k;
+            uint32_t x[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t v[4] = {0u, 0u, 0u, 0u};
+                const int left = K - k - 8 * q;
+                if (left >= 8 && p.xvec) {
+                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src + 8 * q));
+                    v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
+                } else {
+                    const unsigned short *s = reinterpret_cast<const unsigned short *>(src + 8 * q);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < left) v[e >> 1] |= (uint32_t)__ldg(s + e) << (16 * (e & 1));
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[4 * q + e] = v[e];
+            }
+            to_pair_order<B>(x);
+            uint8_t *d = xs + row * pitch + c * 64;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4 *>(d + ((q ^ ((c >> 1) & 1)) << 4)) =
+                    make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+        }
+        __syncthreads();
+    };
+#pragma unroll 1
+    for (int r0 = 0; r0 < rounds; r0 += AHEAD) {
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d) {
+            const int round = r0 + d;
+            if (round >= rounds) break;
+            if (round % per_span == 0) stage(round);
+            if (round >= mine) continue;
+            const int c = ((round % per_span) * TK_WARPS + warp) * 4 + quad;     // chunk of the span
+            const int k0 = ((warp + round * TK_WARPS) * 4 + quad) * 32;
             uint32_t x[NT][16];
 #pragma unroll
             for (int b = 0; b < NT; ++b) {
-                const int row = b * 8 + g;
-                const T *src = X + (t0 + row) * m.ldx + k0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t v[4] = {0u, 0u, 0u, 0u};
-                    const int left = row < n ? K - k0 - 8 * q : 0;
-                    if (left >= 8 && p.xvec) {
-                        const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src + 8 * q));
-                        v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
-                    } else if (left > 0) {
-                        const unsigned short *s = reinterpret_cast<const unsigned short *>(src + 8 * q);
-#pragma unroll 1
-                        for (int i = 0; i < 8 && i < left; ++i) {
-                            const uint32_t h = (uint32_t)__ldg(s + i) << (16 * (i & 1));
-                            v[0] |= i >> 1 == 0 ? h : 0u;
-                            v[1] |= i >> 1 == 1 ? h : 0u;
-                            v[2] |= i >> 1 == 2 ? h : 0u;
-                            v[3] |= i >> 1 == 3 ? h : 0u;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[b][4 * q + i] = v[i];
+                    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+                    if (b * 8 + g < n)
+                        y = *reinterpret_cast<const uint4 *>(xs + (b * 8 + g) * pitch + c * 64 + ((q ^ (quad >> 1)) << 4));
+                    x[b][4 * q] = y.x; x[b][4 * q + 1] = y.y; x[b][4 * q + 2] = y.z; x[b][4 * q + 3] = y.w;
                 }
-                to_pair_order<B>(x[b]);
             }
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
+            for (int a = 0; a < 2; ++a) {
                 uint32_t v[2][16];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int i = 2 * a + h;
-                    uint32_t w[B];
-#pragma unroll
-                    for (int j = 0; j < B; ++j) w[j] = cur[i][c * B + j];
-                    unpack32<B, T, false>(w, v[h]);
-                    if (p.fold) {
-                        if (gi) {
-                            if (srow[i] && k0 < K)
-                                scale32_by_index<T, B, false>(v[h], srow[i], gi, k0, K, m.w.groups, m.status);
-                        } else {
-                            scale32<T>(v[h], sc[i][c]);
-                        }
+                    unpack32<B, T, false>(w[d][i], v[h]);
+                    if constexpr (IDX) {
+                        if (srow[i] && k0 < K)
+                            scale32_by_index<T, B, false>(v[h], srow[i], gi, k0, K, m.w.groups, m.status);
+                    } else if (p.fold) {
+                        scale32<T>(v[h], sc[d][i]);
                     }
                 }
 #pragma unroll
@@ -272,18 +278,12 @@ __global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
                         mma_16816<T>(acc[a][b], v[0][2 * j], v[1][2 * j], v[0][2 * j + 1], v[1][2 * j + 1],
                                      x[b][2 * j], x[b][2 * j + 1]);
             }
-        }
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-#pragma unroll
-            for (int j = 0; j < U * B; ++j) cur[i][j] = nxt[i][j];
-#pragma unroll
-            for (int c = 0; c < U; ++c) sc[i][c] = sn[i][c];
+            if (round + AHEAD < mine) fetch(round + AHEAD, w[d], sc[d]);
         }
     }
     // fragment (16 channels x 8 rows): channel g (+ 8), rows 2 quad, 2 quad + 1
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -315,14 +315,22 @@ __global__ void __launch_bounds__(TK_WARPS * 32, MT == 1 ? 2 : 1)
     }
 }
 
-template <typename T, int NT, int MT>
+template <typename T, int NT, bool IDX>
 static gptq_status launch_token(const TokenArg &p, int bits, dim3 grid, cudaStream_t st) {
+    const size_t smem = (size_t)p.rows * (p.span * 2 + 32);
     switch (bits) {
-        case 2: return launch_pdl(k_matmul_token<T, 2, NT, MT>, grid, TK_WARPS * 32, 0, 1, st, p);
-        case 3: return launch_pdl(k_matmul_token<T, 3, NT, MT>, grid, TK_WARPS * 32, 0, 1, st, p);
-        case 4: return launch_pdl(k_matmul_token<T, 4, NT, MT>, grid, TK_WARPS * 32, 0, 1, st, p);
-        default: return launch_pdl(k_matmul_token<T, 8, NT, MT>, grid, TK_WARPS * 32, 0, 1, st, p);
+        case 2: return launch_pdl(k_matmul_token<T, 2, NT, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
+        case 3: return launch_pdl(k_matmul_token<T, 3, NT, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
+        case 4: return launch_pdl(k_matmul_token<T, 4, NT, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
+        default: return launch_pdl(k_matmul_token<T, 8, NT, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
     }
+}
+
+template <typename T>
+static gptq_status launch_rows(const TokenArg &p, int bits, bool wide, dim3 grid, cudaStream_t st) {
+    if (p.m.w.g_idx)
+        return wide ? launch_token<T, 2, true>(p, bits, grid, st) : launch_token<T, 1, true>(p, bits, grid, st);
+    return wide ? launch_token<T, 2, false>(p, bits, grid, st) : launch_token<T, 1, false>(p, bits, grid, st);
 }
 
 gptq_status matmul_token(const MatmulArg &m, int dtype, int bits, cudaStream_t st) {
@@ -332,17 +340,15 @@ gptq_status matmul_token(const MatmulArg &m, int dtype, int bits, cudaStream_t s
     p.fold = m.w.groups > 0 ? 1 : 0;
     p.vec = aligned(m.w.words, 16) && m.w.ldw % 4 == 0;
     p.xvec = aligned(m.X, 16) && m.ldx % 8 == 0;
-    // one range: up to 16 rows at once, which share the reading of X between 32 channels;
-    // several ranges: most have a few rows
+    // one range: up to 16 rows at once; several: most have a few rows
     const bool wide = p.E == 1 && m.M > 8;
-    const int rows = wide ? 16 : 8, channels = wide ? 32 : 16;
+    const int rows = wide ? 16 : 8;
+    p.rows = (int)std::min<int64_t>(rows, m.M);
+    p.span = std::min((m.w.K + TK_SPAN - 1) / TK_SPAN, std::max(1, TK_SMEM / (p.rows * 2 * TK_SPAN))) * TK_SPAN;
     const int64_t items = p.E == 1 ? (m.M + rows - 1) / rows : std::min<int64_t>(p.E, m.M) + m.M / rows;
-    const dim3 grid((m.w.N + channels - 1) / channels, (unsigned)items);
-    if (dtype == GPTQ_BF16)
-        return wide ? launch_token<__nv_bfloat16, 2, 2>(p, bits, grid, st)
-                    : launch_token<__nv_bfloat16, 1, 1>(p, bits, grid, st);
-    return wide ? launch_token<__half, 2, 2>(p, bits, grid, st)
-                : launch_token<__half, 1, 1>(p, bits, grid, st);
+    const dim3 grid((m.w.N + TK_CH - 1) / TK_CH, (unsigned)items);
+    return dtype == GPTQ_BF16 ? launch_rows<__nv_bfloat16>(p, bits, wide, grid, st)
+                              : launch_rows<__half>(p, bits, wide, grid, st);
 }
 
 }  // namespace gptq
