@@ -213,6 +213,55 @@ __device__ __forceinline__ void unpack32(const uint32_t (&w)[B], uint32_t (&out)
     }
 }
 
+// Eight of the codes (the I-th of four groups) as 4 pairs, in the order of unpack32<B, T, false>.
+template <int B, typename T, int I>
+__device__ __forceinline__ void unpack8(const uint32_t (&w)[B], uint32_t (&q)[4]) {
+    if constexpr (B == 8) {
+        uint32_t all[16], two[8] = {w[2 * I], w[2 * I + 1], 0u, 0u, 0u, 0u, 0u, 0u};
+        unpack32<8, T, false>(two, all);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = all[j];
+    } else {
+        constexpr uint32_t MASK = ((1u << B) - 1u) * 0x00010001u;
+        constexpr int PER = (Half2<T>::kType == 1 ? 7 : 10) / B;
+        uint32_t f;
+        if constexpr (B == 3) {
+            const uint32_t g = I == 0 ? w[0]
+                               : I == 1 ? __funnelshift_r(w[0], w[1], 24)
+                               : I == 2 ? __funnelshift_r(w[1], w[2], 16)
+                                        : (w[2] >> 8);
+            f = (g & 0xfffu) | ((g << 4) & 0x0fff0000u);
+        } else if constexpr (B == 2) {
+            f = w[I >> 1] >> (8 * (I & 1));
+        } else {
+            f = w[I];
+        }
+        pair_fields<B, T, 0, 4, PER, MASK, 1 << (B - 1)>(f, q);
+    }
+}
+
+// Four values' pairs times one scale (as scale32).
+template <typename T>
+__device__ __forceinline__ void scale8(uint32_t (&v)[4], float s) {
+    if constexpr (Half2<T>::kType == 1) {
+        const uint32_t hi = Half2<T>::pack(s, s);
+        const float rest = s - __uint_as_float(hi & 0xffff0000u);
+        const uint32_t lo = Half2<T>::pack(rest, rest);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t t;
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t) : "r"(v[i]), "r"(lo));
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(v[i]), "r"(hi), "r"(t));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = Half2<T>::unpack(v[i]);
+            v[i] = Half2<T>::pack(f.x * s, f.y * s);
+        }
+    }
+}
+
 // The 32 values times one scale, each product rounded once to the 16-bit type. bf16: the
 // scale as a pair of bf16 (16 significant bits), v s_lo + v s_hi in one packed multiply-add.
 // fp16 scales can lie below fp16's normal range, so there the products are formed in fp32.

@@ -14,6 +14,7 @@
 // Scales: one scale a channel enters in fp32 at the end (the codes are exact); with input
 // groups each weight is rounded once to the rows' 16-bit type, as in the tiled kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "matmul.cuh"
 
@@ -78,10 +79,9 @@ __device__ __forceinline__ void to_pair_order(uint32_t (&x)[16]) {
 
 // NT fragments of 8 rows; IDX: groups by g_idx.
 template <typename T, int B, int NT, bool IDX>
-__global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 && !IDX && B <= 4 ? (B == 4 ? 3 : 4) : 2)
     k_matmul_token(const __grid_constant__ TokenArg p) {
     constexpr int ROWS = 8 * NT, NR = 4;
-    constexpr int AHEAD = IDX || B == 8 ? 1 : B == 4 ? 2 : 3;     // steps of words in flight
     extern __shared__ uint8_t xs[];                     // [row][chunk of 64 bytes], padded rows
     __shared__ float part[TK_WARPS][ROWS][TK_CH + 1];
     __shared__ int found[4];
@@ -167,14 +167,14 @@ __global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 ? 2 : 1)
     const int K = m.w.K;
     const T *X = static_cast<const T *>(m.X);
     const int32_t *gi = IDX ? m.w.g_idx + (int64_t)e * K : nullptr;
-    const uint32_t *rows[NR];
-    const float *srow[NR];
+    // channels g, g + 8, ... of the block (past the last channel the last one again: its sums are
+    // not written)
+    const uint32_t *row[NR];
+    int last[NR];                                       // their scales' rows
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-        const int ch = c0 + g + 8 * i;
-        const bool in = ch < m.w.N;
-        rows[i] = in ? m.w.words + (erow + ch) * m.w.ldw : nullptr;
-        srow[i] = in && p.fold ? m.w.scales + (erow + ch) * m.w.groups : nullptr;
+        last[i] = min(c0 + g + 8 * i, m.w.N - 1);
+        row[i] = m.w.words + (erow + last[i]) * m.w.ldw + (warp * 4 + quad) * B;
     }
     float acc[2][NT][4];
 #pragma unroll
@@ -184,21 +184,48 @@ __global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.f;
 
-    // a step: the warp's quads cover 4 chunks of 32 columns; the warps take steps in turn
+    // a step: the warp's quads cover 4 chunks of 32 columns; the warps take steps in turn. Words and
+    // scales are requested a step ahead only by the next block on the SM: four of them fit, and all
+    // blocks of a layer run at once (with words held a step ahead three fitted, and the few blocks
+    // over took as long again).
     const int steps = (K + 127) / 128, mine = (steps - warp + TK_WARPS - 1) / TK_WARPS;
-    uint32_t w[AHEAD][NR][B];
-    float sc[AHEAD][NR];
-    auto fetch = [&](int j, uint32_t (&w)[NR][B], float (&s)[NR]) {
-        const int chunk = (warp + j * TK_WARPS) * 4 + quad;
+    uint32_t w[NR][B];
+    float sc[NR];
+    auto fetch = [&](int j) {
+        if (j >= mine) return;
+        const int chunk = (warp + j * TK_WARPS) * 4 + quad, by = j * (TK_WARPS * 4 * B);
+        if ((chunk + 1) * B <= nw) {
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            load_chunk<B>(j < mine ? rows[i] : nullptr, chunk, nw, p.vec, w[i]);
-            if (!IDX && p.fold)
-                s[i] = srow[i] && chunk * 32 < K ? __ldg(srow[i] + ((chunk * 32) >> m.w.gshift)) : 0.f;
+            for (int i = 0; i < NR; ++i) {
+                const uint32_t *r = row[i] + by;
+                if (B == 3 || !p.vec) {
+#pragma unroll
+                    for (int e = 0; e < B; ++e) w[i][e] = __ldg(r + e);
+                } else if constexpr (B == 2) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(r));
+                    w[i][0] = v.x; w[i][1] = v.y;
+                } else if constexpr (B != 3) {
+#pragma unroll
+                    for (int e = 0; e < B; e += 4) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(r + e));
+                        w[i][e] = v.x; w[i][e + 1] = v.y; w[i][e + 2] = v.z; w[i][e + 3] = v.w;
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int e = 0; e < B; ++e) w[i][e] = chunk * B + e < nw ? __ldg(row[i] + by + e) : 0u;
+        }
+        if (!IDX && p.fold) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+                sc[i] = chunk * 32 < K ? __ldg(m.w.scales + (erow + last[i]) * m.w.groups + ((chunk * 32) >> m.w.gshift))
+                                       : 0.f;
         }
     };
-#pragma unroll
-    for (int d = 0; d < AHEAD; ++d) fetch(d, w[d], sc[d]);
+    fetch(0);
 
     // X by spans of columns. Piece q of chunk c stands at q ^ (c >> 1 & 1), rows 32 bytes apart
     // modulo 128: the eight lanes that read together then meet eight different 16-byte banks.
@@ -207,9 +234,10 @@ __global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 ? 2 : 1)
     auto stage = [&](int round) {
         const int k0 = round * TK_SPAN, chunks = min(p.span, (K - k0 + 127) & ~127) / 32;
         if (round > 0) __syncthreads();                 // everyone is done with the span before
-        for (int i = threadIdx.x; i < n * chunks; i += TK_WARPS * 32) {
-            const int row = i / chunks, c = i - row * chunks, k = k0 + c * 32;
-            const T *src = X + (t0 + row) * m.ldx + k;
+        for (int r = 0; r < n; ++r)
+        for (int c = threadIdx.x; c < chunks; c += TK_WARPS * 32) {
+            const int k = k0 + c * 32;
+            const T *src = X + (t0 + r) * m.ldx + k;
             uint32_t x[16];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -228,7 +256,7 @@ __global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 ? 2 : 1)
                 for (int e = 0; e < 4; ++e) x[4 * q + e] = v[e];
             }
             to_pair_order<B>(x);
-            uint8_t *d = xs + row * pitch + c * 64;
+            uint8_t *d = xs + r * pitch + c * 64;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 *reinterpret_cast<uint4 *>(d + ((q ^ ((c >> 1) & 1)) << 4)) =
@@ -237,49 +265,55 @@ __global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 ? 2 : 1)
         __syncthreads();
     };
 #pragma unroll 1
-    for (int r0 = 0; r0 < rounds; r0 += AHEAD) {
+    for (int round = 0; round < rounds; ++round) {
+        if (round % per_span == 0) stage(round);
+        if (round >= mine) continue;
+        const uint8_t *xr = xs + g * pitch + (((round % per_span) * TK_WARPS + warp) * 4 + quad) * 64;
+        const int k0 = ((warp + round * TK_WARPS) * 4 + quad) * 32;
+        uint32_t all[IDX ? NR : 1][16];                 // by g_idx a chunk is scaled as a whole
+        if constexpr (IDX) {
 #pragma unroll
-        for (int d = 0; d < AHEAD; ++d) {
-            const int round = r0 + d;
-            if (round >= rounds) break;
-            if (round % per_span == 0) stage(round);
-            if (round >= mine) continue;
-            const int c = ((round % per_span) * TK_WARPS + warp) * 4 + quad;     // chunk of the span
-            const int k0 = ((warp + round * TK_WARPS) * 4 + quad) * 32;
-            uint32_t x[NT][16];
+            for (int i = 0; i < NR; ++i) {
+                unpack32<B, T, false>(w[i], all[i]);
+                if (k0 < K)
+                    scale32_by_index<T, B, false>(all[i], m.w.scales + (erow + last[i]) * m.w.groups, gi, k0, K,
+                                                  m.w.groups, m.status);
+            }
+        }
+        // eight columns a lane at a time: the pairs of four channels, then their MMAs
+        auto eight = [&](auto I) {
+            constexpr int i8 = decltype(I)::value;
+            uint32_t v[NR][4], x[NT][4];
 #pragma unroll
             for (int b = 0; b < NT; ++b) {
+                uint4 y = make_uint4(0u, 0u, 0u, 0u);
+                if (b * 8 + g < n) y = *reinterpret_cast<const uint4 *>(xr + b * 8 * pitch + ((i8 ^ (quad >> 1)) << 4));
+                x[b][0] = y.x; x[b][1] = y.y; x[b][2] = y.z; x[b][3] = y.w;
+            }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint4 y = make_uint4(0u, 0u, 0u, 0u);
-                    if (b * 8 + g < n)
-                        y = *reinterpret_cast<const uint4 *>(xs + (b * 8 + g) * pitch + c * 64 + ((q ^ (quad >> 1)) << 4));
-                    x[b][4 * q] = y.x; x[b][4 * q + 1] = y.y; x[b][4 * q + 2] = y.z; x[b][4 * q + 3] = y.w;
+            for (int i = 0; i < NR; ++i) {
+                if constexpr (IDX) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[i][j] = all[i][4 * i8 + j];
+                } else {
+                    unpack8<B, T, i8>(w[i], v[i]);
+                    if (p.fold) scale8<T>(v[i], sc[i]);
                 }
             }
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                uint32_t v[2][16];
+            for (int a = 0; a < 2; ++a)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int i = 2 * a + h;
-                    unpack32<B, T, false>(w[d][i], v[h]);
-                    if constexpr (IDX) {
-                        if (srow[i] && k0 < K)
-                            scale32_by_index<T, B, false>(v[h], srow[i], gi, k0, K, m.w.groups, m.status);
-                    } else if (p.fold) {
-                        scale32<T>(v[h], sc[d][i]);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int b = 0; b < NT; ++b)
-                        mma_16816<T>(acc[a][b], v[0][2 * j], v[1][2 * j], v[0][2 * j + 1], v[1][2 * j + 1],
-                                     x[b][2 * j], x[b][2 * j + 1]);
-            }
-            if (round + AHEAD < mine) fetch(round + AHEAD, w[d], sc[d]);
-        }
+                        mma_16816<T>(acc[a][b], v[2 * a][2 * j], v[2 * a + 1][2 * j], v[2 * a][2 * j + 1],
+                                     v[2 * a + 1][2 * j + 1], x[b][2 * j], x[b][2 * j + 1]);
+        };
+        eight(std::integral_constant<int, 0>{});
+        eight(std::integral_constant<int, 1>{});
+        eight(std::integral_constant<int, 2>{});
+        eight(std::integral_constant<int, 3>{});
+        fetch(round + 1);
     }
     // fragment (16 channels x 8 rows): channel g (+ 8), rows 2 quad, 2 quad + 1
 #pragma unroll
