@@ -321,6 +321,30 @@ __device__ __forceinline__ void scale32_by_index(uint32_t (&v)[16], const float 
     for (int i = 0; i < 16; ++i) v[i] = t[i];
 }
 
+// The 32 values of columns k0 .. k0 + 31, each times the scale of its column's group, the row's
+// scales at scales[g * stride]. The columns are the same for the whole warp.
+template <typename T>
+__device__ __forceinline__ void scale32_by_table(uint32_t (&v)[16], const float *scales, int stride,
+                                                 const int32_t *g_idx, int k0, int K, int groups,
+                                                 int32_t *status) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float s[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = k0 + 2 * i + h;
+            int g = k < K ? __ldg(g_idx + k) : 0;
+            if ((unsigned)g >= (unsigned)groups) {
+                set_status(status, GPTQ_ERR_ARG);
+                g = 0;
+            }
+            s[h] = scales[g * stride];
+        }
+        const float2 f = Half2<T>::unpack(v[i]);
+        v[i] = Half2<T>::pack(f.x * s[0], f.y * s[1]);
+    }
+}
+
 // B words of chunk `chunk` of a row; words at or past the row's end read as zero. `row` NULL:
 // zeros. vec: rows start on 16-byte boundaries.
 template <int B>

@@ -72,8 +72,9 @@ gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStre
     if (!pair)
         while (p.split < 8 && tiles(MM_LANES, p.cols) <= matmul_tc_clusters(2 * p.split) && steps >= 4 * p.split)
             p.split *= 2;
-    // the partial sums of 128 rows would leave the input gradient one operand stage
-    if (p.split > 1 && dir == 1) p.cols = 64;
+    // beside the words of 8 bits, the partial sums of 128 rows would leave the input gradient one
+    // operand stage
+    if (p.split > 1 && dir == 1 && bits == 8) p.cols = 64;
     // large boxes of X (few copies to issue), smaller ones where most ranges have a few rows
     p.box_rows = mean <= 32 ? 32 : mean <= 64 ? 64 : MM_ROWS;
     CUtensorMap map{};
@@ -86,7 +87,14 @@ gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStre
     // staging: a whole tall tile where it holds the only accumulator, partial sums in fp32 when split
     p.epi = p.split > 1 ? p.cols * MM_LANES * 4 : p.accs == 1 ? p.cols * MM_LANES * 2 : 32 * MM_LANES * 2;
     const int stage = MM_B_BYTES + (dir == 1 ? MM_A_BYTES : 0);
-    const size_t fixed = ring_bytes(bits, dir) + p.epi + MM_TABLE + 1024 + 320;
+    size_t fixed = ring_bytes(bits, dir) + p.epi + MM_TABLE + 1024 + 320;
+    // by g_idx: each unpacking thread keeps its row's scales in shared memory where they leave two
+    // operand stages (gathered from global memory for each code, they cost 13,000 clocks a step)
+    const size_t table = (size_t)m.w.groups * MM_WARP_OUT * 32 * 4;
+    if (m.w.g_idx && fixed + table + 2 * stage <= 227 * 1024) {
+        p.idx_table = 1;
+        fixed += table;
+    }
     p.stages = (int)std::min<size_t>(MM_MAX_STAGES, (227 * 1024 - fixed) / stage);
     const size_t smem = fixed + (size_t)p.stages * stage;
     const int cluster = pair ? 2 : p.split;

@@ -99,6 +99,7 @@ struct MmTcArg {
     int fold;             // scales folded into the weights
     int wtiled, yvec;     // packed rows by tiled copies; output rows start on 16-byte boundaries
     int epi;              // bytes of the output staging (or of the partial sums)
+    int idx_table;        // g_idx: the scales of each unpacking thread's row stand in shared memory
     int E;                // row ranges
 };
 
@@ -187,6 +188,8 @@ __device__ __forceinline__ MmTile mm_tile(const MmTcArg &p, const int *table, in
     return t;
 }
 
+__device__ __forceinline__ int m_groups(const MmTcArg &p) { return p.m.w.groups; }
+
 // A place in the ring of operand stages.
 struct RingPos {
     int stage;
@@ -216,7 +219,10 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     uint8_t *words = smem + p.stages * stage_bytes;             // the words' ring
     uint8_t *epi = words + Ring::BYTES;
     int *table = reinterpret_cast<int *>(epi + p.epi);
-    uint64_t *full = reinterpret_cast<uint64_t *>(epi + p.epi + MM_TABLE);
+    constexpr int UNPACKERS = MM_WARP_OUT * 32;
+    float *own_scales = reinterpret_cast<float *>(epi + p.epi + MM_TABLE);     // [groups][thread]
+    uint64_t *full = reinterpret_cast<uint64_t *>(epi + p.epi + MM_TABLE +
+                                                  (IDX && p.idx_table ? m_groups(p) * UNPACKERS * 4 : 0));
     uint64_t *empty = full + MM_MAX_STAGES;
     uint64_t *tfull = empty + MM_MAX_STAGES;
     uint64_t *tempty = tfull + 2;
@@ -445,6 +451,15 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&wempty[wpos.stage]);
+                if constexpr (IDX) {
+                    // this thread's row of scales, in its own column of the table (forward: once a tile)
+                    const int n = DIR == 0 ? ch : step * MM_BK + arow;
+                    if (p.idx_table && n < m.w.N && (DIR == 1 || h < MM_SETS)) {
+                        const float *row = m.w.scales + (erow + n) * m.w.groups;
+#pragma unroll 8
+                        for (int q = 0; q < m.w.groups; ++q) own_scales[q * UNPACKERS + tid] = __ldg(row + q);
+                    }
+                }
                 uint32_t v[2][16];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -452,10 +467,14 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     if constexpr (IDX) {
                         const int n = DIR == 0 ? ch : step * MM_BK + arow;
                         const int c = DIR == 0 ? step * MM_BK + side * 64 + 32 * q : t.c0 + ahalf * 64 + 32 * q;
-                        if (n < m.w.N && c < m.w.K)
-                            scale32_by_index<T, B, true>(v[q], m.w.scales + (erow + n) * m.w.groups,
-                                                         m.w.g_idx + (int64_t)t.e * m.w.K, c, m.w.K, m.w.groups,
-                                                         m.status);
+                        if (c < m.w.K) {
+                            const int32_t *gi = m.w.g_idx + (int64_t)t.e * m.w.K;
+                            if (p.idx_table)
+                                scale32_by_table<T>(v[q], own_scales + tid, UNPACKERS, gi, c, m.w.K, m.w.groups, m.status);
+                            else if (n < m.w.N)
+                                scale32_by_index<T, B, true>(v[q], m.w.scales + (erow + n) * m.w.groups, gi, c, m.w.K,
+                                                             m.w.groups, m.status);
+                        }
                     } else {
                         if (p.fold) scale32<T>(v[q], sc[q]);
                     }
@@ -776,7 +795,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             float *d = dump + (r + j) * MM_LANES + wq * 32 + lane;
-                            const bool mine = shorts && (r + j) % split == (int)rank && r + j < t.n;
+                            // (split is a power of two)
+                            const bool mine = shorts && ((r + j) & (split - 1)) == (int)rank && r + j < t.n;
                             *d = mine ? *d + __uint_as_float(y[j]) : __uint_as_float(y[j]);
                         }
                     }
@@ -787,17 +807,41 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 bool all = tc::mbar_wait_cluster(ready, sum_phase, abort);
                 all = __all_sync(~0u, all) && ok;
                 if (all) {
+                    // a warp a row, four channels a lane; the blocks' sums are requested at once
+                    const int c4 = t.c0 + 4 * lane;
+                    float s4[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s4[j] = per_channel && c4 + j < p.out ? __ldg(m.w.scales + (int64_t)t.e * m.w.N + c4 + j) : 1.f;
 #pragma unroll 2
-                    for (int row = (int)rank; row < t.n; row += split) {
-                        float sum = 0.f;
-                        const uint32_t from = tc::smem_u32(dump + row * MM_LANES + wq * 32 + lane);
-                        for (int c = 0; c < split; ++c)
-                            sum += __uint_as_float(tc::ld_shared_cluster(tc::mapa_shared(from, c)));
-                        if (ch < p.out) Y[(t.t0 + row) * m.ldy + ch] = from_f32<T>(s * sum);
+                    for (int row = (int)rank + split * wq; row < t.n; row += 4 * split) {
+                        const uint32_t from = tc::smem_u32(dump + row * MM_LANES + 4 * lane);
+                        float4 v[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            v[c] = c < split ? tc::ld_shared_cluster_f4(tc::mapa_shared(from, c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        float4 sum = v[0];
+#pragma unroll
+                        for (int c = 1; c < 8; ++c) {
+                            sum.x += v[c].x; sum.y += v[c].y; sum.z += v[c].z; sum.w += v[c].w;
+                        }
+                        const uint32_t y0 = Half2<T>::pack(s4[0] * sum.x, s4[1] * sum.y);
+                        const uint32_t y1 = Half2<T>::pack(s4[2] * sum.z, s4[3] * sum.w);
+                        T *d = Y + (t.t0 + row) * m.ldy + c4;
+                        if (p.yvec && c4 + 4 <= p.out) {
+                            *reinterpret_cast<uint2 *>(d) = make_uint2(y0, y1);
+                        } else {
+                            uint16_t *e = reinterpret_cast<uint16_t *>(d);
+                            if (c4 < p.out) e[0] = (uint16_t)y0;
+                            if (c4 + 1 < p.out) e[1] = (uint16_t)(y0 >> 16);
+                            if (c4 + 2 < p.out) e[2] = (uint16_t)y1;
+                            if (c4 + 3 < p.out) e[3] = (uint16_t)(y1 >> 16);
+                        }
                     }
                 }
+                // before the next tile's sums (the release waits for the outputs, too: not for nothing)
                 __syncwarp();
-                if (lane < split)
+                if (u + ngroups < tiles && lane < split)
                     tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(done), lane));
                 sum_phase ^= 1;
             }
@@ -890,7 +934,6 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
             }
         } else {
-            const int tid = threadIdx.x - MM_WARP_WORDS * 32;
             const int nw = (int)(((int64_t)m.w.K * B + 31) / 32);
             for (int u = group; u < tiles && ok; u += ngroups) {
                 const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
@@ -901,14 +944,19 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     if (!ok) break;
                     const int w0 = ((DIR == 0 ? (k0 + i) * MM_BK : t.c0) >> 5) * B;
                     const int n0 = DIR == 0 ? t.c0 : (k0 + i) * MM_BK;
+                    // lanes take neighbouring words of as many whole rows as fit a warp
+                    constexpr int RW = 4 * B, PW = B == 3 ? 2 : 4, RL = 32 / RW;    // words of a row, of a piece; rows
                     const uint32_t dst = tc::smem_u32(words + stage * Ring::STAGE);
-                    constexpr int RW = 4 * B, PW = B == 3 ? 2 : 4;      // words of a row, of a piece
-#pragma unroll 4
-                    for (int j = tid; j < 128 * RW; j += 64) {
-                        const int r = j / RW, w = j - r * RW;
-                        const bool in = n0 + r < m.w.N && w0 + w < nw;
-                        copy_async<4>(dst + Ring::at(r, w / PW) + (w % PW) * 4,
-                                      in ? m.w.words + (erow + n0 + r) * m.w.ldw + w0 + w : nullptr, m.w.words);
+                    const int sub = lane / RW, wd = lane - sub * RW;
+                    if (sub < RL) {
+                        const bool in = w0 + wd < nw;
+                        const int first_row = (warp - MM_WARP_WORDS) * 64 + sub, left = m.w.N - n0;
+                        const uint32_t *src = m.w.words + (erow + n0 + first_row) * m.w.ldw + w0 + wd;
+                        const int64_t by = RL * m.w.ldw;
+#pragma unroll 8
+                        for (int r = first_row; r < (warp - MM_WARP_WORDS) * 64 + 64; r += RL, src += by)
+                            copy_async<4>(dst + Ring::at(r, wd / PW) + (wd % PW) * 4, in && r < left ? src : nullptr,
+                                          m.w.words);
                     }
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&wfull[stage]))
                                  : "memory");
@@ -1003,7 +1051,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
-    if (cluster > 1) tc::cluster_sync();    // no block leaves while others use its memory
+    if (cluster > 1) tc::cluster_sync_relaxed();    // no block leaves while others use its memory
     if (*abort && threadIdx.x == 0) set_status(m.status, GPTQ_ERR_TIMEOUT);
     if (warp == MM_WARP_MMA) {
         tc::fence_after_sync();
