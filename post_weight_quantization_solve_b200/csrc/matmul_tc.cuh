@@ -498,8 +498,9 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         for (int q = 0; q < 8; ++q) {
                             const uint32_t(&y)[16] = v[q >> 2];
                             const int j = 4 * (q & 3);
+                            // (rows past the layer's last: their scale is zero already)
                             *reinterpret_cast<uint4 *>(a + ((q ^ (arow & 7)) << 4)) =
-                                in ? make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]) : make_uint4(0u, 0u, 0u, 0u);
+                                !IDX || in ? make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]) : make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                     if (!tiled) {
