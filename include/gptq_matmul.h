@@ -84,7 +84,7 @@ GPTQ_API gptq_status gptq_matmul_grouped_dx(void *dX, int64_t lddx, const void *
  *            its values when accumulating).
  *   dY, X    device [M][lddy >= N], [M][ldx >= K], dtype GPTQ_BF16 or GPTQ_F16.
  *   offsets, status, errors: as gptq_matmul_grouped.
- *   Rows are added in order, in chains of 2,048 on the tensor cores and in fp32 to nearest
+ *   Rows are added in order, in chains of 512 on the tensor cores and in fp32 to nearest
  *   across chains; results do not change from call to call.
  */
 GPTQ_API gptq_status gptq_matmul_grouped_dw(float *dW, const void *dY, int64_t lddy, const void *X,
@@ -107,8 +107,8 @@ GPTQ_API gptq_status gptq_matmul_grouped_dw(float *dW, const void *dY, int64_t l
  *            checked as a whole as in gptq_matmul_grouped (ids in [-1, adapters)); rows
  *            outside [offsets[0], offsets[requests]) are left as they were.
  *   ws       gptq_lora_workspace_size(0, M, N, K, requests, adapters, rank) bytes.
- *   Arithmetic: fp32 sums; alpha A X is kept as a pair of dtype halves (16 bits for bf16,
- *            22 for fp16 inside its normal range; it must lie in fp16's range). Up to 16
+ *   Arithmetic: fp32 sums; alpha A X enters as two dtype parts that add up to it (16 bits
+ *            for bf16, 22 for fp16 inside its normal range; it must lie in fp16's range). Up to 16
  *            rows, W^ enters as in gptq_matmul_grouped; above, each weight is rounded
  *            once to dtype.
  *   Others as gptq_matmul_grouped. GPTQ_ERR_WORKSPACE for the workspace.
@@ -131,8 +131,8 @@ GPTQ_API gptq_status gptq_matmul_lora(void *Y, int64_t ldy, const void *X, int64
  *            added to: zeros for an adapter that no row uses.
  *   X        may be NULL when neither dA nor dB is wanted.
  *   ws       gptq_lora_workspace_size(1, M, N, K, requests, adapters, rank) bytes.
- *   Others as gptq_matmul_lora; T and U are kept as pairs of dtype halves, dA and dB are
- *   fp32 sums added in a fixed order.
+ *   Others as gptq_matmul_lora; T and U enter dA and dB as parts that add up to them (24 bits
+ *   for bf16, 22 for fp16 inside its normal range); dA and dB are fp32 sums in a fixed order.
  */
 GPTQ_API gptq_status gptq_matmul_lora_backward(void *dX, int64_t lddx, float *dA, float *dB,
                                                const void *dY, int64_t lddy, const void *X,

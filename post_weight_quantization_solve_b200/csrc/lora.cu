@@ -5,9 +5,9 @@
 //   U[t] = alpha_a B_a^T dY[t]     (gradients of X and A)
 //
 // Both are a thin product rows x [rank][inner], bound by reading the rows (long prompts) or the
-// adapters (requests that decode, each with an adapter of its own). The result leaves as a pair
-// of 16-bit halves [hi | lo], 16 bits of the fp32 sum, which the products that follow read as
-// matrix operands. Tiles of rows are cut inside each request, so a tile has one adapter.
+// adapters (requests that decode, each with an adapter of its own). The result leaves as
+// 16-bit parts that add up to the fp32 sum (two of fp16, three of bf16, side by side), which the
+// products that follow read as matrix operands. Tiles of rows are cut inside each request, so a tile has one adapter.
 //   k_rank_tc    prompts: the adapter is the A operand of tcgen05 (rank lanes), 64 rows the B
 //                operand, both by tiled copies in steps of 128 columns.
 //   k_rank_rows  a few rows, or layouts that tiled copies refuse: fragments of mma.sync m16n8k16
@@ -38,7 +38,7 @@ struct RankArg {
     const float *alpha;       // [L]
     const int32_t *offsets, *ids;
     int R, L, rank, inner;
-    void *T2;                 // [M][2 rank]
+    void *T2;                 // [M][LORA_HALVES rank]
     int xvec, avec, split;
     int32_t *status;
 };
@@ -120,13 +120,16 @@ __device__ __forceinline__ bool rank_tile(const RankArg &p, int64_t b, int rows,
     return n > 0;
 }
 
-// A rank-space value as its two halves.
+// A rank-space value as its parts.
 template <typename T>
-__device__ __forceinline__ void store_pair(T *d, int rank, float v) {
-    const T hi = from_f32<T>(v);
-    const float f = to_f32<T>(hi);
-    d[0] = hi;
-    d[rank] = from_f32<T>(isfinite(f) ? v - f : 0.f);      // an infinite half has no rest
+__device__ __forceinline__ void store_parts(T *d, int rank, float v) {
+#pragma unroll
+    for (int h = 0; h < LORA_HALVES<T>; ++h) {
+        const T x = from_f32<T>(v);
+        const float f = to_f32<T>(x);
+        d[h * rank] = x;
+        v = isfinite(f) ? v - f : 0.f;          // an infinite part has no rest
+    }
 }
 
 // Block (row tile, part of the contraction): MW warps of 16 rows x KW warps of the contraction;
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constan
         } else {
             sum = part[0][row][j];
         }
-        if (j < p.rank) store_pair<T>(out + ((int64_t)t + row) * 2 * p.rank + j, p.rank, alpha * sum);
+        if (j < p.rank) store_parts<T>(out + ((int64_t)t + row) * LORA_HALVES<T> * p.rank + j, p.rank, alpha * sum);
     }
     if (p.split > 1) tc::cluster_sync();
 }
@@ -215,10 +218,13 @@ constexpr int RK_A = 128 * RK_BK * 2;                   // 32 KB; only `rank` ro
 constexpr int RK_STAGE = RK_X + RK_A;
 constexpr int RK_SMEM = RK_STAGES * RK_STAGE + 1024 + 256;
 constexpr int RK_THREADS = 192;
+constexpr int RK_ACCS = 8;
 }  // namespace
 
 // Roles: warp 0 tiled copies, warp 1 TMEM and MMAs, warps 2-5 outputs. The lanes past the rank
-// multiply what the stage happens to hold; nothing reads them.
+// multiply what the stage happens to hold; nothing reads them. The steps go to eight accumulators
+// in turn, added in fp32 to nearest at the end: the tensor core's own accumulation rounds each
+// step the same way (one chain of 256 MMAs was 4e-6 off in the mean).
 template <typename T>
 __global__ void __launch_bounds__(RK_THREADS, 1)
     k_rank_tc(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
         tc::prefetch_tmap(&xmap);
         tc::prefetch_tmap(&amap);
     }
-    if (warp == 1) tc::tmem_alloc(tmem_slot, 64);
+    if (warp == 1) tc::tmem_alloc(tmem_slot, RK_ACCS * RK_ROWS);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -294,9 +300,9 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
                 if (tc::elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < RK_BK / 16; ++kk)
-                        tc::mma_bf16(tmem, ad0 + by + ((kk >> 2) * (RK_A / 2) + (kk & 3) * 32 >> 4),
+                        tc::mma_bf16(tmem + (i % RK_ACCS) * RK_ROWS, ad0 + by + ((kk >> 2) * (RK_A / 2) + (kk & 3) * 32 >> 4),
                                      bd0 + by + ((kk >> 2) * (RK_X / 2) + (kk & 3) * 32 >> 4), idesc,
-                                     (i > 0 || kk > 0) ? 1u : 0u);
+                                     (i >= RK_ACCS || kk > 0) ? 1u : 0u);
                     tc::mma_commit(&empty[stage]);
                 }
                 __syncwarp();
@@ -314,12 +320,19 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
             tc::fence_after_sync();
             if (ok && quad * 32 < p.rank) {
                 for (int c = 0; c < n16; c += 16) {
-                    uint32_t v[16];
-                    tc::tmem_ld_32x32b_x16(tmem + c + ((uint32_t)(quad * 32) << 16), v);
-                    tc::tmem_ld_wait();
+                    float add[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) add[q] = 0.f;
+                    for (int k = 0; k < min(RK_ACCS, s1 - s0); ++k) {
+                        uint32_t v[16];
+                        tc::tmem_ld_32x32b_x16(tmem + k * RK_ROWS + c + ((uint32_t)(quad * 32) << 16), v);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) add[q] += __uint_as_float(v[q]);
+                    }
                     if (j < p.rank) {
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) sums[(c + q) * p.rank + j] = __uint_as_float(v[q]);
+                        for (int q = 0; q < 16; ++q) sums[(c + q) * p.rank + j] = add[q];
                     }
                 }
             }
@@ -348,14 +361,14 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
             } else {
                 sum = sums[i];
             }
-            store_pair<T>(out + ((int64_t)t + row) * 2 * p.rank + j, p.rank, alpha * sum);
+            store_parts<T>(out + ((int64_t)t + row) * LORA_HALVES<T> * p.rank + j, p.rank, alpha * sum);
         }
     }
     if (p.split > 1) tc::cluster_sync();
     if (*abort && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_TIMEOUT);
     if (warp == 1) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, 64);
+        tc::tmem_dealloc(tmem, RK_ACCS * RK_ROWS);
     }
 }
 
@@ -479,11 +492,12 @@ struct LoraSpace {
 };
 
 static LoraSpace lora_space(void *ws, bool backward, int64_t M, int N, int K, int R, int L, int rank) {
+    constexpr int parts = 3;                            // room for either type
     Carver c(ws);
     LoraSpace s{};
-    s.T2 = c.take<uint16_t>((size_t)M * 2 * rank);
+    s.T2 = c.take<uint16_t>((size_t)M * parts * rank);
     if (backward) {
-        s.U2 = c.take<uint16_t>((size_t)M * 2 * rank);
+        s.U2 = c.take<uint16_t>((size_t)M * parts * rank);
         s.Bt = c.take<uint16_t>((size_t)L * N * rank);
         const size_t pb = (size_t)adapter_parts(M, L, N) * L * N * rank, pa = (size_t)adapter_parts(M, L, K) * L * K * rank;
         s.parts = c.take<float>(std::max(pa, pb));

@@ -31,10 +31,19 @@ struct PackedArg {
 // Adapters beside a product, and the rows that use them.
 struct LoraArg {
     const void *P;            // forward: B [L][N][rank]; input gradient: A [L][rank][K]
-    const void *T2;           // [M][2 rank]: hi and lo halves of the rank-space rows
+    const void *T2;           // [M][LORA_HALVES rank]: the rank-space rows as 16-bit parts
     const int32_t *ids;       // [R] adapter of each request, -1 none
     int R, L, rank;
 };
+
+// A rank-space value is kept as 16-bit parts that add up to it: two of fp16 (22 bits), three of
+// bf16 (24 bits). The adapters' gradients, fp32 sums, take all of them; the products whose
+// outputs are 16 bits wide take the first two.
+template <typename T>
+constexpr int LORA_HALVES = 2;
+template <>
+constexpr int LORA_HALVES<__nv_bfloat16> = 3;
+inline int lora_halves(int dtype) { return dtype == GPTQ_BF16 ? 3 : 2; }
 
 struct MatmulArg {
     PackedArg w;
@@ -432,7 +441,7 @@ __device__ __forceinline__ void lora_terms(const LoraArg &l, const int (&id)[NRO
         for (int i = 0; i < NROW; ++i) {
             hv[i] = lv[i] = pv[i] = make_uint4(0u, 0u, 0u, 0u);
             if (id[i] < 0) continue;
-            const T *h = static_cast<const T *>(l.T2) + t[i] * 2 * r + j;
+            const T *h = static_cast<const T *>(l.T2) + t[i] * LORA_HALVES<T> * r + j;
             hv[i] = __ldcg(reinterpret_cast<const uint4 *>(h));
             lv[i] = __ldcg(reinterpret_cast<const uint4 *>(h + r));
             if constexpr (DIR == 0) {

@@ -1,7 +1,7 @@
 // Products over the rows of each range: G_e (+)= sum over t of P[t]^T Q[t], fp32. The experts'
 // weight gradients (P = dY, Q = X), and the adapters' gradients, where the range of an adapter
-// is the rows of all requests that use it and Q is the rank-space matrix as a pair of 16-bit
-// halves [hi | lo], whose two products are added in the epilogue.
+// is the rows of all requests that use it and Q is the rank-space matrix as 16-bit parts side by
+// side, whose products are added in the epilogue.
 //
 // Both operands come straight from row-major matrices: rows are the contraction, so a box of
 // 128 rows x 64 columns in the 128-byte swizzle is an MN-major operand. The 128-row steps of a
@@ -13,15 +13,19 @@
 // (cta_group::2): each loads its own columns of P and half of Q's, 64 KB a step. Single blocks
 // take 128 columns of P x up to 256 of Q: narrow Q (adapters), and products with few tiles.
 //
-// The tensor core's fp32 accumulation rounds each step the same way, so a chain is at most
-// 2,048 rows (128 MMAs); longer ranges swap accumulators and the epilogue adds the next chain
-// to the stored sum in fp32 to nearest, in order, so results do not change from run to run.
-// Outputs leave through shared memory as tiled stores of 32 x 32 boxes (a later chain as tiled
-// adds, after the one before has completed): row by row from registers they took 25,000 clocks a
-// tile, three times its products. Layouts that tiled stores refuse go row by row.
+// The tensor core's fp32 accumulation rounds each step the same way, so a chain is 512 rows (32
+// MMAs) only: two accumulators in turn, and the epilogue adds each chain to its sums in registers,
+// in fp32 to nearest and in order. Mean error over 1,024 rows: 1.7e-6 in one chain, 4.7e-7 in
+// chains of 512 (plain fp32 sums: 3.4e-7), 2.5e-7 in chains of 256, at 245, 275 and 310 us for
+// eight experts of 4,096 x 4,096. Nothing is added across blocks, so results do not change from
+// run to run.
+// Outputs leave through shared memory as tiled stores (or adds) of 32 x 32 boxes: row by row they
+// took 25,000 clocks a tile, three times its products. Layouts that tiled stores refuse go row
+// by row.
 //
-// Roles (384 threads): warp 0 tiled copies, warp 1 TMEM and MMAs, warp 2 range ends, warps 4-7
-// epilogue, warps 8-11 plain copies where the layout refuses tiled ones.
+// Roles (384 threads): warp 0 tiled copies, warp 1 TMEM and MMAs, warp 2 range ends, warps 4-11
+// epilogue (half of the tile's columns each four); where the layout refuses tiled copies, warps 0,
+// 2 and 3 make plain ones.
 #include <algorithm>
 
 #include "matmul.cuh"
@@ -31,10 +35,10 @@ namespace gptq {
 namespace {
 constexpr int DW_LANES = 128, DW_COLS = 256, DW_BK = 128, DW_MAX_STAGES = 4;
 constexpr int DW_BOX = 128 * 64 * 2;                            // 16 KB
-constexpr int DW_EPI = 4 * 2 * 32 * 32 * 4;                     // two boxes a warp
+constexpr int DW_EPI = 8 * 32 * 33 * 4;                         // one box (or a padded one) a warp
 constexpr int DW_FIXED = DW_EPI + 1024 + 256;
 constexpr int DW_THREADS = 384;
-constexpr int DW_CHAIN = 16;                                    // steps of one accumulator
+constexpr int DW_CHAIN = 4;                                     // steps of one accumulator
 }  // namespace
 
 struct DwArg {
@@ -47,7 +51,9 @@ struct DwArg {
     int R, groups, L;
     const int32_t *ids;       // checked with the offsets when given
     int split;                // parts of a group's steps; each writes its own output
-    int pair;                 // Q is [hi | lo]: columns j and j + nq / 2 are added
+    // Q is `parts` parts of `rank` columns side by side, added in the epilogue (1: plain). Where they
+    // do not fit a tile together (apart), a tile takes 64 columns of each, a box a part.
+    int parts, rank, apart;
     int transposed;           // output [q][p] instead of [p][q]
     int accumulate;
     float *out;               // [split][groups][np][nq'] (or [nq'][np])
@@ -150,15 +156,15 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? tc::cluster_ctarank() : 0u;
     if (threadIdx.x == 0) {
-        // tiled: the copies' warp of each block, or its warp for range ends; plain: four warps each
+        // tiled: the copies' warp of each block, or its warp for range ends; plain: three warps each
         for (int s = 0; s < stages; ++s) {
-            tc::mbar_init(&full[s], (p.tiled ? 1 : 4) * (PAIR ? 2 : 1));
+            tc::mbar_init(&full[s], (p.tiled ? 1 : 3) * (PAIR ? 2 : 1));
             tc::mbar_init(&empty[s], 1);
             tc::mbar_init(&tail[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&tfull[b], 1);
-            tc::mbar_init(&tempty[b], PAIR ? 8 : 4);
+            tc::mbar_init(&tempty[b], PAIR ? 16 : 8);
         }
         tc::mbar_init(drain, 1);
         *abort = 0;
@@ -192,7 +198,10 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     if constexpr (PAIR) skip = (int)tc::ld_shared_cluster(tc::mapa_shared(tc::smem_u32(refuse), 0));
 
     constexpr int PW = PAIR ? 2 * DW_LANES : DW_LANES;
-    const int tp = (p.np + PW - 1) / PW, tq = (p.nq + DW_COLS - 1) / DW_COLS;
+    const int nout = p.parts > 1 ? p.rank : p.nq;       // columns of the outputs
+    const int qw = p.apart ? 64 : DW_COLS;              // of them a tile
+    const int tp = (p.np + PW - 1) / PW, tq = (nout + qw - 1) / qw;
+    const int qstep = p.apart ? p.rank : 64;            // from one box of Q to the next
     const int per_group = tp * tq * p.split;
     const int64_t units = skip ? 0 : (int64_t)p.groups * per_group;
     const int64_t first = blockIdx.x / (PAIR ? 2 : 1), by = gridDim.x / (PAIR ? 2 : 1);
@@ -214,8 +223,8 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         t.s0 = (int)((int64_t)n * part / p.split);
         t.s1 = (int)((int64_t)n * (part + 1) / p.split);
         // columns that the MMAs take: multiples of 16 (a pair: all 256, zeros past Q's end)
-        t.cols = PAIR ? DW_COLS : min(DW_COLS, (p.nq - t.qt * DW_COLS + 15) & ~15);
-        t.qc = t.qt * DW_COLS + (PAIR ? (int)rank * (DW_COLS / 2) : 0);
+        t.cols = PAIR ? DW_COLS : p.apart ? p.parts * 64 : min(DW_COLS, (p.nq - t.qt * DW_COLS + 15) & ~15);
+        t.qc = t.qt * qw + (PAIR ? (int)rank * (DW_COLS / 2) : 0);
         t.qb = PAIR ? 2 : (t.cols + 63) / 64;
         return t;
     };
@@ -246,7 +255,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                         uint64_t *bar = ends ? &tail[stage] : &full[stage];
                         tc::mbar_arrive_expect_tx(bar, bytes);
                         for (int i = 0; i < 2; ++i) tc::tma_load_2d(a + i * DW_BOX, &pmap, bar, x0 + 64 * i, y);
-                        for (int i = 0; i < t.qb; ++i) tc::tma_load_2d(b + i * DW_BOX, &qmap, bar, x1 + 64 * i, y);
+                        for (int i = 0; i < t.qb; ++i) tc::tma_load_2d(b + i * DW_BOX, &qmap, bar, x1 + qstep * i, y);
                     } else {
                         if (rank == 0) tc::mbar_arrive_expect_tx(&full[stage], 2 * bytes);
                         const uint32_t fb = tc::mapa_shared(tc::smem_u32(&full[stage]), 0);
@@ -356,111 +365,104 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                 tc::mbar_wait(drain, 0, &never);
             }
         }
-    } else if (warp >= 4 && warp < 8) {
-        const int quad = warp & 3;
-        uint8_t *boxes = reinterpret_cast<uint8_t *>(epi) + quad * 8192;
-        float *buf = reinterpret_cast<float *>(boxes);      // or [32][33]
-        int box = 0;
+    } else if (warp >= 4) {
+        const int quad = warp & 3, side = (warp >> 2) - 1;
+        uint8_t *box = reinterpret_cast<uint8_t *>(epi) + (warp - 4) * 4096;            // swizzled, or
+        float *buf = epi + (warp - 4) * 32 * 33;                                        // [32][33]
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        const int half = p.pair ? p.nq / 2 : 0, nout = p.pair ? half : p.nq;
+        const int spacing = p.apart ? 64 : nout;       // of the parts in the accumulator
+        // this warp's columns of a tile: up to 128 from `side` times 128 (parts: 64)
+        const int own = p.parts > 1 ? 64 : 128;
         for (int64_t u = first; u < units && ok; u += by) {
             const Unit t = unit(u);
             const int part = (int)(u / (tp * tq)) % p.split;
             float *out = p.out + ((int64_t)part * p.groups + t.g) * p.np * nout;
-            const int r0 = t.pc + quad * 32;
-            const int chains = max(1, (t.s1 - t.s0 + DW_CHAIN - 1) / DW_CHAIN);
-            for (int c = 0; c < chains && ok; ++c) {
-                const bool none = t.s1 == t.s0;         // a range without rows: zeros
-                if (!none) {
-                    ok = __all_sync(~0u, tc::mbar_wait(&tfull[acc], acc_phase, abort));
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                }
-                const bool add = p.accumulate || c > 0;
-                const int qn = min(DW_COLS, nout - t.qt * DW_COLS);
-                if (!(none && add)) {
+            const int r0 = t.pc + quad * 32, c0 = side * own;
+            const int qn = max(0, min(own, min(qw, nout - t.qt * qw) - c0));                // columns it has
+            const int chains = (t.s1 - t.s0 + DW_CHAIN - 1) / DW_CHAIN;                     // none: zeros
+            float sum[128];
+#pragma unroll
+            for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+            for (int c = 0; c < chains; ++c) {
+                ok = __all_sync(~0u, tc::mbar_wait(&tfull[acc], acc_phase, abort));
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t at = tmem + acc * DW_COLS + c0 + ((uint32_t)(quad * 32) << 16);
+#pragma unroll
+                for (int cb = 0; cb < 8; ++cb) {
+                    if (cb * 16 >= qn) break;
 #pragma unroll 1
-                    for (int cb = 0; cb < qn; cb += 32) {
-                        uint32_t v[32];
+                    for (int h = 0; h < p.parts; ++h) {
+                        uint32_t v[16];
+                        tc::tmem_ld_32x32b_x16(at + cb * 16 + h * spacing, v);
+                        tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0u;
-                        if (!none) {
-                            const uint32_t at = tmem + acc * DW_COLS + cb + ((uint32_t)(quad * 32) << 16);
-                            tc::tmem_ld_32x32b_x32(at, v);
-                            tc::tmem_ld_wait();
-                            if (p.pair) {
-                                uint32_t w[32];
-                                tc::tmem_ld_32x32b_x32(at + half, w);
-                                tc::tmem_ld_wait();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
-                            }
-                        }
-                        const int q0 = t.qt * DW_COLS + cb;
-                        if (p.tstore) {
-                            // row = lane, 16-byte piece q at q ^ (lane & 7); the box two stores ago is free
-                            uint8_t *to = boxes + box * 4096;
-                            box ^= 1;
-                            if (lane == 0) tc::bulk_wait_read<1>();
-                            __syncwarp();
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                *reinterpret_cast<uint4 *>(to + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-                                    make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                            tc::fence_async_shared();
-                            __syncwarp();
-                            if (lane == 0 && r0 < p.np) {
-                                if (add) tc::tma_reduce_add_3d(&omap, to, q0, r0, t.g);
-                                else tc::tma_store_3d(&omap, to, q0, r0, t.g);
-                                tc::bulk_commit();
-                            }
-                        } else if (p.transposed) {
-                            if (r0 + lane < p.np) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (cb + i < qn) {
-                                        float *d = out + (int64_t)(q0 + i) * p.np + r0 + lane;
-                                        *d = add ? *d + __uint_as_float(v[i]) : __uint_as_float(v[i]);
-                                    }
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = __uint_as_float(v[i]);
-                            __syncwarp();
-                            const int rows = min(32, p.np - r0);
-                            if (cb + lane < qn) {
-                                float *d = out + (int64_t)r0 * nout + q0 + lane;
-                                if (add) {
-#pragma unroll 8
-                                    for (int i = 0; i < rows; ++i) d[(int64_t)i * nout] += buf[i * 33 + lane];
-                                } else {
-#pragma unroll 8
-                                    for (int i = 0; i < rows; ++i) d[(int64_t)i * nout] = buf[i * 33 + lane];
-                                }
-                            }
-                            __syncwarp();
-                        }
+                        for (int i = 0; i < 16; ++i) sum[cb * 16 + i] += __uint_as_float(v[i]);
                     }
                 }
-                // the next chain adds to what this one stored
-                if (p.tstore && chains > 1 && lane == 0) tc::bulk_wait_all();
-                if (!none) {
-                    tc::fence_before_sync();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR && rank != 0) tc::mbar_arrive_remote(tc::mapa_shared(tc::smem_u32(&tempty[acc]), 0));
+                    else tc::mbar_arrive(&tempty[acc]);
+                }
+                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            }
+            if (!ok) break;
+            if (chains == 0 && p.accumulate) continue;
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) {
+                if (cb * 32 >= qn) break;
+                const int q0 = t.qt * qw + c0 + cb * 32, cols = min(32, qn - cb * 32);
+                if (p.tstore) {
+                    // row = lane, 16-byte piece q at q ^ (lane & 7), once the box is free again
+                    if (lane == 0) tc::bulk_wait_read<0>();
                     __syncwarp();
-                    if (lane == 0) {
-                        if (PAIR && rank != 0) tc::mbar_arrive_remote(tc::mapa_shared(tc::smem_u32(&tempty[acc]), 0));
-                        else tc::mbar_arrive(&tempty[acc]);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<float4 *>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                            make_float4(sum[cb * 32 + 4 * q], sum[cb * 32 + 4 * q + 1], sum[cb * 32 + 4 * q + 2],
+                                        sum[cb * 32 + 4 * q + 3]);
+                    tc::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0 && r0 < p.np) {
+                        if (p.accumulate) tc::tma_reduce_add_3d(&omap, box, q0, r0, t.g);
+                        else tc::tma_store_3d(&omap, box, q0, r0, t.g);
+                        tc::bulk_commit();
                     }
-                    if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                } else if (p.transposed) {
+                    if (r0 + lane < p.np) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < cols) {
+                                float *d = out + (int64_t)(q0 + i) * p.np + r0 + lane;
+                                *d = p.accumulate ? *d + sum[cb * 32 + i] : sum[cb * 32 + i];
+                            }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = sum[cb * 32 + i];
+                    __syncwarp();
+                    const int rows = min(32, p.np - r0);
+                    if (lane < cols) {
+                        float *d = out + (int64_t)r0 * nout + q0 + lane;
+                        if (p.accumulate) {
+#pragma unroll 8
+                            for (int i = 0; i < rows; ++i) d[(int64_t)i * nout] += buf[i * 33 + lane];
+                        } else {
+#pragma unroll 8
+                            for (int i = 0; i < rows; ++i) d[(int64_t)i * nout] = buf[i * 33 + lane];
+                        }
+                    }
+                    __syncwarp();
                 }
             }
         }
         if (lane == 0) tc::bulk_wait_all();
-    } else if (warp >= 8 && !p.tiled) {
-        const int tid = threadIdx.x - 256;
+    } else if (!p.tiled) {
+        const int tid = (warp == 0 ? 0 : warp - 1) * 32 + lane;         // warps 0, 2, 3
         const T *P = static_cast<const T *>(p.P), *Q = static_cast<const T *>(p.Q);
         int stage = 0;
         uint32_t phase = 0;
@@ -470,14 +472,14 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
             StepWalk walk(p, t.g, t.s0, t.s1);
             int64_t r;
             int n;
-            while (ok && walk.next(r, n)) {
+            while (walk.next(r, n)) {
                 ok = __all_sync(~0u, tc::mbar_wait(&empty[stage], phase ^ 1, abort));
                 if (!ok) break;
                 uint8_t *a = smem + stage * stage_bytes, *b = a + 2 * DW_BOX;
                 for (int i = 0; i < 2; ++i)
-                    dw_plain_box<T>(a + i * DW_BOX, P, p.ldp, r, n, t.pc + 64 * i, p.np, (p.vec & 1) != 0, tid, 128);
+                    dw_plain_box<T>(a + i * DW_BOX, P, p.ldp, r, n, t.pc + 64 * i, p.np, (p.vec & 1) != 0, tid, 96);
                 for (int i = 0; i < t.qb; ++i)
-                    dw_plain_box<T>(b + i * DW_BOX, Q, p.ldq, r, n, t.qc + 64 * i, p.nq, (p.vec & 2) != 0, tid, 128);
+                    dw_plain_box<T>(b + i * DW_BOX, Q, p.ldq, r, n, t.qc + qstep * i, p.nq, (p.vec & 2) != 0, tid, 96);
                 tc::fence_async_shared();
                 __syncwarp();
                 if (lane == 0) arrive_full(stage);
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(256) k_sum_parts(const float *__restrict__ par
 // The outputs [groups][np][nq] as boxes of 32 x 32 of one group.
 static bool out_map(CUtensorMap *map, const DwArg &p) {
     EncodeTiled enc = encode_tiled();
-    if (!enc || p.pair || p.split != 1 || !aligned(p.out, 16) || p.nq % 4 != 0) return false;
+    if (!enc || p.parts > 1 || p.split != 1 || !aligned(p.out, 16) || p.nq % 4 != 0) return false;
     const cuuint64_t dim[3] = {(cuuint64_t)p.nq, (cuuint64_t)p.np, (cuuint64_t)p.groups};
     const cuuint64_t stride[2] = {(cuuint64_t)p.nq * 4, (cuuint64_t)p.nq * 4 * p.np};
     const cuuint32_t box[3] = {32, 32, 1}, step[3] = {1, 1, 1};
@@ -529,11 +531,12 @@ static gptq_status launch_dw(DwArg &p, int dtype, cudaStream_t st) {
               rows_map(&qm, p.Q, dtype, p.M, p.nq, p.ldq, DW_BK);
     p.vec = (aligned(p.P, 16) && p.ldp % 8 == 0 ? 1 : 0) | (aligned(p.Q, 16) && p.ldq % 8 == 0 ? 2 : 0);
     auto units = [&](int pw) {
-        return (int64_t)((p.np + pw - 1) / pw) * ((p.nq + DW_COLS - 1) / DW_COLS) * p.groups * p.split;
+        const int nout = p.parts > 1 ? p.rank : p.nq, qw = p.apart ? 64 : DW_COLS;
+        return (int64_t)((p.np + pw - 1) / pw) * ((nout + qw - 1) / qw) * p.groups * p.split;
     };
     // pairs where both operands fill their tiles and there are pairs enough for the machine
-    const bool pair = !p.pair && p.np > DW_LANES && p.nq > DW_COLS / 2 && 2 * units(2 * DW_LANES) >= device_sms();
-    p.boxes = pair ? 4 : 2 + (std::min(p.nq, DW_COLS) + 63) / 64;
+    const bool pair = p.parts == 1 && p.np > DW_LANES && p.nq > DW_COLS / 2 && 2 * units(2 * DW_LANES) >= device_sms();
+    p.boxes = pair ? 4 : p.apart ? 2 + p.parts : 2 + (std::min(p.nq, DW_COLS) + 63) / 64;
     p.stages = std::min(DW_MAX_STAGES, (227 * 1024 - DW_FIXED) / (p.boxes * DW_BOX));
     const size_t smem = (size_t)p.stages * p.boxes * DW_BOX + DW_FIXED;
     const int blocks = pair ? (int)std::min<int64_t>(units(2 * DW_LANES), device_sms() / 2) * 2
@@ -555,7 +558,7 @@ gptq_status matmul_dw(float *G, const void *dY, int64_t lddy, const void *X, int
     p.M = M;
     p.offsets = offsets;
     p.R = p.groups = E;
-    p.split = 1;
+    p.split = p.parts = 1;
     p.accumulate = accumulate;
     p.out = G;
     p.status = status;
@@ -578,7 +581,10 @@ gptq_status adapter_gradient(float *out, float *parts, int split, const void *P,
                              const int32_t *list, int R, int L, int32_t *status, cudaStream_t st) {
     DwArg p{};
     p.P = P; p.ldp = ldp; p.np = np;
-    p.Q = T2; p.ldq = 2 * rank; p.nq = 2 * rank;
+    p.parts = lora_halves(dtype);
+    p.rank = rank;
+    p.Q = T2; p.ldq = p.nq = p.parts * rank;
+    p.apart = p.nq > DW_COLS;
     p.M = M;
     p.offsets = offsets;
     p.list_off = list_off;
@@ -587,7 +593,6 @@ gptq_status adapter_gradient(float *out, float *parts, int split, const void *P,
     p.groups = p.L = L;
     p.ids = ids;
     p.split = split;
-    p.pair = 1;
     p.transposed = transposed;
     p.out = split > 1 ? parts : out;
     p.status = status;

@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                                 const int tr = row0 + row;
                                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
                                 if (tr >= run_begin && tr < run_end && col < two_r)
-                                    x = __ldcg(reinterpret_cast<const uint4 *>(T2 + (t.t0 + tr) * two_r + col));
+                                    x = __ldcg(reinterpret_cast<const uint4 *>(T2 + (t.t0 + tr) * (LORA_HALVES<T> * r) + col));
                                 *reinterpret_cast<uint4 *>(st + side * MM_HALF + row * 128 + ((q ^ (row & 7)) << 4)) = x;
                             }
                             tc::fence_async_shared();

@@ -200,9 +200,9 @@ def test_weight_gradient(dtype, counts, N, K, accumulate):
     d, x = np.nan_to_num(f64(dY)), np.nan_to_num(f64(X), posinf=0)
     want = ref.grouped_dw(d, x, o) + (start if accumulate else 0)
     S = ref.grouped_dw(np.abs(d), np.abs(x), o) + np.abs(start)
-    # fp32: products are exact, a truncating sum of up to 2,048 terms and the chains' sums
+    # fp32: products are exact, a truncating sum of up to 512 terms and the chains' sums
     n = max(counts)
-    check(f64(out), want, (min(n, 2048) + 4) * 2.0 ** -23 * S + 1e-30)
+    check(f64(out), want, (min(n, 512) + n // 512 + 4) * 2.0 ** -23 * S + 1e-30)
     again = dev(start) if accumulate else torch.empty_like(out)
     gq.gptq_matmul_grouped_dw(dY, X, dev(o), out=again, accumulate=accumulate)
     assert torch.equal(again, out)
@@ -224,8 +224,13 @@ def lora_case(seed, dtype, bits, groupsize, counts, ids, adapters, rank, N, K, f
 
 
 def pair_eps(t):
-    """A rank-space row is kept as two halves: half a step of the second one."""
+    """A rank-space row enters 16-bit outputs as two parts: half a step of the second one."""
     return (torch.finfo(t).eps / 2) ** 2
+
+
+def part_eps(t):
+    """It enters the fp32 gradients as all its parts, three of bf16 and two of fp16."""
+    return (torch.finfo(t).eps / 2) ** (3 if t == torch.bfloat16 else 2)
 
 
 def check_lora(c, y, start):
@@ -273,13 +278,13 @@ def test_lora_backward(counts, ids, dtype, bits, groupsize, rank, N, K):
     al = c["alpha"].astype(np.float64)
     want = ref.lora_backward(*arrays, al, o, c["ids"], np.full((c["M"], K), 7.0))
     S = ref.lora_backward(*map(np.abs, arrays), al, o, c["ids"], np.zeros((c["M"], K)))
-    pe = 2 * pair_eps(t)
-    # fp16's second half has a fixed smallest step: 2^-25 a value of T or U
+    pe, ge = 2 * pair_eps(t), 2 * part_eps(t)
+    # fp16's second part has a fixed smallest step: 2^-25 a value of T or U
     floor = 2.0 ** -24 if t == torch.float16 else 0.0
     check(f64(dX), want[0], limit(want[0], S[0], N + 2 * rank, t, 1) + pe * S[0] + floor * rank * np.abs(arrays[3]).max())
     m = int(o[-1] - o[0])
     for got, w, s, other in ((dA, want[1], S[1], arrays[1]), (dB, want[2], S[2], arrays[0])):
-        check(f64(got), w, ((max(N, K) + min(m, 2048) + 20) * 2.0 ** -23 + pe) * s
+        check(f64(got), w, ((max(N, K) + min(m, 512) + m // 512 + 20) * 2.0 ** -23 + ge) * s
               + floor * m * np.abs(other).max() + 1e-30)
     # each gradient alone, and again: the same bits
     only = gq.gptq_matmul_lora_backward(c["dY"], c["X"], *c["args"], want=(False, True, False))
