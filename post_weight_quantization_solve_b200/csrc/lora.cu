@@ -15,7 +15,7 @@
 //                its row and of its adapter row, which permutes the contraction index alike on
 //                both sides.
 // A cluster of up to 8 blocks shares the contraction of a tile when there are few tiles.
-// B_a is stored [N][rank]; its gradient pass reads it transposed once (k_transpose).
+// B_a is stored [N][rank]; the backward pass reads it transposed (k_lora_setup).
 #include <algorithm>
 
 #include "matmul.cuh"
@@ -23,10 +23,9 @@
 namespace gptq {
 
 int adapter_parts(int64_t M, int L, int width);
-gptq_status adapter_gradient(float *out, float *parts, int split, const void *P, int64_t ldp, int np,
-                             const void *T2, int rank, int transposed, int dtype, int64_t M,
-                             const int32_t *offsets, const int32_t *ids, const int32_t *list_off,
-                             const int32_t *list, int R, int L, int32_t *status, cudaStream_t st);
+gptq_status adapter_gradients(const AdapterGrad *grads, int count, int rank, int dtype, int64_t M,
+                              const int32_t *offsets, const int32_t *ids, const int32_t *list_off,
+                              const int32_t *list, int R, int L, int32_t *status, cudaStream_t st);
 gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStream_t st);
 gptq_status matmul_token(const MatmulArg &m, int dtype, int bits, cudaStream_t st);
 bool matmul_few_rows(int64_t M, int E);
@@ -41,6 +40,14 @@ struct RankArg {
     void *T2;                 // [M][LORA_HALVES rank]
     int xvec, avec, split;
     int32_t *status;
+};
+
+// One launch makes T or U, or both (blockIdx.y).
+struct RankArgs {
+    RankArg a[2];
+};
+struct RankMaps {
+    CUtensorMap x[2], a[2];
 };
 
 template <typename T>
@@ -135,7 +142,8 @@ __device__ __forceinline__ void store_parts(T *d, int rank, float v) {
 // Block (row tile, part of the contraction): MW warps of 16 rows x KW warps of the contraction;
 // a cluster of `split` blocks shares a tile's contraction.
 template <typename T, int NR, int MW, int KW>
-__global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constant__ RankArg p) {
+__global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constant__ RankArgs args) {
+    const RankArg &p = args.a[blockIdx.y];
     constexpr int THREADS = MW * KW * 32, ROWS = 16 * MW;
     __shared__ float part[KW][ROWS][NR * 8 + 1];
     __shared__ int found[4];
@@ -227,8 +235,9 @@ constexpr int RK_ACCS = 8;
 // step the same way (one chain of 256 MMAs was 4e-6 off in the mean).
 template <typename T>
 __global__ void __launch_bounds__(RK_THREADS, 1)
-    k_rank_tc(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
-              const __grid_constant__ RankArg p) {
+    k_rank_tc(const __grid_constant__ RankMaps maps, const __grid_constant__ RankArgs args) {
+    const RankArg &p = args.a[blockIdx.y];
+    const CUtensorMap *xmap = &maps.x[blockIdx.y], *amap = &maps.a[blockIdx.y];
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -248,8 +257,8 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
         tc::mbar_init(tfull, 1);
         *abort = 0;
         tc::fence_mbar_init();
-        tc::prefetch_tmap(&xmap);
-        tc::prefetch_tmap(&amap);
+        tc::prefetch_tmap(xmap);
+        tc::prefetch_tmap(amap);
     }
     if (warp == 1) tc::tmem_alloc(tmem_slot, RK_ACCS * RK_ROWS);
     tc::fence_before_sync();
@@ -274,10 +283,10 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
                 uint8_t *x = smem + stage * RK_STAGE, *a = x + RK_X;
                 if (tc::elect_one()) {
                     tc::mbar_arrive_expect_tx(&full[stage], RK_X + p.rank * 256);
-                    tc::tma_load_2d(x, &xmap, &full[stage], s * RK_BK, t);
-                    tc::tma_load_2d(x + RK_X / 2, &xmap, &full[stage], s * RK_BK + 64, t);
-                    tc::tma_load_2d(a, &amap, &full[stage], s * RK_BK, id * p.rank);
-                    tc::tma_load_2d(a + RK_A / 2, &amap, &full[stage], s * RK_BK + 64, id * p.rank);
+                    tc::tma_load_2d(x, xmap, &full[stage], s * RK_BK, t);
+                    tc::tma_load_2d(x + RK_X / 2, xmap, &full[stage], s * RK_BK + 64, t);
+                    tc::tma_load_2d(a, amap, &full[stage], s * RK_BK, id * p.rank);
+                    tc::tma_load_2d(a + RK_A / 2, amap, &full[stage], s * RK_BK + 64, id * p.rank);
                 }
                 __syncwarp();
             }
@@ -373,78 +382,75 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
 }
 
 template <typename T, int NR>
-static gptq_status launch_rank_nr(RankArg &p, cudaStream_t st) {
+static gptq_status launch_rank_nr(RankArgs &q, int count, cudaStream_t st) {
+    const RankArg &p = q.a[0];
     if (p.M >= 1024) {
         // many rows in a layout that tiled copies refuse: 64 rows a block share the adapter
         constexpr int KW = NR > 8 ? 1 : 2;
-        p.split = 1;
-        return launch_pdl(k_rank_rows<T, NR, 4, KW>, dim3((unsigned)(p.R + p.M / 64)), 128 * KW, 0, 1, st, p);
+        for (int i = 0; i < count; ++i) q.a[i].split = 1;
+        return launch_pdl(k_rank_rows<T, NR, 4, KW>, dim3((unsigned)(p.R + p.M / 64), count), 128 * KW, 0, 1, st, q);
     }
     constexpr int KW = NR > 8 ? 4 : 8;
-    const int steps = (p.inner + 31) / 32;
-    p.split = 1;
+    const int steps = (std::min(p.inner, q.a[count - 1].inner) + 31) / 32;
+    int split = 1;
     const int64_t tiles = std::min<int64_t>(p.M, p.R + p.M / 16);
-    while (p.split < 8 && tiles * p.split * 2 <= 2 * device_sms() && steps >= 4 * KW * p.split) p.split *= 2;
-    return launch_pdl(k_rank_rows<T, NR, 1, KW>, dim3((unsigned)(tiles * p.split)), 32 * KW, 0, p.split, st, p);
+    while (split < 8 && tiles * count * split * 2 <= 2 * device_sms() && steps >= 4 * KW * split) split *= 2;
+    for (int i = 0; i < count; ++i) q.a[i].split = split;
+    return launch_pdl(k_rank_rows<T, NR, 1, KW>, dim3((unsigned)(tiles * split), count), 32 * KW, 0, split, st, q);
 }
 
 template <typename T>
-static gptq_status launch_rank(RankArg &p, int dtype, cudaStream_t st) {
+static gptq_status launch_rank(RankArgs &q, int count, int dtype, cudaStream_t st) {
+    const RankArg &p = q.a[0];
     // prompts: 64 rows a tile. The bound on short requests is that of tiles that a few rows fill.
     if (p.M >= 256 && p.M >= 16 * (int64_t)p.R) {
-        CUtensorMap xm{}, am{};
-        if (rows_map(&xm, p.X, dtype, p.M, p.inner, p.ldx, RK_ROWS) &&
-            rows_map(&am, p.A, dtype, (int64_t)p.L * p.rank, p.inner, p.inner, p.rank)) {
+        RankMaps maps{};
+        bool tiled = true;
+        for (int i = 0; i < count; ++i) {
+            const RankArg &r = q.a[i];
+            tiled = tiled && rows_map(&maps.x[i], r.X, dtype, r.M, r.inner, r.ldx, RK_ROWS) &&
+                    rows_map(&maps.a[i], r.A, dtype, (int64_t)r.L * r.rank, r.inner, r.inner, r.rank);
+        }
+        if (tiled) {
             const int64_t tiles = p.R + p.M / RK_ROWS;
-            const int steps = (p.inner + RK_BK - 1) / RK_BK;
-            p.split = 1;
-            while (p.split < 8 && tiles * p.split * 2 <= device_sms() && steps >= 4 * p.split) p.split *= 2;
-            return launch_pdl(k_rank_tc<T>, dim3((unsigned)(tiles * p.split)), RK_THREADS, RK_SMEM, p.split, st, xm,
-                              am, p);
+            const int steps = (std::min(p.inner, q.a[count - 1].inner) + RK_BK - 1) / RK_BK;
+            int split = 1;
+            while (split < 8 && tiles * count * split * 2 <= device_sms() && steps >= 4 * split) split *= 2;
+            for (int i = 0; i < count; ++i) q.a[i].split = split;
+            return launch_pdl(k_rank_tc<T>, dim3((unsigned)(tiles * split), count), RK_THREADS, RK_SMEM, split, st,
+                              maps, q);
         }
     }
-    if (p.rank <= 8) return launch_rank_nr<T, 1>(p, st);
-    if (p.rank <= 16) return launch_rank_nr<T, 2>(p, st);
-    if (p.rank <= 32) return launch_rank_nr<T, 4>(p, st);
-    if (p.rank <= 64) return launch_rank_nr<T, 8>(p, st);
-    return launch_rank_nr<T, 16>(p, st);
+    if (p.rank <= 8) return launch_rank_nr<T, 1>(q, count, st);
+    if (p.rank <= 16) return launch_rank_nr<T, 2>(q, count, st);
+    if (p.rank <= 32) return launch_rank_nr<T, 4>(q, count, st);
+    if (p.rank <= 64) return launch_rank_nr<T, 8>(q, count, st);
+    return launch_rank_nr<T, 16>(q, count, st);
 }
 
+// What the backward pass needs first. Block 0: the requests of each adapter, in request order
+// (list_off [L + 1], list [R]; a thread takes whole adapters, so the order is fixed). The others:
 // out[l][j][n] = in[l][n][j], 16-bit elements, 32 x 32 tiles through shared memory.
-__global__ void __launch_bounds__(256) k_transpose(const uint16_t *__restrict__ in, uint16_t *__restrict__ out,
-                                                   int N, int r) {
-    __shared__ uint16_t tile[32][34];
-    grid_dependency();
-    const int n0 = blockIdx.x * 32, j0 = blockIdx.y * 32;
-    const int64_t base = (int64_t)blockIdx.z * N * r;
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    for (int i = y; i < 32; i += 8)
-        if (n0 + i < N && j0 + x < r) tile[i][x] = in[base + (int64_t)(n0 + i) * r + j0 + x];
-    __syncthreads();
-    for (int i = y; i < 32; i += 8)
-        if (j0 + i < r && n0 + x < N) out[base + (int64_t)(j0 + i) * N + n0 + x] = tile[x][i];
-}
+struct SetupArg {
+    const int32_t *ids;
+    int R, L;
+    int32_t *list_off, *list, *status;
+    const uint16_t *in;
+    uint16_t *out;
+    int N, r;
+};
 
-// Requests of each adapter, in request order: list_off [L + 1], list [R]. One block; a thread
-// takes whole adapters, so the order is fixed.
-__global__ void __launch_bounds__(256) k_adapter_lists(const int32_t *__restrict__ ids, int R, int L,
-                                                       int32_t *list_off, int32_t *list, int32_t *status) {
-    __shared__ int bad, warp_sum[8], base;
-    grid_dependency();
-    if (threadIdx.x == 0) {
-        bad = 0;
-        base = 0;
-    }
-    __syncthreads();
-    if (ids_bad(ids, R, L, threadIdx.x, 256)) bad = 1;
-    __syncthreads();
-    if (bad && threadIdx.x == 0) set_status(status, GPTQ_ERR_ARG);
+__device__ __forceinline__ void adapter_lists(const SetupArg &p) {
+    __shared__ int warp_sum[8], base;
+    if (threadIdx.x == 0) base = 0;
+    const bool bad = __syncthreads_or(ids_bad(p.ids, p.R, p.L, threadIdx.x, 256));
+    if (bad && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_ARG);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int a0 = 0; a0 < L; a0 += 256) {
+    for (int a0 = 0; a0 < p.L; a0 += 256) {
         const int a = a0 + threadIdx.x;
         int n = 0;
-        if (a < L && !bad)
-            for (int i = 0; i < R; ++i) n += __ldg(ids + i) == a;
+        if (a < p.L && !bad)
+            for (int i = 0; i < p.R; ++i) n += __ldg(p.ids + i) == a;
         int sum = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -455,38 +461,62 @@ __global__ void __launch_bounds__(256) k_adapter_lists(const int32_t *__restrict
         __syncthreads();
         int at = base + sum - n;
         for (int w = 0; w < warp; ++w) at += warp_sum[w];
-        if (a < L) {
-            list_off[a] = at;
+        if (a < p.L) {
+            p.list_off[a] = at;
             if (!bad)
-                for (int i = 0, k = at; i < R; ++i)
-                    if (__ldg(ids + i) == a) list[k++] = i;
+                for (int i = 0, k = at; i < p.R; ++i)
+                    if (__ldg(p.ids + i) == a) p.list[k++] = i;
         }
         __syncthreads();
         if (threadIdx.x == 0)
             for (int w = 0; w < 8; ++w) base += warp_sum[w];
         __syncthreads();
     }
-    if (threadIdx.x == 0) list_off[L] = base;
+    if (threadIdx.x == 0) p.list_off[p.L] = base;
 }
 
-static gptq_status rank_rows(void *T2, const void *X, int64_t ldx, int64_t M, const void *A, int inner,
-                             const float *alpha, const int32_t *offsets, const int32_t *ids, int R, int L,
-                             int rank, int dtype, int32_t *status, cudaStream_t st) {
+__global__ void __launch_bounds__(256) k_lora_setup(const __grid_constant__ SetupArg p) {
+    __shared__ uint16_t tile[32][34];
+    grid_dependency();
+    if (blockIdx.x == 0) {
+        adapter_lists(p);
+        return;
+    }
+    const int tn = (p.N + 31) / 32, tr = (p.r + 31) / 32;
+    const int64_t b = blockIdx.x - 1;
+    const int l = (int)(b / (tn * tr)), rest = (int)(b - (int64_t)l * tn * tr);
+    const int n0 = rest % tn * 32, j0 = rest / tn * 32;
+    const int64_t base = (int64_t)l * p.N * p.r;
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    for (int i = y; i < 32; i += 8)
+        if (n0 + i < p.N && j0 + x < p.r) tile[i][x] = p.in[base + (int64_t)(n0 + i) * p.r + j0 + x];
+    __syncthreads();
+    for (int i = y; i < 32; i += 8)
+        if (j0 + i < p.r && n0 + x < p.N) p.out[base + (int64_t)(j0 + i) * p.N + n0 + x] = tile[x][i];
+}
+
+static RankArg rank_arg(void *T2, const void *X, int64_t ldx, int64_t M, const void *A, int inner,
+                        const float *alpha, const int32_t *offsets, const LoraArg &l, int32_t *status) {
     RankArg p{};
     p.X = X; p.ldx = ldx; p.M = M;
     p.A = A; p.alpha = alpha;
-    p.offsets = offsets; p.ids = ids;
-    p.R = R; p.L = L; p.rank = rank; p.inner = inner;
+    p.offsets = offsets; p.ids = l.ids;
+    p.R = l.R; p.L = l.L; p.rank = l.rank; p.inner = inner;
     p.T2 = T2;
     p.xvec = aligned(X, 16) && ldx % 8 == 0;
     p.avec = aligned(A, 16) && inner % 8 == 0;
     p.status = status;
-    return dtype == GPTQ_BF16 ? launch_rank<__nv_bfloat16>(p, dtype, st) : launch_rank<__half>(p, dtype, st);
+    return p;
+}
+
+static gptq_status rank_rows(RankArgs &q, int count, int dtype, cudaStream_t st) {
+    return dtype == GPTQ_BF16 ? launch_rank<__nv_bfloat16>(q, count, dtype, st)
+                              : launch_rank<__half>(q, count, dtype, st);
 }
 
 struct LoraSpace {
     void *T2, *U2, *Bt;
-    float *parts;
+    float *parts_a, *parts_b;
     int32_t *list_off, *list;
     size_t bytes;
 };
@@ -500,7 +530,8 @@ static LoraSpace lora_space(void *ws, bool backward, int64_t M, int N, int K, in
         s.U2 = c.take<uint16_t>((size_t)M * parts * rank);
         s.Bt = c.take<uint16_t>((size_t)L * N * rank);
         const size_t pb = (size_t)adapter_parts(M, L, N) * L * N * rank, pa = (size_t)adapter_parts(M, L, K) * L * K * rank;
-        s.parts = c.take<float>(std::max(pa, pb));
+        s.parts_a = c.take<float>(pa);
+        s.parts_b = c.take<float>(pb);
         s.list_off = c.take<int32_t>(L + 1);
         s.list = c.take<int32_t>(std::max(R, 1));
     }
@@ -516,8 +547,9 @@ gptq_status matmul_lora(MatmulArg m, const void *A, const void *B, const float *
                         void *ws, cudaStream_t st) {
     const LoraArg &l = m.lora;
     const LoraSpace s = lora_space(ws, false, m.M, m.w.N, m.w.K, l.R, l.L, l.rank);
-    gptq_status r = rank_rows(s.T2, m.X, m.ldx, m.M, A, m.w.K, alpha, m.offsets, l.ids, l.R, l.L, l.rank,
-                              dtype, m.status, st);
+    RankArgs q{};
+    q.a[0] = rank_arg(s.T2, m.X, m.ldx, m.M, A, m.w.K, alpha, m.offsets, l, m.status);
+    gptq_status r = rank_rows(q, 1, dtype, st);
     if (r != GPTQ_OK) return r;
     m.lora.P = B;
     m.lora.T2 = s.T2;
@@ -532,31 +564,26 @@ gptq_status matmul_lora_backward(MatmulArg m, float *dA, float *dB, const void *
     const LoraArg l = m.lora;
     const int N = m.w.N, K = m.w.K;
     const LoraSpace s = lora_space(ws, true, m.M, N, K, l.R, l.L, l.rank);
-    gptq_status r = GPTQ_OK;
-    if (dA || dB) {
-        r = launch_pdl(k_adapter_lists, dim3(1), 256, 0, 1, st, l.ids, l.R, l.L, s.list_off, s.list, m.status);
+    const bool need_u = (m.Y || dA) && m.M > 0, need_t = dB && m.M > 0;
+    SetupArg setup{l.ids, l.R, l.L, s.list_off, s.list, m.status, (const uint16_t *)B, (uint16_t *)s.Bt, N, l.rank};
+    const int64_t tiles = need_u ? (int64_t)((N + 31) / 32) * ((l.rank + 31) / 32) * l.L : 0;
+    gptq_status r = launch_pdl(k_lora_setup, dim3((unsigned)(1 + tiles)), 256, 0, 1, st, setup);
+    if (r != GPTQ_OK) return r;
+    RankArgs q{};
+    int count = 0;
+    if (need_u) q.a[count++] = rank_arg(s.U2, m.X, m.ldx, m.M, s.Bt, N, alpha, m.offsets, l, m.status);
+    if (need_t) q.a[count++] = rank_arg(s.T2, X, ldx, m.M, A, K, alpha, m.offsets, l, m.status);
+    if (count > 0) {
+        r = rank_rows(q, count, dtype, st);
         if (r != GPTQ_OK) return r;
     }
-    if ((m.Y || dA) && m.M > 0) {
-        r = launch_pdl(k_transpose, dim3((N + 31) / 32, (l.rank + 31) / 32, l.L), 256, 0, 1, st,
-                       (const uint16_t *)B, (uint16_t *)s.Bt, N, l.rank);
-        if (r != GPTQ_OK) return r;
-        r = rank_rows(s.U2, m.X, m.ldx, m.M, s.Bt, N, alpha, m.offsets, l.ids, l.R, l.L, l.rank, dtype,
-                      m.status, st);
-        if (r != GPTQ_OK) return r;
-    }
-    if (dB) {
-        if (m.M > 0) {
-            r = rank_rows(s.T2, X, ldx, m.M, A, K, alpha, m.offsets, l.ids, l.R, l.L, l.rank, dtype, m.status, st);
-            if (r != GPTQ_OK) return r;
-        }
-        r = adapter_gradient(dB, s.parts, adapter_parts(m.M, l.L, N), m.X, m.ldx, N, s.T2, l.rank, 0, dtype, m.M,
-                             m.offsets, l.ids, s.list_off, s.list, l.R, l.L, m.status, st);
-        if (r != GPTQ_OK) return r;
-    }
-    if (dA) {
-        r = adapter_gradient(dA, s.parts, adapter_parts(m.M, l.L, K), X, ldx, K, s.U2, l.rank, 1, dtype, m.M,
-                             m.offsets, l.ids, s.list_off, s.list, l.R, l.L, m.status, st);
+    AdapterGrad grads[2];
+    int wanted = 0;
+    if (dB) grads[wanted++] = {m.X, m.ldx, N, s.T2, dB, s.parts_b, 0};
+    if (dA) grads[wanted++] = {X, ldx, K, s.U2, dA, s.parts_a, 1};
+    if (wanted > 0) {
+        r = adapter_gradients(grads, wanted, l.rank, dtype, m.M, m.offsets, l.ids, s.list_off, s.list, l.R, l.L,
+                              m.status, st);
         if (r != GPTQ_OK) return r;
     }
     if (m.Y && m.M > 0) {

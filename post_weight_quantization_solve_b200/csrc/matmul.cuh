@@ -57,6 +57,17 @@ struct MatmulArg {
     int32_t *status;
 };
 
+// One gradient of the adapters: P [M][ldp] against the rank-space rows T2; parts: room for the sums
+// of adapter_parts() parts where there is more than one.
+struct AdapterGrad {
+    const void *P;
+    int64_t ldp;
+    int np;
+    const void *T2;
+    float *out, *parts;
+    int transposed;
+};
+
 constexpr int MATMUL_MAX_EXPERTS = 512;
 
 // ---- 16-bit types --------------------------------------------------------------------------

@@ -57,10 +57,19 @@ struct DwArg {
     int transposed;           // output [q][p] instead of [p][q]
     int accumulate;
     float *out;               // [split][groups][np][nq'] (or [nq'][np])
-    int tiled, vec;
+    int vec;
     int tstore;               // outputs by tiled stores
-    int stages, boxes;        // operand ring; boxes of a stage (P's two, then Q's)
     int32_t *status;
+};
+
+// One launch does one or two products over the same rows (an adapter's two gradients).
+struct DwArgs {
+    DwArg a[2];
+    int64_t units0, units;    // tiles of the first, of all
+    int tiled, stages, boxes; // alike for both: operand ring; boxes of a stage (P's two, then Q's)
+};
+struct DwMaps {
+    CUtensorMap p[2], q[2], o;
 };
 
 // The ranges of a group in order, cut to the steps [s0, s1) of one part.
@@ -136,12 +145,12 @@ __device__ __forceinline__ void dw_plain_box(uint8_t *dst, const T *x, int64_t l
 
 template <typename T, bool PAIR>
 __global__ void __launch_bounds__(DW_THREADS, 1)
-    k_matmul_dw(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
-                const __grid_constant__ CUtensorMap omap, const __grid_constant__ DwArg p) {
+    k_matmul_dw(const __grid_constant__ DwMaps maps, const __grid_constant__ DwArgs args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int stages = p.stages, stage_bytes = p.boxes * DW_BOX;
+    const DwArg &first_arg = args.a[0];
+    const int stages = args.stages, stage_bytes = args.boxes * DW_BOX;
     float *epi = reinterpret_cast<float *>(smem + stages * stage_bytes);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + stages * stage_bytes + DW_EPI);
     uint64_t *empty = full + DW_MAX_STAGES;
@@ -158,7 +167,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     if (threadIdx.x == 0) {
         // tiled: the copies' warp of each block, or its warp for range ends; plain: three warps each
         for (int s = 0; s < stages; ++s) {
-            tc::mbar_init(&full[s], (p.tiled ? 1 : 3) * (PAIR ? 2 : 1));
+            tc::mbar_init(&full[s], (args.tiled ? 1 : 3) * (PAIR ? 2 : 1));
             tc::mbar_init(&empty[s], 1);
             tc::mbar_init(&tail[s], 1);
         }
@@ -170,9 +179,9 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         *abort = 0;
         *refuse = 0;
         tc::fence_mbar_init();
-        if (p.tiled) {
-            tc::prefetch_tmap(&pmap);
-            tc::prefetch_tmap(&qmap);
+        if (args.tiled) {
+            tc::prefetch_tmap(&maps.p[0]);
+            tc::prefetch_tmap(&maps.q[0]);
         }
     }
     if (warp == 1) {
@@ -184,13 +193,13 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     grid_dependency();
-    if (threadIdx.x == DW_THREADS - 1 && failed(p.status)) *refuse = 2;
-    bool bad = p.offsets && offsets_bad(p.offsets, p.R, p.M, threadIdx.x, DW_THREADS);
-    if (p.ids) bad |= ids_bad(p.ids, p.R, p.L, threadIdx.x, DW_THREADS);
+    if (threadIdx.x == DW_THREADS - 1 && failed(first_arg.status)) *refuse = 2;
+    bool bad = first_arg.offsets && offsets_bad(first_arg.offsets, first_arg.R, first_arg.M, threadIdx.x, DW_THREADS);
+    if (first_arg.ids) bad |= ids_bad(first_arg.ids, first_arg.R, first_arg.L, threadIdx.x, DW_THREADS);
     bad = __syncthreads_or(bad);
     if (bad && threadIdx.x == 0) {
         *refuse = 1;
-        set_status(p.status, GPTQ_ERR_ARG);
+        set_status(first_arg.status, GPTQ_ERR_ARG);
     }
     __syncthreads();
     if constexpr (PAIR) tc::cluster_sync();     // both blocks' barriers and refusal are in place
@@ -198,33 +207,35 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     if constexpr (PAIR) skip = (int)tc::ld_shared_cluster(tc::mapa_shared(tc::smem_u32(refuse), 0));
 
     constexpr int PW = PAIR ? 2 * DW_LANES : DW_LANES;
-    const int nout = p.parts > 1 ? p.rank : p.nq;       // columns of the outputs
-    const int qw = p.apart ? 64 : DW_COLS;              // of them a tile
-    const int tp = (p.np + PW - 1) / PW, tq = (nout + qw - 1) / qw;
-    const int qstep = p.apart ? p.rank : 64;            // from one box of Q to the next
-    const int per_group = tp * tq * p.split;
-    const int64_t units = skip ? 0 : (int64_t)p.groups * per_group;
+    const int64_t units = skip ? 0 : args.units;
     const int64_t first = blockIdx.x / (PAIR ? 2 : 1), by = gridDim.x / (PAIR ? 2 : 1);
-    // unit -> group, part of its steps, this block's first columns of P and Q (operand) and of the
-    // tile's Q columns, tiles of P fastest
+    // unit -> product, group, part of its steps, this block's first columns of P and Q (operand),
+    // tiles of P fastest
     struct Unit {
-        int g, s0, s1, pc, qc, qb, cols;        // qb boxes of Q from qc; the tile's columns
-        int qt;
+        int which, g, part, s0, s1, pc, qc, qb, cols;   // qb boxes of Q from qc, qstep apart; the tile's columns
+        int qt, qw, qstep, nout;                        // tile of Q, outputs' columns of a tile, of all
     };
     auto unit = [&](int64_t u) {
         Unit t;
-        t.g = (int)(u / per_group);
-        int r = (int)(u - (int64_t)t.g * per_group);
-        const int part = r / (tp * tq);
-        r -= part * tp * tq;
-        t.qt = r / tp;
-        t.pc = (r - t.qt * tp) * PW + (int)rank * DW_LANES;
+        t.which = u >= args.units0 ? 1 : 0;
+        const DwArg &p = args.a[t.which];
+        if (t.which) u -= args.units0;
+        t.nout = p.parts > 1 ? p.rank : p.nq;
+        t.qw = p.apart ? 64 : DW_COLS;
+        t.qstep = p.apart ? p.rank : 64;
+        // (the host keeps the units below 2^31)
+        const unsigned tp = (p.np + PW - 1) / PW, tq = p.apart ? (t.nout + 63) / 64 : (t.nout + DW_COLS - 1) / DW_COLS;
+        const unsigned v = (unsigned)u, w = v / tp, x = w / tq;
+        t.pc = (int)(v - w * tp) * PW + (int)rank * DW_LANES;
+        t.qt = (int)(w - x * tq);
+        t.g = (int)(p.split > 1 ? x / (unsigned)p.split : x);
+        t.part = (int)x - t.g * p.split;
         const int n = StepWalk::total(p, t.g);
-        t.s0 = (int)((int64_t)n * part / p.split);
-        t.s1 = (int)((int64_t)n * (part + 1) / p.split);
+        t.s0 = (int)((int64_t)n * t.part / p.split);
+        t.s1 = (int)((int64_t)n * (t.part + 1) / p.split);
         // columns that the MMAs take: multiples of 16 (a pair: all 256, zeros past Q's end)
         t.cols = PAIR ? DW_COLS : p.apart ? p.parts * 64 : min(DW_COLS, (p.nq - t.qt * DW_COLS + 15) & ~15);
-        t.qc = t.qt * qw + (PAIR ? (int)rank * (DW_COLS / 2) : 0);
+        t.qc = t.qt * t.qw + (PAIR ? (int)rank * (DW_COLS / 2) : 0);
         t.qb = PAIR ? 2 : (t.cols + 63) / 64;
         return t;
     };
@@ -233,17 +244,18 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         else tc::mbar_arrive(&full[stage]);
     };
 
-    if (warp == 0 && p.tiled) {
+    if (warp == 0 && args.tiled) {
         // the whole warp walks, one elected lane issues
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int64_t u = first; u < units && ok; u += by) {
             const Unit t = unit(u);
-            StepWalk walk(p, t.g, t.s0, t.s1);
+            StepWalk walk(args.a[t.which], t.g, t.s0, t.s1);
             int64_t r;
             int n;
             const uint32_t bytes = (2 + t.qb) * DW_BOX;
+            const CUtensorMap *pmap = &maps.p[t.which], *qmap = &maps.q[t.which];
             while (walk.next(r, n)) {
                 ok = __all_sync(~0u, tc::mbar_wait(&empty[stage], phase ^ 1, abort));
                 if (!ok) break;
@@ -254,13 +266,13 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                     if (ends || !PAIR) {
                         uint64_t *bar = ends ? &tail[stage] : &full[stage];
                         tc::mbar_arrive_expect_tx(bar, bytes);
-                        for (int i = 0; i < 2; ++i) tc::tma_load_2d(a + i * DW_BOX, &pmap, bar, x0 + 64 * i, y);
-                        for (int i = 0; i < t.qb; ++i) tc::tma_load_2d(b + i * DW_BOX, &qmap, bar, x1 + qstep * i, y);
+                        for (int i = 0; i < 2; ++i) tc::tma_load_2d(a + i * DW_BOX, pmap, bar, x0 + 64 * i, y);
+                        for (int i = 0; i < t.qb; ++i) tc::tma_load_2d(b + i * DW_BOX, qmap, bar, x1 + t.qstep * i, y);
                     } else {
                         if (rank == 0) tc::mbar_arrive_expect_tx(&full[stage], 2 * bytes);
                         const uint32_t fb = tc::mapa_shared(tc::smem_u32(&full[stage]), 0);
-                        for (int i = 0; i < 2; ++i) tc::tma_load_2d_pair(a + i * DW_BOX, &pmap, fb, x0 + 64 * i, y);
-                        for (int i = 0; i < 2; ++i) tc::tma_load_2d_pair(b + i * DW_BOX, &qmap, fb, x1 + 64 * i, y);
+                        for (int i = 0; i < 2; ++i) tc::tma_load_2d_pair(a + i * DW_BOX, pmap, fb, x0 + 64 * i, y);
+                        for (int i = 0; i < 2; ++i) tc::tma_load_2d_pair(b + i * DW_BOX, qmap, fb, x1 + 64 * i, y);
                         if (rank != 0) tc::mbar_arrive_remote(fb);
                     }
                 }
@@ -273,14 +285,14 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
             while (clock64() - from < 20000000ll) {
             }
         }
-    } else if (warp == 2 && p.tiled) {
+    } else if (warp == 2 && args.tiled) {
         // steps that a range ends in: rows n .. the next multiple of 16 belong to others
         int stage = 0;
         uint32_t phases = 0;                // of the tail barriers, a bit a stage
         bool ok = true;
         for (int64_t u = first; u < units && ok; u += by) {
             const Unit t = unit(u);
-            StepWalk walk(p, t.g, t.s0, t.s1);
+            StepWalk walk(args.a[t.which], t.g, t.s0, t.s1);
             int64_t r;
             int n;
             while (ok && walk.next(r, n)) {
@@ -318,7 +330,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
             };
             for (int64_t u = first; u < units && ok; u += by) {
                 const Unit t = unit(u);
-                StepWalk walk(p, t.g, t.s0, t.s1);
+                StepWalk walk(args.a[t.which], t.g, t.s0, t.s1);
                 int64_t r;
                 int n;
                 const uint32_t id = tc::idesc_f16_f32(Half2<T>::kType, PW, t.cols, 1, 1);
@@ -372,15 +384,15 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        const int spacing = p.apart ? 64 : nout;       // of the parts in the accumulator
-        // this warp's columns of a tile: up to 128 from `side` times 128 (parts: 64)
-        const int own = p.parts > 1 ? 64 : 128;
         for (int64_t u = first; u < units && ok; u += by) {
             const Unit t = unit(u);
-            const int part = (int)(u / (tp * tq)) % p.split;
-            float *out = p.out + ((int64_t)part * p.groups + t.g) * p.np * nout;
+            const DwArg &p = args.a[t.which];
+            const int nout = t.nout, spacing = p.apart ? 64 : nout;     // of the parts in the accumulator
+            // this warp's columns of a tile: up to 128 from `side` times 128 (parts: 64)
+            const int own = p.parts > 1 ? 64 : 128;
+            float *out = p.out + ((int64_t)t.part * p.groups + t.g) * p.np * nout;
             const int r0 = t.pc + quad * 32, c0 = side * own;
-            const int qn = max(0, min(own, min(qw, nout - t.qt * qw) - c0));                // columns it has
+            const int qn = max(0, min(own, min(t.qw, nout - t.qt * t.qw) - c0));            // columns it has
             const int chains = (t.s1 - t.s0 + DW_CHAIN - 1) / DW_CHAIN;                     // none: zeros
             float sum[128];
 #pragma unroll
@@ -415,7 +427,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb) {
                 if (cb * 32 >= qn) break;
-                const int q0 = t.qt * qw + c0 + cb * 32, cols = min(32, qn - cb * 32);
+                const int q0 = t.qt * t.qw + c0 + cb * 32, cols = min(32, qn - cb * 32);
                 if (p.tstore) {
                     // row = lane, 16-byte piece q at q ^ (lane & 7), once the box is free again
                     if (lane == 0) tc::bulk_wait_read<0>();
@@ -428,8 +440,8 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                     tc::fence_async_shared();
                     __syncwarp();
                     if (lane == 0 && r0 < p.np) {
-                        if (p.accumulate) tc::tma_reduce_add_3d(&omap, box, q0, r0, t.g);
-                        else tc::tma_store_3d(&omap, box, q0, r0, t.g);
+                        if (p.accumulate) tc::tma_reduce_add_3d(&maps.o, box, q0, r0, t.g);
+                        else tc::tma_store_3d(&maps.o, box, q0, r0, t.g);
                         tc::bulk_commit();
                     }
                 } else if (p.transposed) {
@@ -461,15 +473,16 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
             }
         }
         if (lane == 0) tc::bulk_wait_all();
-    } else if (!p.tiled) {
+    } else if (!args.tiled) {
         const int tid = (warp == 0 ? 0 : warp - 1) * 32 + lane;         // warps 0, 2, 3
-        const T *P = static_cast<const T *>(p.P), *Q = static_cast<const T *>(p.Q);
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int64_t u = first; u < units && ok; u += by) {
             const Unit t = unit(u);
-            StepWalk walk(p, t.g, t.s0, t.s1);
+            const DwArg &p = args.a[t.which];
+            const T *P = static_cast<const T *>(p.P), *Q = static_cast<const T *>(p.Q);
+            StepWalk walk(args.a[t.which], t.g, t.s0, t.s1);
             int64_t r;
             int n;
             while (walk.next(r, n)) {
@@ -479,7 +492,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                 for (int i = 0; i < 2; ++i)
                     dw_plain_box<T>(a + i * DW_BOX, P, p.ldp, r, n, t.pc + 64 * i, p.np, (p.vec & 1) != 0, tid, 96);
                 for (int i = 0; i < t.qb; ++i)
-                    dw_plain_box<T>(b + i * DW_BOX, Q, p.ldq, r, n, t.qc + qstep * i, p.nq, (p.vec & 2) != 0, tid, 96);
+                    dw_plain_box<T>(b + i * DW_BOX, Q, p.ldq, r, n, t.qc + t.qstep * i, p.nq, (p.vec & 2) != 0, tid, 96);
                 tc::fence_async_shared();
                 __syncwarp();
                 if (lane == 0) arrive_full(stage);
@@ -492,7 +505,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     tc::fence_before_sync();
     __syncthreads();
     if constexpr (PAIR) tc::cluster_sync();     // neither block leaves while the pair uses its memory
-    if (*abort && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_TIMEOUT);
+    if (*abort && threadIdx.x == 0) set_status(first_arg.status, GPTQ_ERR_TIMEOUT);
     if (warp == 1) {
         tc::fence_after_sync();
         if constexpr (PAIR) tc::tmem_dealloc_pair(tmem, 512);
@@ -500,16 +513,23 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     }
 }
 
-// out[i] = the parts' sum, parts in order.
-__global__ void __launch_bounds__(256) k_sum_parts(const float *__restrict__ parts, int split, int64_t n,
-                                                   float *__restrict__ out, const int32_t *status) {
+// out[i] = the parts' sum, parts in order, for one or two outputs.
+struct SumArg {
+    const float *parts[2];
+    float *out[2];
+    int64_t n[2];
+    int split[2];
+};
+__global__ void __launch_bounds__(256) k_sum_parts(const __grid_constant__ SumArg p, const int32_t *status) {
     grid_dependency();
     if (failed(status)) return;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int w = i >= p.n[0] ? 1 : 0;
+    if (w) i -= p.n[0];
+    if (i >= p.n[w]) return;
     float s = 0.f;
-    for (int k = 0; k < split; ++k) s += parts[k * n + i];
-    out[i] = s;
+    for (int k = 0; k < p.split[w]; ++k) s += p.parts[w][k * p.n[w] + i];
+    p.out[w][i] = s;
 }
 
 // The outputs [groups][np][nq] as boxes of 32 x 32 of one group.
@@ -524,28 +544,38 @@ static bool out_map(CUtensorMap *map, const DwArg &p) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static gptq_status launch_dw(DwArg &p, int dtype, cudaStream_t st) {
-    CUtensorMap pm{}, qm{}, om{};
-    p.tstore = out_map(&om, p);
-    p.tiled = rows_map(&pm, p.P, dtype, p.M, p.np, p.ldp, DW_BK) &&
-              rows_map(&qm, p.Q, dtype, p.M, p.nq, p.ldq, DW_BK);
-    p.vec = (aligned(p.P, 16) && p.ldp % 8 == 0 ? 1 : 0) | (aligned(p.Q, 16) && p.ldq % 8 == 0 ? 2 : 0);
-    auto units = [&](int pw) {
+static gptq_status launch_dw(DwArg *a, int count, int dtype, cudaStream_t st) {
+    DwMaps maps{};
+    DwArgs args{};
+    const DwArg &p = a[0];
+    auto units = [&](const DwArg &p, int pw) {
         const int nout = p.parts > 1 ? p.rank : p.nq, qw = p.apart ? 64 : DW_COLS;
         return (int64_t)((p.np + pw - 1) / pw) * ((nout + qw - 1) / qw) * p.groups * p.split;
     };
     // pairs where both operands fill their tiles and there are pairs enough for the machine
-    const bool pair = p.parts == 1 && p.np > DW_LANES && p.nq > DW_COLS / 2 && 2 * units(2 * DW_LANES) >= device_sms();
-    p.boxes = pair ? 4 : p.apart ? 2 + p.parts : 2 + (std::min(p.nq, DW_COLS) + 63) / 64;
-    p.stages = std::min(DW_MAX_STAGES, (227 * 1024 - DW_FIXED) / (p.boxes * DW_BOX));
-    const size_t smem = (size_t)p.stages * p.boxes * DW_BOX + DW_FIXED;
-    const int blocks = pair ? (int)std::min<int64_t>(units(2 * DW_LANES), device_sms() / 2) * 2
-                            : (int)std::max<int64_t>(1, std::min<int64_t>(units(DW_LANES), device_sms()));
+    const bool pair = count == 1 && p.parts == 1 && p.np > DW_LANES && p.nq > DW_COLS / 2 &&
+                      2 * units(p, 2 * DW_LANES) >= device_sms();
+    args.tiled = 1;
+    for (int i = 0; i < count; ++i) {
+        DwArg &p = a[i];
+        p.tstore = count == 1 && out_map(&maps.o, p);
+        args.tiled &= rows_map(&maps.p[i], p.P, dtype, p.M, p.np, p.ldp, DW_BK) &&
+                      rows_map(&maps.q[i], p.Q, dtype, p.M, p.nq, p.ldq, DW_BK);
+        p.vec = (aligned(p.P, 16) && p.ldp % 8 == 0 ? 1 : 0) | (aligned(p.Q, 16) && p.ldq % 8 == 0 ? 2 : 0);
+        args.a[i] = p;
+        args.units += units(p, pair ? 2 * DW_LANES : DW_LANES);
+        if (i == 0) args.units0 = args.units;
+    }
+    if (args.units > 0x7fffffff) return GPTQ_ERR_ARG;
+    args.boxes = pair ? 4 : p.apart ? 2 + p.parts : 2 + (std::min(p.nq, DW_COLS) + 63) / 64;
+    args.stages = std::min(DW_MAX_STAGES, (227 * 1024 - DW_FIXED) / (args.boxes * DW_BOX));
+    const size_t smem = (size_t)args.stages * args.boxes * DW_BOX + DW_FIXED;
+    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(args.units, device_sms() / (pair ? 2 : 1))) * (pair ? 2 : 1);
     if (dtype == GPTQ_BF16)
-        return pair ? launch_pdl(k_matmul_dw<__nv_bfloat16, true>, dim3(blocks), DW_THREADS, smem, 2, st, pm, qm, om, p)
-                    : launch_pdl(k_matmul_dw<__nv_bfloat16, false>, dim3(blocks), DW_THREADS, smem, 1, st, pm, qm, om, p);
-    return pair ? launch_pdl(k_matmul_dw<__half, true>, dim3(blocks), DW_THREADS, smem, 2, st, pm, qm, om, p)
-                : launch_pdl(k_matmul_dw<__half, false>, dim3(blocks), DW_THREADS, smem, 1, st, pm, qm, om, p);
+        return pair ? launch_pdl(k_matmul_dw<__nv_bfloat16, true>, dim3(blocks), DW_THREADS, smem, 2, st, maps, args)
+                    : launch_pdl(k_matmul_dw<__nv_bfloat16, false>, dim3(blocks), DW_THREADS, smem, 1, st, maps, args);
+    return pair ? launch_pdl(k_matmul_dw<__half, true>, dim3(blocks), DW_THREADS, smem, 2, st, maps, args)
+                : launch_pdl(k_matmul_dw<__half, false>, dim3(blocks), DW_THREADS, smem, 1, st, maps, args);
 }
 
 // G[e] (+)= dY^T X over the rows of range e.
@@ -562,7 +592,7 @@ gptq_status matmul_dw(float *G, const void *dY, int64_t lddy, const void *X, int
     p.accumulate = accumulate;
     p.out = G;
     p.status = status;
-    return launch_dw(p, dtype, st);
+    return launch_dw(&p, 1, dtype, st);
 }
 
 // Parts of an adapter's rows: enough blocks to fill the machine, at least 512 rows a part.
@@ -573,34 +603,44 @@ int adapter_parts(int64_t M, int L, int width) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(s, 16));
 }
 
-// One adapter gradient: dB[a][n][j] = sum dY[t][n] T[t][j] (transposed 0) or
-// dA[a][j][k] = sum U[t][j] X[t][k] (transposed 1), rows of the requests listed for a.
-gptq_status adapter_gradient(float *out, float *parts, int split, const void *P, int64_t ldp, int np,
-                             const void *T2, int rank, int transposed, int dtype, int64_t M,
-                             const int32_t *offsets, const int32_t *ids, const int32_t *list_off,
-                             const int32_t *list, int R, int L, int32_t *status, cudaStream_t st) {
-    DwArg p{};
-    p.P = P; p.ldp = ldp; p.np = np;
-    p.parts = lora_halves(dtype);
-    p.rank = rank;
-    p.Q = T2; p.ldq = p.nq = p.parts * rank;
-    p.apart = p.nq > DW_COLS;
-    p.M = M;
-    p.offsets = offsets;
-    p.list_off = list_off;
-    p.list = list;
-    p.R = R;
-    p.groups = p.L = L;
-    p.ids = ids;
-    p.split = split;
-    p.transposed = transposed;
-    p.out = split > 1 ? parts : out;
-    p.status = status;
-    gptq_status s = launch_dw(p, dtype, st);
-    if (s != GPTQ_OK || split == 1) return s;
-    const int64_t n = (int64_t)L * np * rank;
-    return launch_pdl(k_sum_parts, dim3((unsigned)((n + 255) / 256)), 256, 0, 1, st, (const float *)parts, split,
-                      n, out, (const int32_t *)status);
+// The adapters' gradients, the one or both that are wanted, over the rows of the requests listed for
+// each: dB[a][n][j] = sum dY[t][n] T[t][j], dA[a][j][k] = sum U[t][j] X[t][k].
+gptq_status adapter_gradients(const AdapterGrad *grads, int count, int rank, int dtype, int64_t M,
+                              const int32_t *offsets, const int32_t *ids, const int32_t *list_off,
+                              const int32_t *list, int R, int L, int32_t *status, cudaStream_t st) {
+    DwArg a[2] = {};
+    SumArg sum{};
+    int64_t n = 0;
+    for (int i = 0; i < count; ++i) {
+        const AdapterGrad &g = grads[i];
+        DwArg &p = a[i];
+        p.P = g.P; p.ldp = g.ldp; p.np = g.np;
+        p.parts = lora_halves(dtype);
+        p.rank = rank;
+        p.Q = g.T2; p.ldq = p.nq = p.parts * rank;
+        p.apart = p.nq > DW_COLS;
+        p.M = M;
+        p.offsets = offsets;
+        p.list_off = list_off;
+        p.list = list;
+        p.R = R;
+        p.groups = p.L = L;
+        p.ids = ids;
+        p.split = adapter_parts(M, L, g.np);
+        p.transposed = g.transposed;
+        p.out = p.split > 1 ? g.parts : g.out;
+        p.status = status;
+        if (p.split > 1) {
+            sum.parts[i] = g.parts;
+            sum.out[i] = g.out;
+            sum.n[i] = (int64_t)L * g.np * rank;
+            sum.split[i] = p.split;
+            n += sum.n[i];
+        }
+    }
+    gptq_status s = launch_dw(a, count, dtype, st);
+    if (s != GPTQ_OK || n == 0) return s;
+    return launch_pdl(k_sum_parts, dim3((unsigned)((n + 255) / 256)), 256, 0, 1, st, sum, (const int32_t *)status);
 }
 
 }  // namespace gptq
