@@ -108,7 +108,7 @@ GPTQ_API gptq_status gptq_matmul_grouped_dw(float *dW, const void *dY, int64_t l
  *            outside [offsets[0], offsets[requests]) are left as they were.
  *   ws       gptq_lora_workspace_size(0, M, N, K, requests, adapters, rank) bytes.
  *   Arithmetic: fp32 sums; alpha A X enters as two dtype parts that add up to it (16 bits
- *            for bf16, 22 for fp16 inside its normal range; it must lie in fp16's range). Up to 16
+ *            for bf16, 22 for fp16 inside its normal range; it must lie in fp16's range). Up to 8
  *            rows, W^ enters as in gptq_matmul_grouped; above, each weight is rounded
  *            once to dtype.
  *   Others as gptq_matmul_grouped. GPTQ_ERR_WORKSPACE for the workspace.

@@ -1,14 +1,14 @@
 // Packed-weight products for a few rows: Y[t] = W^_e X[t] (+ adapters) when decoding.
 //
 // With a handful of rows the product is bound by reading the packed words once, so the kernel
-// is laid out for that: a block takes 32 output channels of one range and up to 8 (or 16) of
+// is laid out for that: a block takes 32 output channels of one range and up to 8 of
 // its rows; its 8 warps split the contraction, and each lane reads whole chunks of 32 codes,
 // several requests in flight. Four lanes of a quad hold four neighbouring chunks of one row,
 // which is the m16n8k16 fragment layout with the contraction index permuted: a sum does not
 // care, as long as the rows X are read in the same order. X is put into shared memory once a
 // block, in the order in which codes leave a word, so a fragment is four 16-byte reads and the
 // unpacking needs no permutes (read from global memory per fragment, with its bounds and
-// permutes, X cost as many instructions as the codes: 5.2 a code against 2.6). The matrix
+// permutes, X cost as many instructions as the codes: 5.2 a code against 3.9). The matrix
 // instruction adds in fp32; the warps' partial sums meet in shared memory in warp order.
 //
 // Scales: one scale a channel enters in fp32 at the end (the codes are exact); with input
@@ -77,11 +77,11 @@ __device__ __forceinline__ void to_pair_order(uint32_t (&x)[16]) {
     }
 }
 
-// NT fragments of 8 rows; IDX: groups by g_idx.
-template <typename T, int B, int NT, bool IDX>
-__global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 && !IDX && B <= 4 ? (B == 4 ? 3 : 4) : 2)
+// IDX: groups by g_idx.
+template <typename T, int B, bool IDX>
+__global__ void __launch_bounds__(TK_WARPS * 32, !IDX && B <= 4 ? (B == 4 ? 3 : 4) : 2)
     k_matmul_token(const __grid_constant__ TokenArg p) {
-    constexpr int ROWS = 8 * NT, NR = 4;
+    constexpr int ROWS = 8, NR = 4;
     extern __shared__ uint8_t xs[];                     // [row][chunk of 64 bytes], padded rows
     __shared__ float part[TK_WARPS][ROWS][TK_CH + 1];
     __shared__ int found[4];
@@ -176,13 +176,11 @@ __global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 && !IDX && B <= 4 ? (B 
         last[i] = min(c0 + g + 8 * i, m.w.N - 1);
         row[i] = m.w.words + (erow + last[i]) * m.w.ldw + (warp * 4 + quad) * B;
     }
-    float acc[2][NT][4];
+    float acc[2][4];
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int b = 0; b < NT; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[a][i] = 0.f;
 
     // a step: the warp's quads cover 4 chunks of 32 columns; the warps take steps in turn. Words and
     // scales are requested a step ahead only by the next block on the SM: four of them fit, and all
@@ -283,13 +281,10 @@ __global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 && !IDX && B <= 4 ? (B 
         // eight columns a lane at a time: the pairs of four channels, then their MMAs
         auto eight = [&](auto I) {
             constexpr int i8 = decltype(I)::value;
-            uint32_t v[NR][4], x[NT][4];
-#pragma unroll
-            for (int b = 0; b < NT; ++b) {
-                uint4 y = make_uint4(0u, 0u, 0u, 0u);
-                if (b * 8 + g < n) y = *reinterpret_cast<const uint4 *>(xr + b * 8 * pitch + ((i8 ^ (quad >> 1)) << 4));
-                x[b][0] = y.x; x[b][1] = y.y; x[b][2] = y.z; x[b][3] = y.w;
-            }
+            uint32_t v[NR][4];
+            uint4 y = make_uint4(0u, 0u, 0u, 0u);
+            if (g < n) y = *reinterpret_cast<const uint4 *>(xr + ((i8 ^ (quad >> 1)) << 4));
+            const uint32_t x[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 if constexpr (IDX) {
@@ -304,10 +299,8 @@ __global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 && !IDX && B <= 4 ? (B 
             for (int a = 0; a < 2; ++a)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int b = 0; b < NT; ++b)
-                        mma_16816<T>(acc[a][b], v[2 * a][2 * j], v[2 * a + 1][2 * j], v[2 * a][2 * j + 1],
-                                     v[2 * a + 1][2 * j + 1], x[b][2 * j], x[b][2 * j + 1]);
+                    mma_16816<T>(acc[a], v[2 * a][2 * j], v[2 * a + 1][2 * j], v[2 * a][2 * j + 1],
+                                 v[2 * a + 1][2 * j + 1], x[2 * j], x[2 * j + 1]);
         };
         eight(std::integral_constant<int, 0>{});
         eight(std::integral_constant<int, 1>{});
@@ -319,10 +312,8 @@ __global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 && !IDX && B <= 4 ? (B 
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int b = 0; b < NT; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                part[warp][b * 8 + 2 * quad + (i & 1)][a * 16 + g + 8 * (i >> 1)] = acc[a][b][i];
+        for (int i = 0; i < 4; ++i)
+            part[warp][2 * quad + (i & 1)][a * 16 + g + 8 * (i >> 1)] = acc[a][i];
     __syncthreads();
     if (m.lora.R > 0) grid_wait();
     T *Y = static_cast<T *>(m.Y);
@@ -349,40 +340,35 @@ __global__ void __launch_bounds__(TK_WARPS * 32, NT == 1 && !IDX && B <= 4 ? (B 
     }
 }
 
-template <typename T, int NT, bool IDX>
+template <typename T, bool IDX>
 static gptq_status launch_token(const TokenArg &p, int bits, dim3 grid, cudaStream_t st) {
     const size_t smem = (size_t)p.rows * (p.span * 2 + 32);
     switch (bits) {
-        case 2: return launch_pdl(k_matmul_token<T, 2, NT, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
-        case 3: return launch_pdl(k_matmul_token<T, 3, NT, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
-        case 4: return launch_pdl(k_matmul_token<T, 4, NT, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
-        default: return launch_pdl(k_matmul_token<T, 8, NT, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
+        case 2: return launch_pdl(k_matmul_token<T, 2, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
+        case 3: return launch_pdl(k_matmul_token<T, 3, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
+        case 4: return launch_pdl(k_matmul_token<T, 4, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
+        default: return launch_pdl(k_matmul_token<T, 8, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
     }
 }
 
-template <typename T>
-static gptq_status launch_rows(const TokenArg &p, int bits, bool wide, dim3 grid, cudaStream_t st) {
-    if (p.m.w.g_idx)
-        return wide ? launch_token<T, 2, true>(p, bits, grid, st) : launch_token<T, 1, true>(p, bits, grid, st);
-    return wide ? launch_token<T, 2, false>(p, bits, grid, st) : launch_token<T, 1, false>(p, bits, grid, st);
-}
-
 gptq_status matmul_token(const MatmulArg &m, int dtype, int bits, cudaStream_t st) {
+    constexpr int rows = 8;
     TokenArg p{};
     p.m = m;
     p.E = m.lora.R > 0 ? 1 : m.w.E;
     p.fold = m.w.groups > 0 ? 1 : 0;
     p.vec = aligned(m.w.words, 16) && m.w.ldw % 4 == 0;
     p.xvec = aligned(m.X, 16) && m.ldx % 8 == 0;
-    // one range: up to 16 rows at once; several: most have a few rows
-    const bool wide = p.E == 1 && m.M > 8;
-    const int rows = wide ? 16 : 8;
     p.rows = (int)std::min<int64_t>(rows, m.M);
     p.span = std::min((m.w.K + TK_SPAN - 1) / TK_SPAN, std::max(1, TK_SMEM / (p.rows * 2 * TK_SPAN))) * TK_SPAN;
+    // groups of rows there can be, at most: one of each range that has a row, and the full ones
     const int64_t items = p.E == 1 ? (m.M + rows - 1) / rows : std::min<int64_t>(p.E, m.M) + m.M / rows;
     const dim3 grid((m.w.N + TK_CH - 1) / TK_CH, (unsigned)items);
-    return dtype == GPTQ_BF16 ? launch_rows<__nv_bfloat16>(p, bits, wide, grid, st)
-                              : launch_rows<__half>(p, bits, wide, grid, st);
+    const bool indexed = m.w.g_idx != nullptr;
+    if (dtype == GPTQ_BF16)
+        return indexed ? launch_token<__nv_bfloat16, true>(p, bits, grid, st)
+                       : launch_token<__nv_bfloat16, false>(p, bits, grid, st);
+    return indexed ? launch_token<__half, true>(p, bits, grid, st) : launch_token<__half, false>(p, bits, grid, st);
 }
 
 }  // namespace gptq

@@ -238,7 +238,7 @@ def check_lora(c, y, start):
     W = c["L"]["W"][0]
     want = ref.lora(x, W, A, B, c["alpha"].astype(np.float64), c["o"], c["ids"], np.full((c["M"], c["N"]), start))
     S = ref.lora(np.abs(x), np.abs(W), np.abs(A), np.abs(B), c["alpha"], c["o"], c["ids"], np.zeros((c["M"], c["N"])))
-    fold = 1 if c["groupsize"] or c["M"] > 16 else 0
+    fold = 1 if c["groupsize"] or c["M"] > 8 else 0     # (the tiled kernel folds the scales)
     b = limit(want, S, c["K"] + 2 * c["rank"], c["t"], fold) + 2 * pair_eps(c["t"]) * S
     check(f64(y), want, b)
 
