@@ -429,10 +429,12 @@ static gptq_status launch_rank(RankArgs &q, int count, int dtype, cudaStream_t s
 }
 
 // What the backward pass needs first. Block 0: the requests of each adapter, in request order
-// (list_off [L + 1], list [R]; a thread takes whole adapters, so the order is fixed). The others:
+// (list_off [L + 1], list [R]; a thread takes whole adapters, so the order is fixed; list_off[0] is
+// -1 when offsets or ids are refused, which a caller without a status word would not see). The others:
 // out[l][j][n] = in[l][n][j], 16-bit elements, 32 x 32 tiles through shared memory.
 struct SetupArg {
-    const int32_t *ids;
+    const int32_t *offsets, *ids;
+    int64_t M;
     int R, L;
     int32_t *list_off, *list, *status;
     const uint16_t *in;
@@ -443,7 +445,8 @@ struct SetupArg {
 __device__ __forceinline__ void adapter_lists(const SetupArg &p) {
     __shared__ int warp_sum[8], base;
     if (threadIdx.x == 0) base = 0;
-    const bool bad = __syncthreads_or(ids_bad(p.ids, p.R, p.L, threadIdx.x, 256));
+    const bool bad = __syncthreads_or(ids_bad(p.ids, p.R, p.L, threadIdx.x, 256) ||
+                                      offsets_bad(p.offsets, p.R, p.M, threadIdx.x, 256));
     if (bad && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_ARG);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int a0 = 0; a0 < p.L; a0 += 256) {
@@ -472,7 +475,10 @@ __device__ __forceinline__ void adapter_lists(const SetupArg &p) {
             for (int w = 0; w < 8; ++w) base += warp_sum[w];
         __syncthreads();
     }
-    if (threadIdx.x == 0) p.list_off[p.L] = base;
+    if (threadIdx.x == 0) {
+        p.list_off[p.L] = base;
+        if (bad) p.list_off[0] = -1;
+    }
 }
 
 __global__ void __launch_bounds__(256) k_lora_setup(const __grid_constant__ SetupArg p) {
@@ -565,7 +571,7 @@ gptq_status matmul_lora_backward(MatmulArg m, float *dA, float *dB, const void *
     const int N = m.w.N, K = m.w.K;
     const LoraSpace s = lora_space(ws, true, m.M, N, K, l.R, l.L, l.rank);
     const bool need_u = (m.Y || dA) && m.M > 0, need_t = dB && m.M > 0;
-    SetupArg setup{l.ids, l.R, l.L, s.list_off, s.list, m.status, (const uint16_t *)B, (uint16_t *)s.Bt, N, l.rank};
+    SetupArg setup{m.offsets, l.ids, m.M, l.R, l.L, s.list_off, s.list, m.status, (const uint16_t *)B, (uint16_t *)s.Bt, N, l.rank};
     const int64_t tiles = need_u ? (int64_t)((N + 31) / 32) * ((l.rank + 31) / 32) * l.L : 0;
     gptq_status r = launch_pdl(k_lora_setup, dim3((unsigned)(1 + tiles)), 256, 0, 1, st, setup);
     if (r != GPTQ_OK) return r;

@@ -519,10 +519,11 @@ struct SumArg {
     float *out[2];
     int64_t n[2];
     int split[2];
+    const int32_t *list_off;            // -1 first: refused
 };
 __global__ void __launch_bounds__(256) k_sum_parts(const __grid_constant__ SumArg p, const int32_t *status) {
     grid_dependency();
-    if (failed(status)) return;
+    if (failed(status) || __ldcg(p.list_off) < 0) return;
     int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int w = i >= p.n[0] ? 1 : 0;
     if (w) i -= p.n[0];
@@ -610,6 +611,7 @@ gptq_status adapter_gradients(const AdapterGrad *grads, int count, int rank, int
                               const int32_t *list, int R, int L, int32_t *status, cudaStream_t st) {
     DwArg a[2] = {};
     SumArg sum{};
+    sum.list_off = list_off;
     int64_t n = 0;
     for (int i = 0; i < count; ++i) {
         const AdapterGrad &g = grads[i];

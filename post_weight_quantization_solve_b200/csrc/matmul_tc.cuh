@@ -23,9 +23,11 @@
 //
 // Adapters: after the steps of W^, each run of rows with one adapter adds
 // sum_j P_a[.][j] T[t][j] over the run's columns alone (runs are widened to the MMA's column borders,
-// the rows there that belong to others are zero in shared memory). T comes as a pair of 16-bit
-// halves, so the rank-space rows keep 16 bits. Runs of fewer than 16 rows (requests that decode)
-// are added by the threads that write the outputs: as matrix steps they cost about 1.3 us each.
+// the rows there that belong to others are zero in shared memory; an adapter's infinities and NaN,
+// which would meet those zeros, are left out of such a step and added to the run's own rows at the
+// end). T comes as two 16-bit parts (16 bits of a bf16 pair, 22 of an fp16 one): the outputs have
+// 8 or 11. Runs of fewer than 16 rows (requests that decode) are added by the threads that write
+// the outputs: as matrix steps they cost about 1.3 us each.
 //
 // Order: the tiles of a range run rows first, so that blocks that work at the same time read
 // different rows of X and the same (few) words; with channels first every block asked the L2
@@ -61,6 +63,7 @@ struct LoraRuns {
     int count;
     int begin[256 / LORA_SHORT], end[256 / LORA_SHORT], id[256 / LORA_SHORT];   // rows of the tile
     uint32_t starts[8], longs[8];       // a bit a row: a run starts, a long one
+    int broken;                         // infinities or NaN of an adapter were left out of a step
 };
 
 constexpr int MM_CACHED = 256;                       // offsets kept in shared memory
@@ -68,6 +71,74 @@ constexpr int MM_CACHED = 256;                       // offsets kept in shared m
 constexpr int MM_TABLE = ((MATMUL_MAX_EXPERTS + 4 + MM_CACHED + 4) * 4 + 256 * 2 + (int)sizeof(LoraRuns) + 15) / 16 * 16;
 constexpr uint32_t MM_TMEM = 512;
 constexpr int MM_MAX_STAGES = 4;                    // of 64 TMEM columns beside the accumulators
+
+// Whether a run's widened columns take in rows of others (a tile's columns past its last row are
+// written to nothing).
+__device__ __forceinline__ bool run_shares(int begin, int end, int n, int grain) {
+    return begin % grain != 0 || (end % grain != 0 && end < n);
+}
+
+// The infinities and NaN among 8 values set to zero; whether there were any. An exponent of ones
+// carries into the sign's place.
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite(uint32_t v) {
+    constexpr uint32_t e = Half2<T>::kType == 1 ? 0x7f807f80u : 0x7c007c00u;
+    return ((v & e) + (Half2<T>::kType == 1 ? 0x00800080u : 0x04000400u)) & 0x80008000u;
+}
+template <typename T>
+__device__ __forceinline__ bool finite_only(uint4 (&y)[8]) {
+    uint32_t any = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) any |= nonfinite<T>(y[j].x) | nonfinite<T>(y[j].y) | nonfinite<T>(y[j].z) | nonfinite<T>(y[j].w);
+    if (any == 0u) return false;
+    auto clear = [](uint32_t &v) {
+        const uint32_t bad = nonfinite<T>(v);
+        v &= ~((bad >> 15) * 0xffffu);
+    };
+#pragma unroll
+    for (int j = 0; j < 8; ++j) { clear(y[j].x); clear(y[j].y); clear(y[j].z); clear(y[j].w); }
+    return true;
+}
+
+// What finite_only left out, for the rows of the runs that it concerns, in the accumulators at `at`
+// or the sums at `dump` (both of this thread's channel).
+template <typename T, int DIR>
+__device__ __noinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *runs, int64_t t0, int n, int grain, int ch,
+                                           int channels, uint32_t at, float *dump) {
+    const int r = l.rank;
+    const T *T2 = static_cast<const T *>(l.T2);
+    for (int run = 0; run < runs->count; ++run) {
+        const int begin = runs->begin[run], end = runs->end[run];
+        if (!run_shares(begin, end, n, grain)) continue;
+        const unsigned short *P = reinterpret_cast<const unsigned short *>(l.P) + (int64_t)runs->id[run] * channels * r +
+                                  (DIR == 0 ? (int64_t)ch * r : ch);
+        const int64_t step = DIR == 0 ? 1 : channels;
+        uint32_t bad[4] = {0u, 0u, 0u, 0u};
+        if (ch < channels)
+            for (int j = 0; j < r; ++j)
+                if (nonfinite<T>(__ldg(P + j * step)) & 0x8000u) bad[j >> 5] |= 1u << (j & 31);
+        if (!__any_sync(~0u, (bad[0] | bad[1] | bad[2] | bad[3]) != 0u)) continue;
+        for (int row = begin; row < end; ++row) {
+            const T *t = T2 + (t0 + row) * (LORA_HALVES<T> * r);
+            float add = 0.f;
+            for (int w = 0; w < 4; ++w)
+                for (uint32_t left = bad[w]; left != 0u; left &= left - 1u) {
+                    const int j = 32 * w + __ffs(left) - 1;
+                    const float p = Half2<T>::unpack(__ldg(P + j * step)).x;
+                    add = fmaf(p, to_f32<T>(t[j]) + to_f32<T>(t[r + j]), add);
+                }
+            __syncwarp();
+            if (dump) {
+                dump[row * MM_LANES] += add;
+            } else {
+                const uint32_t y = tc::tmem_ld_32x32b_x1(at + row);
+                tc::tmem_ld_wait();
+                tc::tmem_st_32x32b_x1(at + row, __float_as_uint(__uint_as_float(y) + add));
+                tc::tmem_st_wait();
+            }
+        }
+    }
+}
 
 // The ring of packed words: a stage is 128 rows x 128 codes (16 B bytes a row), as a tiled copy
 // with the swizzle of that width lays it out (48-byte rows of 3 bits have none).
@@ -529,6 +600,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     const int b0 = run_begin & -GRAIN, b1 = (run_end + GRAIN - 1) & -GRAIN;
                     const int rows = PAIR ? (b1 - b0) / 2 : b1 - b0;
                     const int row0 = b0 + (PAIR ? (int)rank * rows : 0);
+                    const bool shares = run_shares(run_begin, run_end, t.n, GRAIN);
                     for (int hs = 0; hs < 2 * rsteps; ++hs, ++half) {
                         const int side = hs & 1, rs = hs >> 1;
                         RingPos pos = base;
@@ -556,6 +628,10 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                             for (int j = 0; j < 8; ++j) y[j] = load8<T>(src + 8 * j, qa < two_r ? m.w.K - c - 8 * j : 0, v8);
                         }
                         bool ok = tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort);
+                        if (shares && finite_only<T>(y)) {
+                            runs->broken = 1;
+                            __threadfence_block();
+                        }
                         ok = __all_sync(~0u, ok);
                         if (ok) {
                             uint8_t *st = smem + pos.stage * stage_bytes;
@@ -675,7 +751,10 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         row_ids[r] = 0xffff;            // its term is a matrix step's
                     }
                 }
-                if (etid == 0) runs->count = free ? count : 0;      // (a time-out leaves no list)
+                if (etid == 0) {
+                    runs->count = free ? count : 0;                 // (a time-out leaves no list)
+                    if (free) runs->broken = 0;
+                }
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 if (adapters) {
                     if (lane == 0) tc::mbar_arrive(lfull);
@@ -718,7 +797,9 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     else tc::mbar_arrive(&tempty[acc]);
                 }
             };
+            const bool broken = m.lora.R > 0 && ok && __any_sync(~0u, *(volatile int *)&runs->broken != 0);
             if (split == 1) {
+                if (broken) add_nonfinite<T, DIR>(m.lora, runs, t.t0, t.n, GRAIN, ch, p.out, at, nullptr);
                 if (shorts && ok) {
                     // their terms into the accumulators
                     for (int r = 0; r < t.n; r += 4) {
@@ -801,6 +882,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                             *d = mine ? *d + __uint_as_float(y[j]) : __uint_as_float(y[j]);
                         }
                     }
+                    if (broken)
+                        add_nonfinite<T, DIR>(m.lora, runs, t.t0, t.n, GRAIN, ch, p.out, 0u, dump + wq * 32 + lane);
                 }
                 release();
                 if (lane < split)

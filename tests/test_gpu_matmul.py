@@ -323,6 +323,50 @@ def test_many_tiles_a_block(dtype, K, N, rank):
           + floor * rank * np.abs(arrays[3]).max())
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("counts,K,N", [([37, 70, 21, 100], 264, 200), ([37, 70, 21, 100] * 12, 136, 2568)])
+@pytest.mark.parametrize("dtype,rank", [("bf16", 16), ("fp16", 72)])
+def test_a_broken_adapter_stays_with_its_rows(value, counts, K, N, dtype, rank):
+    # runs end between the columns that a matrix step takes, so a step holds rows of neighbours
+    ids = [0, 1, 2, 1] * (len(counts) // 4)
+    c = lora_case(7, dtype, 4, 32, counts, ids, 3, rank, N, K, pad=3)
+    own = torch.zeros(c["M"], dtype=torch.bool, device="cuda")
+    for r, a in enumerate(ids):
+        own[int(c["o"][r]):int(c["o"][r + 1])] = a == 0
+    clean = gq.gptq_matmul_lora(c["X"], *c["args"], out=torch.zeros(c["M"], N, dtype=c["t"], device="cuda"))
+    c["B"][0, 5, 3] = value
+    c["B"][0, 150, rank - 1] = -value
+    out = gq.gptq_matmul_lora(c["X"], *c["args"], out=torch.zeros(c["M"], N, dtype=c["t"], device="cuda"))
+    assert torch.equal(out[~own], clean[~own])
+    want = ref.lora(f64(c["X"]), c["L"]["W"][0], f64(c["A"]), f64(c["B"]), c["alpha"].astype(np.float64), c["o"],
+                    c["ids"], np.zeros((c["M"], N)))
+    got = f64(out)
+    bad = ~np.isfinite(want)
+    assert bad[own.cpu().numpy()][:, [5, 150]].all() and (np.isfinite(got) == ~bad).all()
+    assert np.array_equal(got[bad], want[bad], equal_nan=True)
+    # the input gradient of a layer as wide; a gradient of one adapter from rows of its own alone
+    c = lora_case(8, dtype, 4, 32, counts, ids, 3, rank, K, N, pad=3)
+    fresh = lambda: torch.zeros(c["M"], N, dtype=c["t"], device="cuda")
+    clean = gq.gptq_matmul_lora_backward(c["dY"], c["X"], *c["args"], dX=fresh())
+    c["A"][0, 3, 5] = value
+    c["A"][0, rank - 1, 150] = -value
+    dX, dA, dB = gq.gptq_matmul_lora_backward(c["dY"], c["X"], *c["args"], dX=fresh())
+    assert torch.equal(dX[~own], clean[0][~own])
+    want = ref.lora_backward(f64(c["dY"]), f64(c["X"]), c["L"]["W"][0], f64(c["A"]), f64(c["B"]),
+                             c["alpha"].astype(np.float64), c["o"], c["ids"], np.zeros((c["M"], N)))
+    got, bad = f64(dX), ~np.isfinite(want[0])
+    assert bad[own.cpu().numpy()][:, [5, 150]].all() and (np.isfinite(got) == ~bad).all()
+    assert np.array_equal(got[bad], want[0][bad], equal_nan=True)
+    assert torch.equal(dA, clean[1]) and torch.equal(dB[1:], clean[2][1:]) and not torch.isfinite(dB[0]).all()
+    # non-finite rows of one request (its neighbours', in T, U, dX and the other adapters' gradients)
+    c["A"][0, 3, 5] = c["A"][0, rank - 1, 150] = 0
+    clean = gq.gptq_matmul_lora_backward(c["dY"], c["X"], *c["args"], dX=fresh())
+    c["X"][own], c["dY"][own] = value, -value
+    dX, dA, dB = gq.gptq_matmul_lora_backward(c["dY"], c["X"], *c["args"], dX=fresh())
+    assert torch.equal(dX[~own], clean[0][~own]) and not torch.isfinite(dX[own]).any()
+    assert torch.equal(dA[1:], clean[1][1:]) and torch.equal(dB[1:], clean[2][1:])
+
+
 def test_lora_gradients_against_differences():
     # the loss sum(G * Y) is linear in each of X, A and B: a difference along a direction is exact
     c = lora_case(3, "bf16", 4, 0, [9, 30, 2], [0, 1, 0], 2, 8, 64, 96)
@@ -420,6 +464,19 @@ def test_bad_adapter_ids_and_groups_are_refused(n):
     status = gq.new_status()
     gq.gptq_matmul_grouped(c["X"], L["words"], L["s"], 4, None, 32, g, status=status)
     assert int(status.item()) == gq.GPTQ_ERR_ARG
+
+
+def test_refusals_without_a_status_write_nothing():
+    # rows enough for the adapters' gradients to be summed from parts
+    c = lora_case(3, "bf16", 4, 0, [2000, 1], [0, 1], 2, 8, 48, 64)
+    for at, bad in ((6, [0, 2000, 1999]), (7, [0, 5])):
+        args = list(c["args"])
+        args[at] = dev(np.array(bad, dtype=np.int32))
+        x = torch.full((2001, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        ga, gb = torch.full((2, 8, 64), 7.0, device="cuda"), torch.full((2, 48, 8), 7.0, device="cuda")
+        gq.gptq_matmul_lora_backward(c["dY"], c["X"], *args, dX=x, dA=ga, dB=gb)
+        for o in (x, ga, gb):
+            assert (o == 7).all()
 
 
 def test_a_failed_status_skips_the_call():
