@@ -88,45 +88,38 @@ __device__ __forceinline__ uint32_t nonfinite(uint32_t v) {
 template <typename T>
 __device__ __forceinline__ bool finite_only(uint4 (&y)[8]) {
     uint32_t any = 0u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) any |= nonfinite<T>(y[j].x) | nonfinite<T>(y[j].y) | nonfinite<T>(y[j].z) | nonfinite<T>(y[j].w);
-    if (any == 0u) return false;
-    auto clear = [](uint32_t &v) {
+    auto clear = [&](uint32_t &v) {
         const uint32_t bad = nonfinite<T>(v);
+        any |= bad;
         v &= ~((bad >> 15) * 0xffffu);
     };
 #pragma unroll
     for (int j = 0; j < 8; ++j) { clear(y[j].x); clear(y[j].y); clear(y[j].z); clear(y[j].w); }
-    return true;
+    return any != 0u;
 }
 
 // What finite_only left out, for the rows of the runs that it concerns, in the accumulators at `at`
 // or the sums at `dump` (both of this thread's channel).
 template <typename T, int DIR>
-__device__ __noinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *runs, int64_t t0, int n, int grain, int ch,
-                                           int channels, uint32_t at, float *dump) {
-    const int r = l.rank;
-    const T *T2 = static_cast<const T *>(l.T2);
+__device__ __forceinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *runs, int64_t t0, int n, int grain, int ch,
+                                              int channels, uint32_t at, float *dump) {
+#pragma unroll 1
     for (int run = 0; run < runs->count; ++run) {
-        const int begin = runs->begin[run], end = runs->end[run];
-        if (!run_shares(begin, end, n, grain)) continue;
-        const unsigned short *P = reinterpret_cast<const unsigned short *>(l.P) + (int64_t)runs->id[run] * channels * r +
-                                  (DIR == 0 ? (int64_t)ch * r : ch);
-        const int64_t step = DIR == 0 ? 1 : channels;
-        uint32_t bad[4] = {0u, 0u, 0u, 0u};
-        if (ch < channels)
-            for (int j = 0; j < r; ++j)
-                if (nonfinite<T>(__ldg(P + j * step)) & 0x8000u) bad[j >> 5] |= 1u << (j & 31);
-        if (!__any_sync(~0u, (bad[0] | bad[1] | bad[2] | bad[3]) != 0u)) continue;
-        for (int row = begin; row < end; ++row) {
-            const T *t = T2 + (t0 + row) * (LORA_HALVES<T> * r);
+        if (!run_shares(runs->begin[run], runs->end[run], n, grain)) continue;
+#pragma unroll 1
+        for (int row = runs->begin[run]; row < runs->end[run]; ++row) {
+            const unsigned short *P = static_cast<const unsigned short *>(l.P) + (int64_t)runs->id[run] * channels * l.rank +
+                                      (DIR == 0 ? (int64_t)ch * l.rank : ch);
+            const T *t = static_cast<const T *>(l.T2) + (t0 + row) * (LORA_HALVES<T> * l.rank);
             float add = 0.f;
-            for (int w = 0; w < 4; ++w)
-                for (uint32_t left = bad[w]; left != 0u; left &= left - 1u) {
-                    const int j = 32 * w + __ffs(left) - 1;
-                    const float p = Half2<T>::unpack(__ldg(P + j * step)).x;
-                    add = fmaf(p, to_f32<T>(t[j]) + to_f32<T>(t[r + j]), add);
+            if (ch < channels) {
+#pragma unroll 1
+                for (int j = l.rank; j > 0; --j, ++t, P += DIR == 0 ? 1 : channels) {
+                    const uint32_t v = __ldg(P);
+                    if (nonfinite<T>(v) & 0x8000u)
+                        add = fmaf(Half2<T>::unpack(v).x, to_f32<T>(t[0]) + to_f32<T>(t[l.rank]), add);
                 }
+            }
             __syncwarp();
             if (dump) {
                 dump[row * MM_LANES] += add;
