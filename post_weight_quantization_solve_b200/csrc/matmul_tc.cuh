@@ -99,10 +99,10 @@ __device__ __forceinline__ bool finite_only(uint4 (&y)[8]) {
 }
 
 // What finite_only left out, for the rows of the runs that it concerns, in the accumulators at `at`
-// or the sums at `dump` (both of this thread's channel).
+// (this thread's channel).
 template <typename T, int DIR>
-__device__ __forceinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *runs, int64_t t0, int n, int grain, int ch,
-                                              int channels, uint32_t at, float *dump) {
+__device__ __noinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *runs, int64_t t0, int n, int grain, int ch,
+                                              int channels, uint32_t at) {
 #pragma unroll 1
     for (int run = 0; run < runs->count; ++run) {
         if (!run_shares(runs->begin[run], runs->end[run], n, grain)) continue;
@@ -121,14 +121,10 @@ __device__ __forceinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *
                 }
             }
             __syncwarp();
-            if (dump) {
-                dump[row * MM_LANES] += add;
-            } else {
-                const uint32_t y = tc::tmem_ld_32x32b_x1(at + row);
-                tc::tmem_ld_wait();
-                tc::tmem_st_32x32b_x1(at + row, __float_as_uint(__uint_as_float(y) + add));
-                tc::tmem_st_wait();
-            }
+            const uint32_t y = tc::tmem_ld_32x32b_x1(at + row);
+            tc::tmem_ld_wait();
+            tc::tmem_st_32x32b_x1(at + row, __float_as_uint(__uint_as_float(y) + add));
+            tc::tmem_st_wait();
         }
     }
 }
@@ -790,9 +786,9 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     else tc::mbar_arrive(&tempty[acc]);
                 }
             };
-            const bool broken = m.lora.R > 0 && ok && __any_sync(~0u, *(volatile int *)&runs->broken != 0);
+            if (m.lora.R > 0 && ok && __any_sync(~0u, *(volatile int *)&runs->broken != 0))
+                add_nonfinite<T, DIR>(m.lora, runs, t.t0, t.n, GRAIN, ch, p.out, at);
             if (split == 1) {
-                if (broken) add_nonfinite<T, DIR>(m.lora, runs, t.t0, t.n, GRAIN, ch, p.out, at, nullptr);
                 if (shorts && ok) {
                     // their terms into the accumulators
                     for (int r = 0; r < t.n; r += 4) {
@@ -875,8 +871,6 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                             *d = mine ? *d + __uint_as_float(y[j]) : __uint_as_float(y[j]);
                         }
                     }
-                    if (broken)
-                        add_nonfinite<T, DIR>(m.lora, runs, t.t0, t.n, GRAIN, ch, p.out, 0u, dump + wq * 32 + lane);
                 }
                 release();
                 if (lane < split)
