@@ -429,7 +429,7 @@ static gptq_status launch_rank(RankArgs &q, int count, int dtype, cudaStream_t s
 }
 
 // What the backward pass needs first. Block 0: the requests of each adapter, in request order
-// (list_off [L + 1], list [R]; a thread takes whole adapters, so the order is fixed; list_off[0] is
+// (list_off [L + 1], list [R]; a warp takes whole adapters, 32 requests at a time; list_off[0] is
 // -1 when offsets or ids are refused, which a caller without a status word would not see). The others:
 // out[l][j][n] = in[l][n][j], 16-bit elements, 32 x 32 tiles through shared memory.
 struct SetupArg {
@@ -444,17 +444,29 @@ struct SetupArg {
 
 __device__ __forceinline__ void adapter_lists(const SetupArg &p) {
     __shared__ int warp_sum[8], base;
-    if (threadIdx.x == 0) base = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool bad = __syncthreads_or(ids_bad(p.ids, p.R, p.L, threadIdx.x, 256) ||
                                       offsets_bad(p.offsets, p.R, p.M, threadIdx.x, 256));
-    if (bad && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_ARG);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (bad) {
+        if (threadIdx.x == 0) {
+            set_status(p.status, GPTQ_ERR_ARG);
+            p.list_off[0] = -1;
+        }
+        return;
+    }
+    auto uses = [&](int i, int a) { return __ballot_sync(~0u, i < p.R && __ldg(p.ids + i) == a); };
+    if (threadIdx.x == 0) p.list_off[0] = base = 0;
+    for (int a = warp; a < p.L; a += 8) {
+        int n = 0;
+#pragma unroll 4
+        for (int i = 0; i < p.R; i += 32) n += __popc(uses(i + lane, a));
+        if (lane == 0) p.list_off[a + 1] = n;
+    }
+    __syncthreads();
+    // counts to ends
     for (int a0 = 0; a0 < p.L; a0 += 256) {
         const int a = a0 + threadIdx.x;
-        int n = 0;
-        if (a < p.L && !bad)
-            for (int i = 0; i < p.R; ++i) n += __ldg(p.ids + i) == a;
-        int sum = n;
+        int sum = a < p.L ? p.list_off[a + 1] : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int v = __shfl_up_sync(~0u, sum, d);
@@ -462,22 +474,20 @@ __device__ __forceinline__ void adapter_lists(const SetupArg &p) {
         }
         if (lane == 31) warp_sum[warp] = sum;
         __syncthreads();
-        int at = base + sum - n;
-        for (int w = 0; w < warp; ++w) at += warp_sum[w];
-        if (a < p.L) {
-            p.list_off[a] = at;
-            if (!bad)
-                for (int i = 0, k = at; i < p.R; ++i)
-                    if (__ldg(p.ids + i) == a) p.list[k++] = i;
-        }
+        sum += base;
+        for (int w = 0; w < warp; ++w) sum += warp_sum[w];
+        if (a < p.L) p.list_off[a + 1] = sum;
         __syncthreads();
-        if (threadIdx.x == 0)
-            for (int w = 0; w < 8; ++w) base += warp_sum[w];
+        if (threadIdx.x == 255) base = sum;
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        p.list_off[p.L] = base;
-        if (bad) p.list_off[0] = -1;
+    for (int a = warp; a < p.L; a += 8) {
+        int at = p.list_off[a];
+        for (int i = 0; i < p.R; i += 32) {
+            const unsigned b = uses(i + lane, a);
+            if (b >> lane & 1u) p.list[at + __popc(b & ((1u << lane) - 1u))] = i + lane;
+            at += __popc(b);
+        }
     }
 }
 

@@ -367,6 +367,21 @@ def test_a_broken_adapter_stays_with_its_rows(value, counts, K, N, dtype, rank):
     assert torch.equal(dA[1:], clean[1][1:]) and torch.equal(dB[1:], clean[2][1:])
 
 
+@pytest.mark.parametrize("requests,adapters", [(1200, 300), (33, 257), (1, 1)])
+def test_lora_gradients_of_many_requests(requests, adapters):
+    rng = gen(requests)
+    counts = [int(v) for v in rng.integers(0, 4, requests)]
+    ids = [int(v) for v in rng.integers(-1, adapters, requests)]
+    c = lora_case(11, "bf16", 4, 0, counts, ids, adapters, 8, 40, 72, pad=1)
+    _, dA, dB = gq.gptq_matmul_lora_backward(c["dY"], c["X"], *c["args"], want=(False, True, True))
+    arrays = [f64(c["dY"]), f64(c["X"]), c["L"]["W"][0], f64(c["A"]), f64(c["B"])]
+    al, z = c["alpha"].astype(np.float64), np.zeros((c["M"], 72))
+    want = ref.lora_backward(*arrays, al, c["o"], c["ids"], z)
+    S = ref.lora_backward(*map(np.abs, arrays), al, c["o"], c["ids"], z)
+    for got, w, s in ((dA, want[1], S[1]), (dB, want[2], S[2])):
+        check(f64(got), w, ((72 + min(c["M"], 512) + c["M"] // 512 + 20) * 2.0 ** -23 + 2 * part_eps(c["t"])) * s + 1e-30)
+
+
 def test_lora_gradients_against_differences():
     # the loss sum(G * Y) is linear in each of X, A and B: a difference along a direction is exact
     c = lora_case(3, "bf16", 4, 0, [9, 30, 2], [0, 1, 0], 2, 8, 64, 96)
