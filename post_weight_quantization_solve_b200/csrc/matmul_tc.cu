@@ -67,14 +67,15 @@ gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStre
     // leaves machine idle.
     const int64_t mean = m.M / p.E;
     const bool pair = mean > 128 && p.out > MM_LANES && 2 * tiles(2 * MM_LANES, 256) >= sms;
+    // (beside the words of 8 bits, the partial sums of 128 rows would leave the input gradient one
+    // operand stage: its split tiles have 64 rows)
     p.cols = pair ? 256 : 128;
     p.split = 1;
+    const int split_cols = dir == 1 && bits == 8 ? 64 : 128;
     if (!pair)
-        while (p.split < 8 && tiles(MM_LANES, p.cols) <= matmul_tc_clusters(2 * p.split) && steps >= 4 * p.split)
+        while (p.split < 8 && tiles(MM_LANES, split_cols) <= matmul_tc_clusters(2 * p.split) && steps >= 4 * p.split)
             p.split *= 2;
-    // beside the words of 8 bits, the partial sums of 128 rows would leave the input gradient one
-    // operand stage
-    if (p.split > 1 && dir == 1 && bits == 8) p.cols = 64;
+    if (p.split > 1) p.cols = split_cols;
     // large boxes of X (few copies to issue), smaller ones where most ranges have a few rows
     p.box_rows = mean <= 32 ? 32 : mean <= 64 ? 64 : MM_ROWS;
     CUtensorMap map{};
