@@ -485,6 +485,17 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 const int arow = side * 64 + arow64;
                 const float sc[2] = {ahead[0], ahead[1]};
                 if (scaled) fetch();
+                // by g_idx: where the scales of this lane's columns are, of 32 each
+                int place[2] = {0, 0};
+                if constexpr (IDX) {
+                    if (p.idx_table) {
+                        const int32_t *gi = m.w.g_idx + (int64_t)t.e * m.w.K;
+                        const int c = DIR == 0 ? step * MM_BK + side * 64 : t.c0 + ahalf * 64;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            place[q] = group_place(gi, c + 32 * q + lane, m.w.K, m.w.groups, UNPACKERS, m.status);
+                    }
+                }
                 uint32_t raw[2][B];
                 bool ok = tc::mbar_wait(&wfull[wpos.stage], wpos.phase, abort);
                 {
@@ -530,7 +541,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         if (c < m.w.K) {
                             const int32_t *gi = m.w.g_idx + (int64_t)t.e * m.w.K;
                             if (p.idx_table)
-                                scale32_by_table<T>(v[q], own_scales + tid, UNPACKERS, gi, c, m.w.K, m.w.groups, m.status);
+                                scale32_by_table<T>(v[q], own_scales + tid, place[q]);
                             else if (n < m.w.N)
                                 scale32_by_index<T, B, true>(v[q], m.w.scales + (erow + n) * m.w.groups, gi, c, m.w.K,
                                                              m.w.groups, m.status);
