@@ -113,6 +113,68 @@ def test_forward_row_pitch(rows, xpad):
     forward_case("bf16", 4, 64, False, [rows], 96, 128, xpad=xpad)
 
 
+@pytest.mark.parametrize("experts", [257, 512])
+@pytest.mark.parametrize("most", [3, 12])
+def test_many_experts(experts, most):
+    # a few rows each, with ranges of several fragments (most 3), and enough rows for tiles
+    rng = gen(experts + most)
+    counts = [int(v) for v in rng.integers(0, most, experts)]
+    counts[0], counts[experts // 2], counts[-1] = 20, 8, 9
+    forward_case("bf16", 4, 32, False, counts, 40, 72, pad=1)
+    forward_case("fp16", 3, 0, False, counts, 33, 130, first=1)
+    forward_case("bf16", 2, 32, True, counts, 40, 72)
+    o = off(counts)
+    dY, X = rows_of(rng, (int(o[-1]), 40), torch.bfloat16).cuda(), rows_of(rng, (int(o[-1]), 72), torch.bfloat16).cuda()
+    G = gq.gptq_matmul_grouped_dw(dY, X, dev(o))
+    d, x = f64(dY), f64(X)
+    check(f64(G), ref.grouped_dw(d, x, o), 30 * 2.0 ** -23 * ref.grouped_dw(np.abs(d), np.abs(x), o) + 1e-30)
+    L = layer(rng, experts, 40, 72, 4, 32, False)
+    dX = gq.gptq_matmul_grouped_dx(dY, L["words"], L["s"], 4, 72, dev(o), 32)
+    Wt = L["W"].transpose(0, 2, 1)
+    z = np.zeros((int(o[-1]), 72))
+    want, S = ref.grouped(d, Wt, o, z), ref.grouped(np.abs(d), np.abs(Wt), o, z)
+    check(f64(dX), want, limit(want, S, 40, torch.bfloat16, 1))
+
+
+def test_offsets_past_32_bits():
+    # rows that begin 2.4e9 values into their tensors
+    M, K, N, n = 300000, 8192, 40, 150
+    rng, t = gen(1), torch.bfloat16
+    L = layer(rng, 2, N, K, 4, 128, False)
+    o = np.array([0, M - n, M], dtype=np.int32)
+    X = torch.zeros(M, K, dtype=t, device="cuda")
+    X[-n:] = rows_of(rng, (n, K), t).cuda()
+    dY = torch.zeros(M, N, dtype=t, device="cuda")
+    dY[-n:] = rows_of(rng, (n, N), t).cuda()
+    x, d, W = f64(X[-n:]), f64(dY[-n:]), L["W"][1]
+    y = gq.gptq_matmul_grouped(X, L["words"], L["s"], 4, dev(o), 128)
+    want, S = x @ W.T, np.abs(x) @ np.abs(W).T
+    check(f64(y[-n:]), want, limit(want, S, K, t, 1))
+    dX = gq.gptq_matmul_grouped_dx(dY, L["words"], L["s"], 4, K, dev(o), 128)
+    want, S = d @ W, np.abs(d) @ np.abs(W)
+    check(f64(dX[-n:]), want, limit(want, S, N, t, 1))
+    assert not dX[:-n].any() and not y[:-n].any()
+    del dX
+    G = gq.gptq_matmul_grouped_dw(dY, X, dev(o))
+    check(f64(G[1]), d.T @ x, (n + 4) * 2.0 ** -23 * (np.abs(d).T @ np.abs(x)) + 1e-30)
+    assert not G[0].any()
+    A, B = rows_of(rng, (1, 8, K), t, K ** -0.5).cuda(), rows_of(rng, (1, N, 8), t, 0.1).cuda()
+    alpha, ids = torch.ones(1, device="cuda"), dev(np.array([-1, 0], dtype=np.int32))
+    args = (L["words"][1], L["s"][1], 4, A, B, alpha, dev(o), ids, 128)
+    y = gq.gptq_matmul_lora(X, *args)
+    arrays = [x, W, f64(A), f64(B)]
+    tail, z = [0, n], np.zeros((n, N))
+    want = ref.lora(*arrays, [1.0], tail, [0], z)
+    S = ref.lora(*map(np.abs, arrays), [1.0], tail, [0], z)
+    check(f64(y[-n:]), want, limit(want, S, K + 16, t, 1) + 2 * pair_eps(t) * S)
+    dX, dA, dB = gq.gptq_matmul_lora_backward(dY, X, *args)
+    want = ref.lora_backward(d, *arrays, [1.0], tail, [0], np.zeros((n, K)))
+    S = ref.lora_backward(*map(np.abs, [d, *arrays]), [1.0], tail, [0], np.zeros((n, K)))
+    check(f64(dX[-n:]), want[0], limit(want[0], S[0], N + 16, t, 1) + 2 * pair_eps(t) * S[0])
+    for got, w, s in ((dA, want[1], S[1]), (dB, want[2], S[2])):
+        check(f64(got), w, ((K + n + 20) * 2.0 ** -23 + 2 * part_eps(t)) * s + 1e-30)
+
+
 @pytest.mark.parametrize("K,N", [(256, 2560), (201, 2571)])
 @pytest.mark.parametrize("counts", [[1500, 0, 2500], [200] * 20, [60] * 20])
 def test_forward_many_tiles_a_block(K, N, counts):
