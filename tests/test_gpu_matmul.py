@@ -612,6 +612,29 @@ def test_streams_and_graphs():
         assert torch.equal(a, b)
 
 
+def test_new_outputs_on_another_stream():
+    # the current stream is still writing memory that it has freed: a new output of a call on
+    # another stream is not that memory
+    M, K, N = 64, 256, 4096
+    rng = gen(12)
+    L = layer(rng, 1, N, K, 4, 0)
+    X = rows_of(rng, (M, K), torch.bfloat16).cuda()
+    want = gq.gptq_matmul_grouped(X, L["words"], L["s"], 4)
+    big = torch.ones(1 << 28, device="cuda")
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for _ in range(4):
+            big.mul_(1.0)
+        old = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        old.fill_(3.0)
+        del old
+        y = gq.gptq_matmul_grouped(X, L["words"], L["s"], 4, stream=other)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        del y
+
+
 def test_together():
     # a layer as a user has it: quantised with input groups and act-order, packed, multiplied by
     # experts' rows, gradients back through it, the gradient into the first-order start
