@@ -525,8 +525,13 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&wempty[wpos.stage]);
+                // (by g_idx the words wait for a call that scales the first half of them, and were seen to
+                // change under it: the stage is released behind it)
+                auto words_read = [&]() {
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&wempty[wpos.stage]);
+                };
+                if constexpr (!IDX) words_read();
                 if constexpr (IDX) {
                     // this thread's row of scales, in its own column of the table (forward: once a tile)
                     const int n = DIR == 0 ? ch : step * MM_BK + arow;
@@ -555,6 +560,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         if (p.fold) scale32<T>(v[q], sc[q]);
                     }
                 }
+                if constexpr (IDX) words_read();
                 ok = tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort) && ok;
                 ok = __all_sync(~0u, ok);
                 if (ok) {

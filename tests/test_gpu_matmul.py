@@ -113,6 +113,21 @@ def test_forward_row_pitch(rows, xpad):
     forward_case("bf16", 4, 64, False, [rows], 96, 128, xpad=xpad)
 
 
+@pytest.mark.parametrize("K", [1600, 4200, 9000, 12032])
+@pytest.mark.parametrize("dtype,bits", [("bf16", 4), ("fp16", 8), ("fp16", 3)])
+def test_many_groups_by_index(K, dtype, bits):
+    # with and without room for tables of scales, words by tiled copies and by plain ones
+    forward_case(dtype, bits, 32, True, [40, 300], 200, K)
+    rng, t, counts = gen(K), TYPES[dtype], [130, 0, 21]
+    L = layer(rng, 3, 200, K, bits, 32, True)
+    o = off(counts)
+    dY = rows_of(rng, (151, 200), t).cuda()
+    dX = gq.gptq_matmul_grouped_dx(dY, L["words"], L["s"], bits, K, dev(o), 32, L["g"])
+    d, Wt, z = f64(dY), L["W"].transpose(0, 2, 1), np.zeros((151, K))
+    want, S = ref.grouped(d, Wt, o, z), ref.grouped(np.abs(d), np.abs(Wt), o, z)
+    check(f64(dX), want, limit(want, S, 200, t, 1))
+
+
 @pytest.mark.parametrize("experts", [257, 512])
 @pytest.mark.parametrize("most", [3, 12])
 def test_many_experts(experts, most):
