@@ -49,12 +49,13 @@
 #include <algorithm>
 
 #include "matmul.cuh"
+#include "unpack_turns.h"
 
 namespace gptq {
 
 constexpr int MM_LANES = 128;                       // output channels of a block's tile
 constexpr int MM_BK = 128;
-constexpr int MM_SETS = 3;                          // of four unpacking warps
+constexpr int MM_SETS = UNPACK_SETS;                // of four unpacking warps
 constexpr int MM_WARP_OUT = 4 * MM_SETS, MM_WARP_X = MM_WARP_OUT + 4, MM_WARP_MMA = MM_WARP_X + 1,
               MM_WARP_WORDS = MM_WARP_X + 2;
 constexpr int MM_THREADS = (MM_WARP_WORDS + 2) * 32;
@@ -433,9 +434,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         // forward: channel = lane of the warp's TMEM quarter, 64 of the step's columns. Input gradient:
         // one of 64 rows n of the step and half of the block's 128 columns.
         const int arow64 = (wq & 1) * 32 + lane, ahalf = wq >> 1;
-        // (halves of a tile's steps: h with (h + turn) % 3 == set, turn moving on with each tile)
-        auto first_half = [&](int turn) { return (set - turn + MM_SETS) % MM_SETS; };
-        const int turns = 2 * nmain % MM_SETS;
+        // (halves of a tile's steps in turn, as unpack_turns.h says)
+        auto first_half = [&](int turn) { return unpack_first_half(set, turn); };
 
         // Scales where they fold into the weights: requested one of this thread's steps ahead of the
         // unpacking, across tiles.
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         auto fetch_tile = [&]() {
             while (fu < tiles && fh >= 2 * nmain) {
                 fu += ngroups;
-                fturn = (fturn + turns) % MM_SETS;
+                fturn = unpack_next_turn(fturn, 2 * nmain);
                 fh = first_half(fturn);
             }
             if (fu >= tiles) return;
@@ -596,16 +596,16 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     if (lane == 0) arrive_full(pos.stage);
                 }
             }
-            turn = (turn + turns) % MM_SETS;
+            turn = unpack_next_turn(turn, 2 * nmain);
             wbase.jump(nmain, Ring::STAGES);
             base.jump(nmain, stages);
             if (adapters) {
                 grid_wait();
-                int half = 0;                           // halves of the adapters' steps, in turn too
+                int half = 0;                           // of the adapters' steps, in turn too
                 const T *P = static_cast<const T *>(m.lora.P);
                 const T *T2 = static_cast<const T *>(m.lora.T2);
                 const int r = m.lora.rank;
-                const int count = runs_wait() ? runs->count : 0;
+                const int count = runs_wait() ? runs->count : 0, halves = 2 * rsteps * count;
                 for (int run = 0; run < count; ++run) {
                     const int run_begin = runs->begin[run], run_end = runs->end[run], run_id = runs->id[run];
                     const int b0 = run_begin & -GRAIN, b1 = (run_end + GRAIN - 1) & -GRAIN;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         const int side = hs & 1, rs = hs >> 1;
                         RingPos pos = base;
                         if (side) base.advance(stages);
-                        if (half % MM_SETS != set) continue;
+                        if (unpack_adapter_set(turn, half, halves) != set) continue;
                         const int arow = side * 64 + arow64;
                         // this thread's part of A, requested before the stage is free. Forward: row n
                         // of B_a twice over, [hi part | lo part] of the contraction; input gradient:
