@@ -14,14 +14,14 @@ static size_t ring_bytes(int bits, int dir) {
     }
 }
 
-// The packed rows of all experts as boxes of 128 rows x 128 codes. False when the rows do not
+// The packed rows of all experts as boxes of `rows` rows x 128 codes. False when the rows do not
 // start on 16-byte boundaries.
-static bool words_map(CUtensorMap *map, const PackedArg &w, int bits) {
+static bool words_map(CUtensorMap *map, const PackedArg &w, int bits, int rows) {
     EncodeTiled enc = encode_tiled();
     if (!enc || !aligned(w.words, 16) || w.ldw % 4 != 0) return false;
     const cuuint64_t dim[2] = {(cuuint64_t)(((int64_t)w.K * bits + 31) / 32), (cuuint64_t)w.E * w.N};
     const cuuint64_t stride[1] = {(cuuint64_t)w.ldw * 4};
-    const cuuint32_t box[2] = {(cuuint32_t)(4 * bits), 128};
+    const cuuint32_t box[2] = {(cuuint32_t)(4 * bits), (cuuint32_t)rows};
     const cuuint32_t step[2] = {1, 1};
     const CUtensorMapSwizzle swizzle = bits == 2   ? CU_TENSOR_MAP_SWIZZLE_32B
                                        : bits == 3 ? CU_TENSOR_MAP_SWIZZLE_NONE
@@ -81,7 +81,7 @@ gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStre
     CUtensorMap map{};
     if (!rows_map(&map, m.X, dtype, m.M, p.inner, m.ldx, p.box_rows)) p.box_rows = 0;
     CUtensorMap wmap{};
-    p.wtiled = words_map(&wmap, m.w, bits);
+    p.wtiled = words_map(&wmap, m.w, bits, dir == 0 ? MmRing<4, 0>::ROWS : MmRing<4, 1>::ROWS);
     // two accumulators where they fit beside the forward product's A stages
     p.accs = dir == 1 || !pair ? 2 : 1;
     p.acc_cols = p.cols;

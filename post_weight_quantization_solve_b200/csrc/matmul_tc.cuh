@@ -135,14 +135,19 @@ __device__ __noinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *run
     }
 }
 
-// The ring of packed words: a stage is 128 rows x 128 codes (16 B bytes a row), as a tiled copy
-// with the swizzle of that width lays it out (48-byte rows of 3 bits have none).
+// The ring of packed words: rows of 128 codes (16 B bytes), as a tiled copy with the swizzle of that
+// width lays them out (48-byte rows of 3 bits have none). A stage is what is read together: the 128
+// channels of a step in the forward product, which two sets read, the 64 rows of half a step in the
+// input gradient, which one does. A multiple of three stages: then a set meets the same stages always,
+// and is there for every use of them (unpack_turns.h).
 template <int B, int DIR>
 struct MmRing {
     static constexpr int ROW = 16 * B;
-    static constexpr int STAGE = 128 * ROW;
+    static constexpr int ROWS = DIR == 0 ? 128 : 64;
+    static constexpr int STAGE = ROWS * ROW;
     // the input gradient's operand stages leave less room
-    static constexpr int STAGES = DIR == 1 ? (B == 2 ? 3 : 2) : B == 8 ? 3 : B == 4 ? 6 : B == 3 ? 7 : 8;
+    static constexpr int STAGES = B >= (DIR == 0 ? 8 : 4) ? 3 : 6;
+    static_assert(STAGES % UNPACK_SETS == 0, "a set's stages are its own");
     static constexpr int WORDS = STAGES * STAGE;
     static constexpr int BYTES = WORDS;
     // byte offset of 16-byte (3 bits: 8-byte) piece q of row r
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         tc::mbar_init(done, 4 * split);
         for (int s = 0; s < Ring::STAGES; ++s) {
             tc::mbar_init(&wfull[s], p.wtiled ? 1 : 64);
-            tc::mbar_init(&wempty[s], 8);
+            tc::mbar_init(&wempty[s], DIR == 0 ? 8 : 4);
         }
         tc::mbar_init(lfull, 4);
         // its readers: the unpacking warps, the X warp where it copies, the MMA warp where it issues
@@ -478,14 +483,12 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             const int64_t erow = (int64_t)t.e * m.w.N;
             const int ch = t.c0 + wq * 32 + lane;       // forward: this thread's channel
             RingPos wpos = wbase, pos = base;
-            int at = 0;                                 // the step that wpos and pos stand at
+            int at = 0, wat = 0;                        // the step that pos stands at, the words' stage
 #pragma unroll 1
             for (int h = first_half(turn); h < 2 * nmain; h += MM_SETS) {
                 const int side = h & 1;                 // which half of the step
-                for (; at < (h >> 1); ++at) {
-                    wpos.advance(Ring::STAGES);
-                    pos.advance(stages);
-                }
+                for (; at < (h >> 1); ++at) pos.advance(stages);
+                for (; wat < (DIR == 0 ? h >> 1 : h); ++wat) wpos.advance(Ring::STAGES);
                 const int step = k0 + at;
                 const int arow = side * 64 + arow64;
                 const float sc[2] = {ahead[0], ahead[1]};
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 {
                     const uint8_t *src = words + wpos.stage * Ring::STAGE;
                     // the row and first 16-byte (8-byte) piece that this thread unpacks
-                    const int wrow = DIR == 0 ? wq * 32 + lane : arow;
+                    const int wrow = DIR == 0 ? wq * 32 + lane : arow64;
                     const int wpiece = (DIR == 0 ? side : ahalf) * (B == 3 ? 3 : B / 2);
                     if constexpr (B == 3) {
 #pragma unroll
@@ -597,7 +600,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
             }
             turn = unpack_next_turn(turn, 2 * nmain);
-            wbase.jump(nmain, Ring::STAGES);
+            wbase.jump(DIR == 0 ? nmain : 2 * nmain, Ring::STAGES);
             base.jump(nmain, stages);
             if (adapters) {
                 grid_wait();
@@ -996,10 +999,10 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             }
         }
     } else if (warp >= MM_WARP_WORDS) {
-        // a stage: the block's channels x a step's columns (forward), or a step's rows x the block's
-        // columns
-        int stage = 0;
-        uint32_t phase = 0;
+        // a stage: the block's channels x a step's columns (forward), or half a step's rows x the
+        // block's columns
+        constexpr int PER = 128 / Ring::ROWS;       // stages of a step
+        RingPos pos{0, 0};
         bool ok = true;
         if (p.wtiled) {
             if (warp == MM_WARP_WORDS) {
@@ -1007,17 +1010,17 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
                     const int erow = t.e * m.w.N;
 #pragma unroll 1
-                    for (int i = 0; i < nmain; ++i) {
-                        ok = __all_sync(~0u, tc::mbar_wait(&wempty[stage], phase ^ 1, abort));
+                    for (int i = 0; i < PER * nmain; ++i) {
+                        ok = __all_sync(~0u, tc::mbar_wait(&wempty[pos.stage], pos.phase ^ 1, abort));
                         if (!ok) break;
                         const int k = DIR == 0 ? (k0 + i) * MM_BK : t.c0;
-                        const int n = DIR == 0 ? t.c0 : (k0 + i) * MM_BK;
+                        const int n = DIR == 0 ? t.c0 : k0 * MM_BK + i * Ring::ROWS;
                         if (tc::elect_one()) {
-                            tc::mbar_arrive_expect_tx(&wfull[stage], Ring::STAGE);
-                            tc::tma_load_2d(words + stage * Ring::STAGE, &wmap, &wfull[stage], (k >> 5) * B, erow + n);
+                            tc::mbar_arrive_expect_tx(&wfull[pos.stage], Ring::STAGE);
+                            tc::tma_load_2d(words + pos.stage * Ring::STAGE, &wmap, &wfull[pos.stage], (k >> 5) * B, erow + n);
                         }
                         __syncwarp();
-                        if (++stage == Ring::STAGES) { stage = 0; phase ^= 1; }
+                        pos.advance(Ring::STAGES);
                     }
                 }
                 if (!ok) {
@@ -1027,33 +1030,34 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
             }
         } else {
+            // half of a stage's rows a warp
             const int nw = (int)(((int64_t)m.w.K * B + 31) / 32);
             for (int u = group; u < tiles && ok; u += ngroups) {
                 const MmTile t = mm_tile(p, table, tiles_out, u, WIDTH, first, GRAIN);
                 const int64_t erow = (int64_t)t.e * m.w.N;
-                for (int i = 0; i < nmain; ++i) {
-                    ok = tc::mbar_wait(&wempty[stage], phase ^ 1, abort);
+                for (int i = 0; i < PER * nmain; ++i) {
+                    ok = tc::mbar_wait(&wempty[pos.stage], pos.phase ^ 1, abort);
                     ok = __all_sync(~0u, ok);
                     if (!ok) break;
                     const int w0 = ((DIR == 0 ? (k0 + i) * MM_BK : t.c0) >> 5) * B;
-                    const int n0 = DIR == 0 ? t.c0 : (k0 + i) * MM_BK;
+                    const int n0 = DIR == 0 ? t.c0 : k0 * MM_BK + i * Ring::ROWS;
                     // lanes take neighbouring words of as many whole rows as fit a warp
                     constexpr int RW = 4 * B, PW = B == 3 ? 2 : 4, RL = 32 / RW;    // words of a row, of a piece; rows
-                    const uint32_t dst = tc::smem_u32(words + stage * Ring::STAGE);
+                    const uint32_t dst = tc::smem_u32(words + pos.stage * Ring::STAGE);
                     const int sub = lane / RW, wd = lane - sub * RW;
                     if (sub < RL) {
                         const bool in = w0 + wd < nw;
-                        const int first_row = (warp - MM_WARP_WORDS) * 64 + sub, left = m.w.N - n0;
-                        const uint32_t *src = m.w.words + (erow + n0 + first_row) * m.w.ldw + w0 + wd;
+                        const int row0 = (warp - MM_WARP_WORDS) * (Ring::ROWS / 2), left = m.w.N - n0;
+                        const uint32_t *src = m.w.words + (erow + n0 + row0 + sub) * m.w.ldw + w0 + wd;
                         const int64_t by = RL * m.w.ldw;
 #pragma unroll 8
-                        for (int r = first_row; r < (warp - MM_WARP_WORDS) * 64 + 64; r += RL, src += by)
+                        for (int r = row0 + sub; r < row0 + Ring::ROWS / 2; r += RL, src += by)
                             copy_async<4>(dst + Ring::at(r, wd / PW) + (wd % PW) * 4, in && r < left ? src : nullptr,
                                           m.w.words);
                     }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&wfull[stage]))
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&wfull[pos.stage]))
                                  : "memory");
-                    if (++stage == Ring::STAGES) { stage = 0; phase ^= 1; }
+                    pos.advance(Ring::STAGES);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");

@@ -10,6 +10,10 @@
 // a row hold a half of every set. So a set that waits at step s for the product of step s - n (n
 // stages) has waited at step s - 1 or s - 2 before, for the product of step s - 2 - n or a later
 // one, and the use before, of step s - 2 n, is over.
+//
+// The words' stages are filled by copies, which land in any order. Their halves go to the sets in turn
+// over all tiles, so with a multiple of three stages (of a step, or of half a step) every use of a
+// stage is read by the same sets: they wait for each of them, one after the other.
 #pragma once
 
 #ifdef __CUDACC__

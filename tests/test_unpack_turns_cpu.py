@@ -68,8 +68,9 @@ struct Bar {
 };
 static void wait(const Bar &b, uint32_t parity) { while (!b.test(parity)) yield(); }
 
-// restart: the adapters' halves from the first set again for each tile
-struct Config { int stages, ring, main_steps, tiles; bool adapters, restart, copies_in_order; };
+// halves: a stage of words is half a step's. restart: the adapters' halves from the first set again for
+// each tile
+struct Config { int stages, ring, main_steps, tiles; bool adapters, halves, restart, copies_in_order; };
 static std::string fault;
 static void blame(const char *what) { if (fault.empty()) fault = what; }
 
@@ -84,7 +85,7 @@ static std::string run(const Config &c, unsigned seed) {
 
     Bar wfull[8], wempty[8], full[4], empty[4];
     int words[8], half[4][2], rows[4], unread[4] = {0, 0, 0, 0};
-    for (int i = 0; i < 8; ++i) { wfull[i].init(1); wempty[i].init(2); words[i] = -1; }
+    for (int i = 0; i < 8; ++i) { wfull[i].init(1); wempty[i].init(c.halves ? 1 : 2); words[i] = -1; }
     for (int i = 0; i < 4; ++i) { full[i].init(3); empty[i].init(1); half[i][0] = half[i][1] = rows[i] = -1; }
     std::deque<std::function<void()>> copies;
     std::deque<std::pair<int, int>> products;           // stage, step
@@ -93,7 +94,7 @@ static std::string run(const Config &c, unsigned seed) {
     spawn([&] {                                         // words
         RingPos p;
         for (int t = 0, s = 0; t < c.tiles; ++t)
-            for (int i = 0; i < c.main_steps; ++i, ++s) {
+            for (int i = 0; i < c.main_steps * (c.halves ? 2 : 1); ++i, ++s) {
                 wait(wempty[p.stage], p.phase ^ 1);
                 const int at = p.stage;
                 copies.push_back([&, at, s] { words[at] = s; wfull[at].arrive(); });
@@ -131,7 +132,7 @@ static std::string run(const Config &c, unsigned seed) {
             };
             for (int t = 0; t < c.tiles; ++t) {
                 for (int h = unpack_first_half(set, turn); h < 2 * c.main_steps; h += UNPACK_SETS) {
-                    const int w = first_words + (h >> 1);
+                    const int w = first_words + (c.halves ? h : h >> 1);
                     in.to(w - in_step, c.ring);
                     in_step = w;
                     const int at = in.stage;
@@ -143,7 +144,7 @@ static std::string run(const Config &c, unsigned seed) {
                     put(h & 1, first_step + (h >> 1));
                 }
                 turn = unpack_next_turn(turn, 2 * c.main_steps);
-                first_words += c.main_steps;
+                first_words += c.main_steps * (c.halves ? 2 : 1);
                 first_step += c.main_steps;
                 for (int h = 0; h < 2 * extra[t]; ++h)
                     if ((c.restart ? h % 3 : unpack_adapter_set(turn, h, 2 * extra[t])) == set)
@@ -207,13 +208,12 @@ static std::string run(const Config &c, unsigned seed) {
     return fault;
 }
 
-static int faults(Config c, int seeds) {
+static int faults(Config c, const std::vector<int> &rings, int seeds) {
     int bad = 0;
-    const int rings[] = {2, 3, 6, 7, 8};
     for (int seed = 0; seed < seeds && bad < 3; ++seed) {
         std::mt19937 r(seed * 7919 + 13);
         c.stages = 2 + (int)(r() % 3u);
-        c.ring = rings[r() % 5u];
+        c.ring = rings[r() % rings.size()];
         c.main_steps = 1 + (int)(r() % 9u);
         c.tiles = 1 + (int)(r() % 5u);
         const std::string f = run(c, seed);
@@ -229,10 +229,13 @@ static int faults(Config c, int seeds) {
 int main(int argc, char **argv) {
     const std::string what = argv[1];
     Config c{};
-    c.copies_in_order = true;
-    c.adapters = what != "main";
+    c.adapters = what.find("main") == std::string::npos;
+    c.halves = what.find("halves") != std::string::npos;
     c.restart = what == "restart";
-    std::printf("%d\n", faults(c, 4000));
+    std::vector<int> rings = {3, 6};
+    if (what.find("two stages") != std::string::npos) rings = {2};
+    if (what.find("four stages") != std::string::npos) rings = {4};
+    std::printf("%d\n", faults(c, rings, 4000));
 }
 """
 
@@ -252,16 +255,23 @@ def faults(tmp_path_factory):
     return count
 
 
-def test_operand_stages(faults):
-    for what in ("main", "adapters"):
-        n, first = faults(what)
-        assert n == 0, first
+@pytest.mark.parametrize("what", ["main", "adapters", "main halves", "adapters halves"])
+def test_rings(faults, what):
+    n, first = faults(what)
+    assert n == 0, first
 
 
 def test_the_program_sees_a_set_that_falls_behind(faults):
     # the adapters' halves from the first set again for each tile: a set may pass over three steps
     n, first = faults("restart")
     assert n > 0 and "standstill" not in first
+
+
+@pytest.mark.parametrize("what", ["main two stages", "main halves four stages"])
+def test_the_program_sees_words_that_land_late(faults, what):
+    # a stage that a set meets every other time, filled by copies that land in any order
+    n, first = faults(what)
+    assert n > 0 and "words" in first
 
 
 def test_any_two_steps_hold_every_set(tmp_path):
