@@ -487,8 +487,12 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
 #pragma unroll 1
             for (int h = first_half(turn); h < 2 * nmain; h += MM_SETS) {
                 const int side = h & 1;                 // which half of the step
-                for (; at < (h >> 1); ++at) pos.advance(stages);
-                for (; wat < (DIR == 0 ? h >> 1 : h); ++wat) wpos.advance(Ring::STAGES);
+                for (; at < (h >> 1); ++at) {
+                    pos.advance(stages);
+                    if (DIR == 0) wpos.advance(Ring::STAGES);
+                }
+                if constexpr (DIR == 1)
+                    for (; wat < h; ++wat) wpos.advance(Ring::STAGES);
                 const int step = k0 + at;
                 const int arow = side * 64 + arow64;
                 const float sc[2] = {ahead[0], ahead[1]};
