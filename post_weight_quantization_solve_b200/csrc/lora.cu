@@ -373,7 +373,7 @@ static gptq_status launch_rank_nr(RankArgs &q, int count, cudaStream_t st) {
         // many rows in a layout that tiled copies refuse: 64 rows a block share the adapter
         constexpr int KW = NR > 8 ? 1 : 2;
         for (int i = 0; i < count; ++i) q.a[i].split = 1;
-        return launch_pdl(k_rank_rows<T, NR, 4, KW>, dim3((unsigned)(p.R + p.M / 64), count), 128 * KW, 0, 1, st, q);
+        return launch_pdl(k_rank_rows<T, NR, 4, KW>, dim3((unsigned)(p.R + p.M / 64), count), 128 * KW, 0, 0, 1, st, q);
     }
     constexpr int KW = NR > 8 ? 4 : 8;
     const int steps = (std::min(p.inner, q.a[count - 1].inner) + 31) / 32;
@@ -381,7 +381,7 @@ static gptq_status launch_rank_nr(RankArgs &q, int count, cudaStream_t st) {
     const int64_t tiles = std::min<int64_t>(p.M, p.R + p.M / 16);
     while (split < 8 && tiles * count * split * 2 <= 2 * device_sms() && steps >= 4 * KW * split) split *= 2;
     for (int i = 0; i < count; ++i) q.a[i].split = split;
-    return launch_pdl(k_rank_rows<T, NR, 1, KW>, dim3((unsigned)(tiles * split), count), 32 * KW, 0, split, st, q);
+    return launch_pdl(k_rank_rows<T, NR, 1, KW>, dim3((unsigned)(tiles * split), count), 32 * KW, 0, 0, split, st, q);
 }
 
 template <typename T>
@@ -402,7 +402,7 @@ static gptq_status launch_rank(RankArgs &q, int count, int dtype, cudaStream_t s
             int split = 1;
             while (split < 8 && tiles * count * split * 2 <= device_sms() && steps >= 4 * split) split *= 2;
             for (int i = 0; i < count; ++i) q.a[i].split = split;
-            return launch_pdl(k_rank_tc<T>, dim3((unsigned)(tiles * split), count), RK_THREADS, RK_SMEM, split, st,
+            return launch_pdl(k_rank_tc<T>, dim3((unsigned)(tiles * split), count), RK_THREADS, RK_SMEM, RK_SMEM, split, st,
                               maps, q);
         }
     }
@@ -568,7 +568,7 @@ gptq_status matmul_lora_backward(MatmulArg m, float *dA, float *dB, const void *
     const bool need_u = (m.Y || dA) && m.M > 0, need_t = dB && m.M > 0;
     SetupArg setup{m.offsets, l.ids, m.M, l.R, l.L, s.list_off, s.list, m.status, (const uint16_t *)B, (uint16_t *)s.Bt, N, l.rank};
     const int64_t tiles = need_u ? (int64_t)((N + 31) / 32) * ((l.rank + 31) / 32) * l.L : 0;
-    gptq_status r = launch_pdl(k_lora_setup, dim3((unsigned)(1 + tiles)), 256, 0, 1, st, setup);
+    gptq_status r = launch_pdl(k_lora_setup, dim3((unsigned)(1 + tiles)), 256, 0, 0, 1, st, setup);
     if (r != GPTQ_OK) return r;
     RankArgs q{};
     int count = 0;

@@ -515,15 +515,20 @@ inline int device_sms() {
     return n > 0 ? n : 148;
 }
 
+constexpr size_t SMEM_MOST = 227 * 1024;                // dynamic shared memory of a block without static
+
 // One launch as a programmatic dependent of the previous kernel on the stream, in clusters of
-// `cluster` blocks along x.
+// `cluster` blocks along x, with `smem` bytes of dynamic shared memory; no launch of the kernel takes
+// more than `most`. The limit belongs to the kernel and the device, and another host thread's call may
+// come between setting it and the launch, so every call sets the same one.
 template <typename... KArgs, typename... Args>
-inline gptq_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
+inline gptq_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, size_t most,
                               int cluster, cudaStream_t st, Args... args) {
+    if (smem > most) return GPTQ_ERR_CUDA;
     // (kernels with dynamic shared memory have less than 24 KB of static)
-    if (smem > 24 * 1024 &&
+    if (most > 24 * 1024 &&
         cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) {
         cudaGetLastError();
         return GPTQ_ERR_CUDA;
     }

@@ -569,14 +569,14 @@ static gptq_status launch_dw(DwArg *a, int count, int dtype, cudaStream_t st) {
     }
     if (args.units > 0x7fffffff) return GPTQ_ERR_ARG;
     args.boxes = pair ? 4 : p.apart ? 2 + p.parts : 2 + (std::min(p.nq, DW_COLS) + 63) / 64;
-    args.stages = std::min(DW_MAX_STAGES, (227 * 1024 - DW_FIXED) / (args.boxes * DW_BOX));
+    args.stages = std::min(DW_MAX_STAGES, (int)((SMEM_MOST - DW_FIXED) / (args.boxes * DW_BOX)));
     const size_t smem = (size_t)args.stages * args.boxes * DW_BOX + DW_FIXED;
     const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(args.units, device_sms() / (pair ? 2 : 1))) * (pair ? 2 : 1);
     if (dtype == GPTQ_BF16)
-        return pair ? launch_pdl(k_matmul_dw<__nv_bfloat16, true>, dim3(blocks), DW_THREADS, smem, 2, st, maps, args)
-                    : launch_pdl(k_matmul_dw<__nv_bfloat16, false>, dim3(blocks), DW_THREADS, smem, 1, st, maps, args);
-    return pair ? launch_pdl(k_matmul_dw<__half, true>, dim3(blocks), DW_THREADS, smem, 2, st, maps, args)
-                : launch_pdl(k_matmul_dw<__half, false>, dim3(blocks), DW_THREADS, smem, 1, st, maps, args);
+        return pair ? launch_pdl(k_matmul_dw<__nv_bfloat16, true>, dim3(blocks), DW_THREADS, smem, SMEM_MOST, 2, st, maps, args)
+                    : launch_pdl(k_matmul_dw<__nv_bfloat16, false>, dim3(blocks), DW_THREADS, smem, SMEM_MOST, 1, st, maps, args);
+    return pair ? launch_pdl(k_matmul_dw<__half, true>, dim3(blocks), DW_THREADS, smem, SMEM_MOST, 2, st, maps, args)
+                : launch_pdl(k_matmul_dw<__half, false>, dim3(blocks), DW_THREADS, smem, SMEM_MOST, 1, st, maps, args);
 }
 
 // G[e] (+)= dY^T X over the rows of range e.
@@ -642,7 +642,7 @@ gptq_status adapter_gradients(const AdapterGrad *grads, int count, int rank, int
     }
     gptq_status s = launch_dw(a, count, dtype, st);
     if (s != GPTQ_OK || n == 0) return s;
-    return launch_pdl(k_sum_parts, dim3((unsigned)((n + 255) / 256)), 256, 0, 1, st, sum, (const int32_t *)status);
+    return launch_pdl(k_sum_parts, dim3((unsigned)((n + 255) / 256)), 256, 0, 0, 1, st, sum, (const int32_t *)status);
 }
 
 }  // namespace gptq

@@ -92,11 +92,11 @@ gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStre
     // by g_idx: each unpacking thread keeps its row's scales in shared memory where they leave two
     // operand stages (gathered from global memory for each code, they cost 13,000 clocks a step)
     const size_t table = (size_t)m.w.groups * MM_WARP_OUT * 32 * 4;
-    if (m.w.g_idx && fixed + table + 2 * stage <= 227 * 1024) {
+    if (m.w.g_idx && fixed + table + 2 * stage <= SMEM_MOST) {
         p.idx_table = 1;
         fixed += table;
     }
-    p.stages = (int)std::min<size_t>(MM_MAX_STAGES, (227 * 1024 - fixed) / stage);
+    p.stages = (int)std::min<size_t>(MM_MAX_STAGES, (SMEM_MOST - fixed) / stage);
     const size_t smem = fixed + (size_t)p.stages * stage;
     const int cluster = pair ? 2 : p.split;
     const int64_t groups = std::min<int64_t>(tiles(pair ? 2 * MM_LANES : MM_LANES, p.cols), matmul_tc_clusters(cluster));

@@ -1164,10 +1164,10 @@ static gptq_status launch_tc(const CUtensorMap &map, const CUtensorMap &wmap, co
                              cudaStream_t st) {
     const int cluster = pair ? 2 : p.split;
     if (p.m.w.g_idx)
-        return pair ? launch_pdl(k_matmul_tc<T, B, DIR, true, true>, dim3(blocks), MM_THREADS, smem, cluster, st, map, wmap, p)
-                    : launch_pdl(k_matmul_tc<T, B, DIR, true, false>, dim3(blocks), MM_THREADS, smem, cluster, st, map, wmap, p);
-    return pair ? launch_pdl(k_matmul_tc<T, B, DIR, false, true>, dim3(blocks), MM_THREADS, smem, cluster, st, map, wmap, p)
-                : launch_pdl(k_matmul_tc<T, B, DIR, false, false>, dim3(blocks), MM_THREADS, smem, cluster, st, map, wmap, p);
+        return pair ? launch_pdl(k_matmul_tc<T, B, DIR, true, true>, dim3(blocks), MM_THREADS, smem, SMEM_MOST, cluster, st, map, wmap, p)
+                    : launch_pdl(k_matmul_tc<T, B, DIR, true, false>, dim3(blocks), MM_THREADS, smem, SMEM_MOST, cluster, st, map, wmap, p);
+    return pair ? launch_pdl(k_matmul_tc<T, B, DIR, false, true>, dim3(blocks), MM_THREADS, smem, SMEM_MOST, cluster, st, map, wmap, p)
+                : launch_pdl(k_matmul_tc<T, B, DIR, false, false>, dim3(blocks), MM_THREADS, smem, SMEM_MOST, cluster, st, map, wmap, p);
 }
 
 template <typename T, int DIR>

@@ -25,7 +25,7 @@ int matmul_tc_occupancy(int cluster) {
     cfg.numAttrs = 1;
     int n = 0;
     if (cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem) != cudaSuccess ||
+                             (int)SMEM_MOST) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;

@@ -27,7 +27,8 @@ namespace {
 constexpr int TK_WARPS = 8;
 constexpr int TK_CH = 32;                  // channels of a block (two 16-row fragments)
 constexpr int TK_SPAN = TK_WARPS * 128;    // columns that the warps cover in one step each
-constexpr int TK_SMEM = 64 * 1024;         // most of X that is staged at a time
+constexpr int TK_SMEM = 64 * 1024;         // most of X that is staged at a time, without the rows' padding
+constexpr int TK_PAD = 32;
 }  // namespace
 
 struct TokenArg {
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(TK_WARPS * 32, !IDX && B <= 4 ? (B == 4 ? 3 : 
 
     // X by spans of columns. Piece q of chunk c stands at q ^ (c >> 1 & 1), rows 32 bytes apart
     // modulo 128: the eight lanes that read together then meet eight different 16-byte banks.
-    const int pitch = p.span * 2 + 32;
+    const int pitch = p.span * 2 + TK_PAD;
     const int rounds = (steps + TK_WARPS - 1) / TK_WARPS, per_span = p.span / TK_SPAN;
     auto stage = [&](int round) {
         const int k0 = round * TK_SPAN, chunks = min(p.span, (K - k0 + 127) & ~127) / 32;
@@ -328,12 +329,12 @@ __global__ void __launch_bounds__(TK_WARPS * 32, !IDX && B <= 4 ? (B == 4 ? 3 : 
 
 template <typename T, bool IDX>
 static gptq_status launch_token(const TokenArg &p, int bits, dim3 grid, cudaStream_t st) {
-    const size_t smem = (size_t)p.rows * (p.span * 2 + 32);
+    const size_t smem = (size_t)p.rows * (p.span * 2 + TK_PAD);
     switch (bits) {
-        case 2: return launch_pdl(k_matmul_token<T, 2, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
-        case 3: return launch_pdl(k_matmul_token<T, 3, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
-        case 4: return launch_pdl(k_matmul_token<T, 4, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
-        default: return launch_pdl(k_matmul_token<T, 8, IDX>, grid, TK_WARPS * 32, smem, 1, st, p);
+        case 2: return launch_pdl(k_matmul_token<T, 2, IDX>, grid, TK_WARPS * 32, smem, TK_SMEM + 8 * TK_PAD, 1, st, p);
+        case 3: return launch_pdl(k_matmul_token<T, 3, IDX>, grid, TK_WARPS * 32, smem, TK_SMEM + 8 * TK_PAD, 1, st, p);
+        case 4: return launch_pdl(k_matmul_token<T, 4, IDX>, grid, TK_WARPS * 32, smem, TK_SMEM + 8 * TK_PAD, 1, st, p);
+        default: return launch_pdl(k_matmul_token<T, 8, IDX>, grid, TK_WARPS * 32, smem, TK_SMEM + 8 * TK_PAD, 1, st, p);
     }
 }
 
