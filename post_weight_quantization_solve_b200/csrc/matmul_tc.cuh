@@ -24,9 +24,9 @@
 // Adapters: after the steps of W^, each run of rows with one adapter adds
 // sum_j P_a[.][j] T[t][j] over the run's columns alone (runs are widened to the MMA's column borders,
 // the rows there that belong to others are zero in shared memory; an adapter's infinities and NaN,
-// which would meet those zeros, are left out of such a step and added to the run's own rows at the
-// end). T comes as two 16-bit parts (16 bits of a bf16 pair, 22 of an fp16 one): the outputs have
-// 8 or 11. Runs of fewer than 16 rows (requests that decode) are added by the threads that write
+// which would meet those zeros, and the parts of T one by one, are left out of these steps and added to
+// the run's own rows at the end). T comes as two 16-bit parts (16 bits of a bf16 pair, 22 of an fp16
+// one): the outputs have 8 or 11. Runs of fewer than 16 rows (requests that decode) are added by the threads that write
 // the outputs: as matrix steps they cost about 1.3 us each.
 //
 // Order: the tiles of a range run rows first, so that blocks that work at the same time read
@@ -78,12 +78,6 @@ constexpr int MM_TABLE = ((MATMUL_MAX_EXPERTS + 4 + MM_CACHED + 4) * 4 + 256 * 2
 constexpr uint32_t MM_TMEM = 512;
 constexpr int MM_MAX_STAGES = 4;                    // of 64 TMEM columns beside the accumulators
 
-// Whether a run's widened columns take in rows of others (a tile's columns past its last row are
-// written to nothing).
-__device__ __forceinline__ bool run_shares(int begin, int end, int n, int grain) {
-    return begin % grain != 0 || (end % grain != 0 && end < n);
-}
-
 // The infinities and NaN among 8 values set to zero; whether there were any. An exponent of ones
 // carries into the sign's place.
 template <typename T>
@@ -104,14 +98,13 @@ __device__ __forceinline__ bool finite_only(uint4 (&y)[8]) {
     return any != 0u;
 }
 
-// What finite_only left out, for the rows of the runs that it concerns, in the accumulators at `at`
-// (this thread's channel).
+// What finite_only left out, for the rows of the tile's runs, in the accumulators at `at` (this
+// thread's channel).
 template <typename T, int DIR>
-__device__ __noinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *runs, int64_t t0, int n, int grain, int ch,
-                                              int channels, uint32_t at) {
+__device__ __noinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *runs, int64_t t0, int ch, int channels,
+                                           uint32_t at) {
 #pragma unroll 1
     for (int run = 0; run < runs->count; ++run) {
-        if (!run_shares(runs->begin[run], runs->end[run], n, grain)) continue;
 #pragma unroll 1
         for (int row = runs->begin[run]; row < runs->end[run]; ++row) {
             const unsigned short *P = static_cast<const unsigned short *>(l.P) + (int64_t)runs->id[run] * channels * l.rank +
@@ -616,7 +609,6 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     const int b0 = run_begin & -GRAIN, b1 = (run_end + GRAIN - 1) & -GRAIN;
                     const int rows = PAIR ? (b1 - b0) / 2 : b1 - b0;
                     const int row0 = b0 + (PAIR ? (int)rank * rows : 0);
-                    const bool shares = run_shares(run_begin, run_end, t.n, GRAIN);
                     for (int hs = 0; hs < 2 * rsteps; ++hs, ++half) {
                         const int side = hs & 1, rs = hs >> 1;
                         RingPos pos = base;
@@ -644,7 +636,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                             for (int j = 0; j < 8; ++j) y[j] = load8<T>(src + 8 * j, qa < two_r ? m.w.K - c - 8 * j : 0, v8);
                         }
                         bool ok = tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort);
-                        if (shares && finite_only<T>(y)) {
+                        if (finite_only<T>(y)) {
                             runs->broken = 1;
                             __threadfence_block();
                         }
@@ -814,7 +806,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 }
             };
             if (m.lora.R > 0 && ok && __any_sync(~0u, *(volatile int *)&runs->broken != 0))
-                add_nonfinite<T, DIR>(m.lora, runs, t.t0, t.n, GRAIN, ch, p.out, at);
+                add_nonfinite<T, DIR>(m.lora, runs, t.t0, ch, p.out, at);
             if (split == 1) {
                 if (shorts && ok) {
                     // their terms into the accumulators
