@@ -107,10 +107,10 @@ GPTQ_API gptq_status gptq_matmul_grouped_dw(float *dW, const void *dY, int64_t l
  *            checked as a whole as in gptq_matmul_grouped (ids in [-1, adapters)); rows
  *            outside [offsets[0], offsets[requests]) are left as they were.
  *   ws       gptq_lora_workspace_size(0, M, N, K, requests, adapters, rank) bytes.
- *   Arithmetic: fp32 sums; alpha A X enters as two dtype parts that add up to it (16 bits
- *            for bf16, 22 for fp16 inside its normal range; it must lie in fp16's range). Up to 8
- *            rows, W^ enters as in gptq_matmul_grouped; above, each weight is rounded
- *            once to dtype.
+ *   Arithmetic: fp32 sums; alpha A X has the range of fp32 for either dtype and enters the
+ *            output with 16 bits (fp16 up to 8 rows, and in runs of fewer than 16 rows of an
+ *            adapter: 24). Up to 8 rows, W^ enters as in gptq_matmul_grouped; above, each
+ *            weight is rounded once to dtype.
  *   Others as gptq_matmul_grouped. GPTQ_ERR_WORKSPACE for the workspace.
  */
 GPTQ_API gptq_status gptq_matmul_lora(void *Y, int64_t ldy, const void *X, int64_t ldx, int dtype,
@@ -131,8 +131,9 @@ GPTQ_API gptq_status gptq_matmul_lora(void *Y, int64_t ldy, const void *X, int64
  *            added to: zeros for an adapter that no row uses.
  *   X        may be NULL when neither dA nor dB is wanted.
  *   ws       gptq_lora_workspace_size(1, M, N, K, requests, adapters, rank) bytes.
- *   Others as gptq_matmul_lora; T and U enter dA and dB as parts that add up to them (24 bits
- *   for bf16, 22 for fp16 inside its normal range); dA and dB are fp32 sums in a fixed order.
+ *   Others as gptq_matmul_lora; T and U enter dA and dB with 24 bits (bf16), or with 22 and no
+ *   step coarser than 2^-39 of the adapter's largest value (fp16); dA and dB are fp32 sums in a
+ *   fixed order. Where dY or X is infinite, they may hold NaN in the place of infinities.
  */
 GPTQ_API gptq_status gptq_matmul_lora_backward(void *dX, int64_t lddx, float *dA, float *dB,
                                                const void *dY, int64_t lddy, const void *X,

@@ -5,9 +5,11 @@
 //   U[t] = alpha_a B_a^T dY[t]     (gradients of X and A)
 //
 // Both are a thin product rows x [rank][inner], bound by reading the rows (long prompts) or the
-// adapters (requests that decode, each with an adapter of its own). The result leaves as
-// 16-bit parts that add up to the fp32 sum (two of fp16, three of bf16, side by side), which the
-// products that follow read as matrix operands. Tiles of rows are cut inside each request, so a tile has one adapter.
+// adapters (requests that decode, each with an adapter of its own). The result leaves as three bf16
+// parts side by side that add up to the fp32 sum, which the products that follow read as matrix
+// operands. The gradients of fp16 adapters have fp16 rows as their other operand, so k_rank_scale makes
+// an fp16 pair of T or U, scaled by the power of two that brings the adapter's largest value below
+// 2^15: 22 bits, and no step coarser than 2^-39 of that largest value, whatever its size. Tiles of rows are cut inside each request, so a tile has one adapter.
 //   k_rank_tc    prompts: the adapter is the A operand of tcgen05 (rank lanes), 64 rows the B
 //                operand, both by tiled copies in steps of 128 columns.
 //   k_rank_rows  a few rows, or layouts that tiled copies refuse: fragments of mma.sync m16n8k16
@@ -39,7 +41,8 @@ struct RankArg {
     const float *alpha;       // [L]
     const int32_t *offsets, *ids;
     int R, L, rank, inner;
-    void *T2;                 // [M][LORA_HALVES rank]
+    __nv_bfloat16 *T3;        // [M][LORA_PARTS rank]
+    uint32_t *most;           // [L] largest finite |value| of each adapter, as bits, or NULL
     int xvec, avec, split;
     int32_t *status;
 };
@@ -112,16 +115,23 @@ __device__ __forceinline__ bool rank_tile(const RankArg &p, int64_t b, int rows,
     return n > 0;
 }
 
-// A rank-space value as its parts.
-template <typename T>
-__device__ __forceinline__ void store_parts(T *d, int rank, float v) {
+// A rank-space value as its parts; the larger of `big` and its size, if it is finite.
+__device__ __forceinline__ float store_parts(__nv_bfloat16 *d, int rank, float v, float big) {
+    big = isfinite(v) ? fmaxf(big, fabsf(v)) : big;
 #pragma unroll
-    for (int h = 0; h < LORA_HALVES<T>; ++h) {
-        const T x = from_f32<T>(v);
-        const float f = to_f32<T>(x);
+    for (int h = 0; h < LORA_PARTS; ++h) {
+        const __nv_bfloat16 x = from_f32<__nv_bfloat16>(v);
+        const float f = to_f32(x);
         d[h * rank] = x;
         v = isfinite(f) ? v - f : 0.f;          // an infinite part has no rest
     }
+    return big;
+}
+
+// By whole warps: bits of positive floats are ordered as they are.
+__device__ __forceinline__ void note_most(uint32_t *most, float big) {
+    const uint32_t b = __reduce_max_sync(~0u, __float_as_uint(big));
+    if ((threadIdx.x & 31) == 0 && b != 0u) atomicMax(most, b);
 }
 
 // Block (row tile, part of the contraction): MW warps of 16 rows x KW warps of the contraction;
@@ -185,7 +195,7 @@ __global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constan
     if (p.split > 1) tc::cluster_sync();
     else __syncthreads();
     const float alpha = __ldg(p.alpha + id);
-    T *out = static_cast<T *>(p.T2);
+    float big = 0.f;
     const int per = (rows * NR * 8 + p.split - 1) / p.split;
     for (int i = (int)rank * per + threadIdx.x; i < min(rows * NR * 8, ((int)rank + 1) * per); i += THREADS) {
         const int row = i / (NR * 8), j = i % (NR * 8);
@@ -197,8 +207,9 @@ __global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constan
         } else {
             sum = part[0][row][j];
         }
-        if (j < p.rank) store_parts<T>(out + ((int64_t)t + row) * LORA_HALVES<T> * p.rank + j, p.rank, alpha * sum);
+        if (j < p.rank) big = store_parts(p.T3 + ((int64_t)t + row) * LORA_PARTS * p.rank + j, p.rank, alpha * sum, big);
     }
+    if (p.most) note_most(p.most + id, big);
     if (p.split > 1) tc::cluster_sync();
 }
 
@@ -343,7 +354,7 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
             all &= tc::ld_shared_cluster(tc::mapa_shared(tc::smem_u32(const_cast<int *>(abort)), c)) == 0;
     if (all) {
         const float alpha = __ldg(p.alpha + id);
-        T *out = static_cast<T *>(p.T2);
+        float big = 0.f;
         const int total = n * p.rank, per = (total + p.split - 1) / p.split;
         for (int i = (int)rank * per + threadIdx.x; i < min(total, ((int)rank + 1) * per); i += RK_THREADS) {
             const int row = i / p.rank, j = i - row * p.rank;
@@ -355,8 +366,9 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
             } else {
                 sum = sums[i];
             }
-            store_parts<T>(out + ((int64_t)t + row) * LORA_HALVES<T> * p.rank + j, p.rank, alpha * sum);
+            big = store_parts(p.T3 + ((int64_t)t + row) * LORA_PARTS * p.rank + j, p.rank, alpha * sum, big);
         }
+        if (p.most) note_most(p.most + id, big);
     }
     if (p.split > 1) tc::cluster_sync();
     if (*abort && threadIdx.x == 0) set_status(p.status, GPTQ_ERR_TIMEOUT);
@@ -413,6 +425,51 @@ static gptq_status launch_rank(RankArgs &q, int count, int dtype, cudaStream_t s
     return launch_rank_nr<T, 16>(q, count, st);
 }
 
+// T and U of fp16 rows (blockIdx.y) as pairs for the gradients, eight values a thread. Rows of requests
+// without an adapter are left out: nothing reads them.
+struct ScaleArg {
+    const __nv_bfloat16 *T3[2];
+    __half *pair[2];                    // [M][2 rank]
+    const uint32_t *most[2];
+    const int32_t *offsets, *ids, *list_off;
+    int64_t M;
+    int R, rank;
+    const int32_t *status;
+};
+__global__ void __launch_bounds__(256) k_rank_scale(const __grid_constant__ ScaleArg p) {
+    grid_dependency();
+    if (failed(p.status) || __ldcg(p.list_off) < 0) return;
+    const int per = p.rank / 8, which = blockIdx.y;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = i / per;
+    if (t >= p.M || t < __ldg(p.offsets) || t >= __ldg(p.offsets + p.R)) return;
+    const int id = __ldg(p.ids + request_of(p.offsets, p.R, (int)t)), j = (int)(i - t * per) * 8;
+    if (id < 0) return;
+    const int e = 141 - (int)(__ldcg(p.most[which] + id) >> 23);
+    const __nv_bfloat16 *src = p.T3[which] + t * LORA_PARTS * p.rank + j;
+    uint4 in[LORA_PARTS];
+#pragma unroll
+    for (int h = 0; h < LORA_PARTS; ++h) in[h] = __ldcg(reinterpret_cast<const uint4 *>(src + h * p.rank));
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int h = LORA_PARTS - 1; h >= 0; --h) {
+            const float2 f = Half2<__nv_bfloat16>::unpack(reinterpret_cast<const uint32_t *>(&in[h])[q]);
+            v.x += f.x;
+            v.y += f.y;
+        }
+        v.x = ldexpf(v.x, e);
+        v.y = ldexpf(v.y, e);
+        hi[q] = Half2<__half>::pack(v.x, v.y);
+        const float2 f = Half2<__half>::unpack(hi[q]);
+        lo[q] = Half2<__half>::pack(isfinite(f.x) ? v.x - f.x : 0.f, isfinite(f.y) ? v.y - f.y : 0.f);
+    }
+    __half *d = p.pair[which] + t * 2 * p.rank + j;
+    *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4 *>(d + p.rank) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
 // What the backward pass needs first. Block 0: the requests of each adapter, in request order
 // (list_off [L + 1], list [R]; a warp takes whole adapters, 32 requests at a time; list_off[0] is
 // -1 when offsets or ids are refused, which a caller without a status word would not see). The others:
@@ -422,6 +479,7 @@ struct SetupArg {
     int64_t M;
     int R, L;
     int32_t *list_off, *list, *status;
+    uint32_t *most;                     // [2][L], set to zero
     const uint16_t *in;
     uint16_t *out;
     int N, r;
@@ -430,6 +488,7 @@ struct SetupArg {
 __device__ __forceinline__ void adapter_lists(const SetupArg &p) {
     __shared__ int warp_sum[8], base;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < 2 * p.L; i += 256) p.most[i] = 0u;
     const bool bad = __syncthreads_or(ids_bad(p.ids, p.R, p.L, threadIdx.x, 256) ||
                                       offsets_bad(p.offsets, p.R, p.M, threadIdx.x, 256));
     if (bad) {
@@ -496,14 +555,15 @@ __global__ void __launch_bounds__(256) k_lora_setup(const __grid_constant__ Setu
         if (j0 + i < p.r && n0 + x < p.N) p.out[base + (int64_t)(j0 + i) * p.N + n0 + x] = tile[x][i];
 }
 
-static RankArg rank_arg(void *T2, const void *X, int64_t ldx, int64_t M, const void *A, int inner,
+static RankArg rank_arg(__nv_bfloat16 *T3, uint32_t *most, const void *X, int64_t ldx, int64_t M, const void *A, int inner,
                         const float *alpha, const int32_t *offsets, const LoraArg &l, int32_t *status) {
     RankArg p{};
     p.X = X; p.ldx = ldx; p.M = M;
     p.A = A; p.alpha = alpha;
     p.offsets = offsets; p.ids = l.ids;
     p.R = l.R; p.L = l.L; p.rank = l.rank; p.inner = inner;
-    p.T2 = T2;
+    p.T3 = T3;
+    p.most = most;
     p.xvec = aligned(X, 16) && ldx % 8 == 0;
     p.avec = aligned(A, 16) && inner % 8 == 0;
     p.status = status;
@@ -516,19 +576,24 @@ static gptq_status rank_rows(RankArgs &q, int count, int dtype, cudaStream_t st)
 }
 
 struct LoraSpace {
-    void *T2, *U2, *Bt;
+    __nv_bfloat16 *T3, *U3;
+    __half *T_pair, *U_pair;            // (made for fp16 rows)
+    uint32_t *most;                     // [2][L]: T, U
+    void *Bt;
     float *parts_a, *parts_b;
     int32_t *list_off, *list;
     size_t bytes;
 };
 
 static LoraSpace lora_space(void *ws, bool backward, int64_t M, int N, int K, int R, int L, int rank) {
-    constexpr int parts = 3;                            // room for either type
     Carver c(ws);
     LoraSpace s{};
-    s.T2 = c.take<uint16_t>((size_t)M * parts * rank);
+    s.T3 = c.take<__nv_bfloat16>((size_t)M * LORA_PARTS * rank);
     if (backward) {
-        s.U2 = c.take<uint16_t>((size_t)M * parts * rank);
+        s.U3 = c.take<__nv_bfloat16>((size_t)M * LORA_PARTS * rank);
+        s.T_pair = c.take<__half>((size_t)M * 2 * rank);
+        s.U_pair = c.take<__half>((size_t)M * 2 * rank);
+        s.most = c.take<uint32_t>(2 * (size_t)L);
         s.Bt = c.take<uint16_t>((size_t)L * N * rank);
         const size_t pb = (size_t)adapter_parts(M, L, N) * L * N * rank, pa = (size_t)adapter_parts(M, L, K) * L * K * rank;
         s.parts_a = c.take<float>(pa);
@@ -549,11 +614,11 @@ gptq_status matmul_lora(MatmulArg m, const void *A, const void *B, const float *
     const LoraArg &l = m.lora;
     const LoraSpace s = lora_space(ws, false, m.M, m.w.N, m.w.K, l.R, l.L, l.rank);
     RankArgs q{};
-    q.a[0] = rank_arg(s.T2, m.X, m.ldx, m.M, A, m.w.K, alpha, m.offsets, l, m.status);
+    q.a[0] = rank_arg(s.T3, nullptr, m.X, m.ldx, m.M, A, m.w.K, alpha, m.offsets, l, m.status);
     gptq_status r = rank_rows(q, 1, dtype, st);
     if (r != GPTQ_OK) return r;
     m.lora.P = B;
-    m.lora.T2 = s.T2;
+    m.lora.T3 = s.T3;
     if (matmul_few_rows(m.M, 1)) return matmul_token(m, dtype, bits, st);
     return matmul_tc(m, 0, dtype, bits, st);
 }
@@ -566,22 +631,43 @@ gptq_status matmul_lora_backward(MatmulArg m, float *dA, float *dB, const void *
     const int N = m.w.N, K = m.w.K;
     const LoraSpace s = lora_space(ws, true, m.M, N, K, l.R, l.L, l.rank);
     const bool need_u = (m.Y || dA) && m.M > 0, need_t = dB && m.M > 0;
-    SetupArg setup{m.offsets, l.ids, m.M, l.R, l.L, s.list_off, s.list, m.status, (const uint16_t *)B, (uint16_t *)s.Bt, N, l.rank};
+    SetupArg setup{m.offsets, l.ids, m.M, l.R, l.L, s.list_off, s.list, m.status, s.most, (const uint16_t *)B, (uint16_t *)s.Bt,
+                   N, l.rank};
     const int64_t tiles = need_u ? (int64_t)((N + 31) / 32) * ((l.rank + 31) / 32) * l.L : 0;
     gptq_status r = launch_pdl(k_lora_setup, dim3((unsigned)(1 + tiles)), 256, 0, 0, 1, st, setup);
     if (r != GPTQ_OK) return r;
+    const bool pair = dtype == GPTQ_F16;
+    uint32_t *t_most = pair && dB ? s.most : nullptr, *u_most = pair && dA ? s.most + l.L : nullptr;
     RankArgs q{};
     int count = 0;
-    if (need_u) q.a[count++] = rank_arg(s.U2, m.X, m.ldx, m.M, s.Bt, N, alpha, m.offsets, l, m.status);
-    if (need_t) q.a[count++] = rank_arg(s.T2, X, ldx, m.M, A, K, alpha, m.offsets, l, m.status);
+    if (need_u) q.a[count++] = rank_arg(s.U3, u_most, m.X, m.ldx, m.M, s.Bt, N, alpha, m.offsets, l, m.status);
+    if (need_t) q.a[count++] = rank_arg(s.T3, t_most, X, ldx, m.M, A, K, alpha, m.offsets, l, m.status);
     if (count > 0) {
         r = rank_rows(q, count, dtype, st);
         if (r != GPTQ_OK) return r;
     }
     AdapterGrad grads[2];
+    ScaleArg scale{};
     int wanted = 0;
-    if (dB) grads[wanted++] = {m.X, m.ldx, N, s.T2, dB, s.parts_b, 0};
-    if (dA) grads[wanted++] = {X, ldx, K, s.U2, dA, s.parts_a, 1};
+    auto want = [&](const void *P, int64_t ldp, int np, const __nv_bfloat16 *T3, __half *to, const uint32_t *most,
+                    float *out, float *parts, int transposed) {
+        if (pair) {
+            scale.T3[wanted] = T3;
+            scale.pair[wanted] = to;
+            scale.most[wanted] = most;
+        }
+        const int halves = pair ? 2 : LORA_PARTS;
+        grads[wanted++] = {P, ldp, np, pair ? (const void *)to : T3, halves * l.rank, halves, most, out, parts, transposed};
+    };
+    if (dB) want(m.X, m.ldx, N, s.T3, s.T_pair, t_most, dB, s.parts_b, 0);
+    if (dA) want(X, ldx, K, s.U3, s.U_pair, u_most, dA, s.parts_a, 1);
+    if (pair && wanted > 0 && m.M > 0) {
+        scale.offsets = m.offsets; scale.ids = l.ids; scale.list_off = s.list_off;
+        scale.M = m.M; scale.R = l.R; scale.rank = l.rank;
+        scale.status = m.status;
+        r = launch_pdl(k_rank_scale, dim3((unsigned)((m.M * (l.rank / 8) + 255) / 256), wanted), 256, 0, 0, 1, st, scale);
+        if (r != GPTQ_OK) return r;
+    }
     if (wanted > 0) {
         r = adapter_gradients(grads, wanted, l.rank, dtype, m.M, m.offsets, l.ids, s.list_off, s.list, l.R, l.L,
                               m.status, st);
@@ -589,7 +675,7 @@ gptq_status matmul_lora_backward(MatmulArg m, float *dA, float *dB, const void *
     }
     if (m.Y && m.M > 0) {
         m.lora.P = A;
-        m.lora.T2 = s.U2;
+        m.lora.T3 = s.U3;
         r = matmul_tc(m, 1, dtype, bits, st);
     }
     return r;

@@ -31,19 +31,16 @@ struct PackedArg {
 // Adapters beside a product, and the rows that use them.
 struct LoraArg {
     const void *P;            // forward: B [L][N][rank]; input gradient: A [L][rank][K]
-    const void *T2;           // [M][LORA_HALVES rank]: the rank-space rows as 16-bit parts
+    const __nv_bfloat16 *T3;  // [M][LORA_PARTS rank]: the rank-space rows as parts
     const int32_t *ids;       // [R] adapter of each request, -1 none
     int R, L, rank;
 };
 
-// A rank-space value is kept as 16-bit parts that add up to it: two of fp16 (22 bits), three of
-// bf16 (24 bits). The adapters' gradients, fp32 sums, take all of them; the products whose
-// outputs are 16 bits wide take the first two.
-template <typename T>
-constexpr int LORA_HALVES = 2;
-template <>
-constexpr int LORA_HALVES<__nv_bfloat16> = 3;
-inline int lora_halves(int dtype) { return dtype == GPTQ_BF16 ? 3 : 2; }
+// A rank-space value is kept as three bf16 parts that add up to it (24 bits, the range of fp32: it is
+// no row of the model, and fp16 would lose small gradients and overflow on large ones). Outputs of 16
+// bits take the first two (16 bits, bf16) or all of them (fp16; two where they are matrix operands).
+// The adapters' gradients, fp32 sums, take all of them, fp16 rows a scaled pair (lora.cu).
+constexpr int LORA_PARTS = 3;
 
 struct MatmulArg {
     PackedArg w;
@@ -57,13 +54,16 @@ struct MatmulArg {
     int32_t *status;
 };
 
-// One gradient of the adapters: P [M][ldp] against the rank-space rows T2; parts: room for the sums
-// of adapter_parts() parts where there is more than one.
+// One gradient of the adapters: P [M][ldp] against the rank-space rows Q [M][ldq], `halves` parts of
+// them side by side, each adapter's times 2^(141 - e) where `most` holds its largest value with the
+// exponent field e; parts: room for the sums of adapter_parts() parts where there is more than one.
 struct AdapterGrad {
     const void *P;
     int64_t ldp;
     int np;
-    const void *T2;
+    const void *Q;
+    int ldq, halves;
+    const uint32_t *most;
     float *out, *parts;
     int transposed;
 };
@@ -434,14 +434,17 @@ __device__ __forceinline__ void lora_terms(const LoraArg &l, const int (&id)[NRO
     for (int i = 0; i < NROW; ++i) add[i] = 0.f;
 #pragma unroll 1
     for (int j = 0; j < r; j += 8) {
-        uint4 hv[NROW], lv[NROW], pv[NROW];
+        constexpr int USED = Half2<T>::kType == 1 ? 2 : 3;
+        uint4 tv[USED][NROW], pv[NROW];
 #pragma unroll
         for (int i = 0; i < NROW; ++i) {
-            hv[i] = lv[i] = pv[i] = make_uint4(0u, 0u, 0u, 0u);
+            pv[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int h = 0; h < USED; ++h) tv[h][i] = make_uint4(0u, 0u, 0u, 0u);
             if (id[i] < 0) continue;
-            const T *h = static_cast<const T *>(l.T2) + t[i] * LORA_HALVES<T> * r + j;
-            hv[i] = __ldcg(reinterpret_cast<const uint4 *>(h));
-            lv[i] = __ldcg(reinterpret_cast<const uint4 *>(h + r));
+            const __nv_bfloat16 *h0 = l.T3 + t[i] * LORA_PARTS * r + j;
+#pragma unroll
+            for (int h = 0; h < USED; ++h) tv[h][i] = __ldcg(reinterpret_cast<const uint4 *>(h0 + h * r));
             if constexpr (DIR == 0) {
                 pv[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(l.P) +
                                                               ((int64_t)id[i] * channels + ch) * r + j));
@@ -457,13 +460,23 @@ __device__ __forceinline__ void lora_terms(const LoraArg &l, const int (&id)[NRO
         }
 #pragma unroll
         for (int i = 0; i < NROW; ++i) {
-            const uint32_t pp[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w}, hh[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w},
-                           ll[4] = {lv[i].x, lv[i].y, lv[i].z, lv[i].w};
+            const uint32_t pp[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w};
+            float2 sum[4] = {};
+#pragma unroll
+            for (int h = USED - 1; h >= 0; --h) {
+                const uint32_t tt[4] = {tv[h][i].x, tv[h][i].y, tv[h][i].z, tv[h][i].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 f = Half2<__nv_bfloat16>::unpack(tt[q]);
+                    sum[q].x += f.x;
+                    sum[q].y += f.y;
+                }
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float2 fp = Half2<T>::unpack(pp[q]), fh = Half2<T>::unpack(hh[q]), fl = Half2<T>::unpack(ll[q]);
-                add[i] = fmaf(fp.x, fh.x + fl.x, add[i]);
-                add[i] = fmaf(fp.y, fh.y + fl.y, add[i]);
+                const float2 fp = Half2<T>::unpack(pp[q]);
+                add[i] = fmaf(fp.x, sum[q].x, add[i]);
+                add[i] = fmaf(fp.y, sum[q].y, add[i]);
             }
         }
     }

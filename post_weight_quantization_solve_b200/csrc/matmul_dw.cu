@@ -54,6 +54,7 @@ struct DwArg {
     // Q is `parts` parts of `rank` columns side by side, added in the epilogue (1: plain). Where they
     // do not fit a tile together (apart), a tile takes 64 columns of each, a box a part.
     int parts, rank, apart;
+    const uint32_t *most;     // Q's groups are scaled by the exponents of these (AdapterGrad), or NULL
     int transposed;           // output [q][p] instead of [p][q]
     int accumulate;
     float *out;               // [split][groups][np][nq'] (or [nq'][np])
@@ -424,6 +425,12 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
             }
             if (!ok) break;
             if (chains == 0 && p.accumulate) continue;
+            if (p.most) {                           // 2^(e - 141) as two normal factors
+                const int e = (int)(__ldcg(p.most + t.g) >> 23) - 141, e1 = e >> 1, e2 = e - e1;
+                const float f1 = __uint_as_float((uint32_t)(127 + e1) << 23), f2 = __uint_as_float((uint32_t)(127 + e2) << 23);
+#pragma unroll
+                for (int i = 0; i < 128; ++i) sum[i] = sum[i] * f1 * f2;
+            }
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb) {
                 if (cb * 32 >= qn) break;
@@ -617,9 +624,10 @@ gptq_status adapter_gradients(const AdapterGrad *grads, int count, int rank, int
         const AdapterGrad &g = grads[i];
         DwArg &p = a[i];
         p.P = g.P; p.ldp = g.ldp; p.np = g.np;
-        p.parts = lora_halves(dtype);
+        p.parts = g.halves;
         p.rank = rank;
-        p.Q = g.T2; p.ldq = p.nq = p.parts * rank;
+        p.Q = g.Q; p.ldq = g.ldq; p.nq = p.parts * rank;
+        p.most = g.most;
         p.apart = p.nq > DW_COLS;
         p.M = M;
         p.offsets = offsets;

@@ -25,8 +25,10 @@
 // sum_j P_a[.][j] T[t][j] over the run's columns alone (runs are widened to the MMA's column borders,
 // the rows there that belong to others are zero in shared memory; an adapter's infinities and NaN,
 // which would meet those zeros, and the parts of T one by one, are left out of these steps and added to
-// the run's own rows at the end). T comes as two 16-bit parts (16 bits of a bf16 pair, 22 of an fp16
-// one): the outputs have 8 or 11. Runs of fewer than 16 rows (requests that decode) are added by the threads that write
+// the run's own rows at the end). These steps are bf16 ones for either type of rows: the contraction is
+// [P | P] against two parts of T (16 bits), and for fp16 rows, whose P are two bf16 numbers exactly,
+// [P's first | P's second | P's first] against T's first, first and second part (16 bits; the outputs
+// have 11, and the weights' rounding to fp16 beside it 11). Runs of fewer than 16 rows (requests that decode) are added by the threads that write
 // the outputs: as matrix steps they cost about 1.3 us each.
 //
 // Order: the tiles of a range run rows first, so that blocks that work at the same time read
@@ -109,14 +111,14 @@ __device__ __noinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *run
         for (int row = runs->begin[run]; row < runs->end[run]; ++row) {
             const unsigned short *P = static_cast<const unsigned short *>(l.P) + (int64_t)runs->id[run] * channels * l.rank +
                                       (DIR == 0 ? (int64_t)ch * l.rank : ch);
-            const T *t = static_cast<const T *>(l.T2) + (t0 + row) * (LORA_HALVES<T> * l.rank);
+            const __nv_bfloat16 *t = l.T3 + (t0 + row) * (LORA_PARTS * l.rank);
             float add = 0.f;
             if (ch < channels) {
 #pragma unroll 1
                 for (int j = l.rank; j > 0; --j, ++t, P += DIR == 0 ? 1 : channels) {
                     const uint32_t v = __ldg(P);
                     if (nonfinite<T>(v) & 0x8000u)
-                        add = fmaf(Half2<T>::unpack(v).x, to_f32<T>(t[0]) + to_f32<T>(t[l.rank]), add);
+                        add = fmaf(Half2<T>::unpack(v).x, to_f32(t[0]) + to_f32(t[l.rank]), add);
                 }
             }
             __syncwarp();
@@ -126,6 +128,24 @@ __device__ __noinline__ void add_nonfinite(const LoraArg &l, const LoraRuns *run
             tc::tmem_st_wait();
         }
     }
+}
+
+// The first bf16 parts of eight fp16 values, or what these leave (for an infinity that is a NaN).
+template <typename T>
+__device__ __forceinline__ uint4 bf16_part8(uint4 v, bool rest) {
+    if constexpr (Half2<T>::kType != 1) {
+        using H = Half2<__nv_bfloat16>;
+        auto part = [&](uint32_t &x) {
+            const float2 f = Half2<T>::unpack(x);
+            x = H::pack(f.x, f.y);
+            if (rest) {
+                const float2 g = H::unpack(x);
+                x = H::pack(f.x - g.x, f.y - g.y);
+            }
+        };
+        part(v.x); part(v.y); part(v.z); part(v.w);
+    }
+    return v;
 }
 
 // The ring of packed words: rows of 128 codes (16 B bytes), as a tiled copy with the swizzle of that
@@ -409,8 +429,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     const int k0 = (int)((int64_t)steps * part / split), k1 = (int)((int64_t)steps * (part + 1) / split);
     const int nmain = k1 - k0;
     const bool adapters = m.lora.R > 0 && part == split - 1;
-    const int two_r = 2 * m.lora.rank;
-    const int rsteps = (two_r + MM_BK - 1) / MM_BK;
+    // blocks of `rank` columns in the adapters' contraction; of block 1, P's second part and T's first
+    // (fp16), or P and T's second
+    constexpr bool SPLIT_P = Half2<T>::kType != 1;
+    const int inner_r = (SPLIT_P ? 3 : 2) * m.lora.rank;
+    const int rsteps = (inner_r + MM_BK - 1) / MM_BK;
     const T *X = static_cast<const T *>(m.X);
     LoraRuns *runs = reinterpret_cast<LoraRuns *>(table + MATMUL_MAX_EXPERTS + 4 + MM_CACHED + 4 + 128);
     uint32_t lphase = 0;
@@ -601,8 +624,9 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 grid_wait();
                 int half = 0;                           // of the adapters' steps, in turn too
                 const T *P = static_cast<const T *>(m.lora.P);
-                const T *T2 = static_cast<const T *>(m.lora.T2);
+                const __nv_bfloat16 *T3 = m.lora.T3;
                 const int r = m.lora.rank;
+                auto block = [&](int q) { return (q >= r ? 1 : 0) + (SPLIT_P && q >= 2 * r ? 1 : 0); };
                 const int count = runs_wait() ? runs->count : 0, halves = 2 * rsteps * count;
                 for (int run = 0; run < count; ++run) {
                     const int run_begin = runs->begin[run], run_end = runs->end[run], run_id = runs->id[run];
@@ -616,8 +640,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         if (unpack_adapter_set(turn, half, halves) != set) continue;
                         const int arow = side * 64 + arow64;
                         // this thread's part of A, requested before the stage is free. Forward: row n
-                        // of B_a twice over, [hi part | lo part] of the contraction; input gradient:
-                        // rows of A_a, twice over too
+                        // of B_a, once for each block of the contraction; input gradient: rows of A_a,
+                        // once for each too
                         uint4 y[8];
                         const int qa = rs * MM_BK + (DIR == 0 ? side * 64 : arow);
                         if constexpr (DIR == 0) {
@@ -625,18 +649,20 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const int q = qa + j * 8;
-                                y[j] = ch < m.w.N && q < two_r ? load8<T>(src + (q < r ? q : q - r), 8, true)
-                                                               : make_uint4(0u, 0u, 0u, 0u);
+                                y[j] = ch < m.w.N && q < inner_r
+                                           ? bf16_part8<T>(load8<T>(src + q - block(q) * r, 8, true), block(q) == 1)
+                                           : make_uint4(0u, 0u, 0u, 0u);
                             }
                         } else {
                             const int c = t.c0 + ahalf * 64;
-                            const T *src = P + ((int64_t)run_id * r + (qa < r ? qa : qa - r)) * m.w.K + c;
+                            const T *src = P + ((int64_t)run_id * r + qa - block(qa) * r) * m.w.K + c;
                             const bool v8 = (m.w.K & 7) == 0;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) y[j] = load8<T>(src + 8 * j, qa < two_r ? m.w.K - c - 8 * j : 0, v8);
+                            for (int j = 0; j < 8; ++j)
+                                y[j] = bf16_part8<T>(load8<T>(src + 8 * j, qa < inner_r ? m.w.K - c - 8 * j : 0, v8), block(qa) == 1);
                         }
                         bool ok = tc::mbar_wait(&empty[pos.stage], pos.phase ^ 1, abort);
-                        if (finite_only<T>(y)) {
+                        if (finite_only<__nv_bfloat16>(y)) {
                             runs->broken = 1;
                             __threadfence_block();
                         }
@@ -659,13 +685,16 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                                 for (int j = 0; j < 8; ++j)
                                     *reinterpret_cast<uint4 *>(a + ((j ^ (arow & 7)) << 4)) = y[j];
                             }
-                            // the run's rows of [hi | lo], zeros for rows of others
+                            // the run's rows of T's parts, zeros for rows of others
                             for (int j = stid; j < rows * 8; j += 128) {
                                 const int row = j >> 3, q = j & 7, col = rs * MM_BK + side * 64 + 8 * q;
                                 const int tr = row0 + row;
                                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                                if (tr >= run_begin && tr < run_end && col < two_r)
-                                    x = __ldcg(reinterpret_cast<const uint4 *>(T2 + (t.t0 + tr) * (LORA_HALVES<T> * r) + col));
+                                if (tr >= run_begin && tr < run_end && col < inner_r) {
+                                    const int b = block(col), of = SPLIT_P ? b >> 1 : b;
+                                    x = __ldcg(reinterpret_cast<const uint4 *>(T3 + (t.t0 + tr) * (LORA_PARTS * r) + col -
+                                                                               (b - of) * r));
+                                }
                                 *reinterpret_cast<uint4 *>(st + side * MM_HALF + row * 128 + ((q ^ (row & 7)) << 4)) = x;
                             }
                             tc::fence_async_shared();
@@ -1110,12 +1139,12 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                     const int count = runs_wait() ? runs->count : 0;
                     for (int run = 0; run < count && ok; ++run) {
                         const int b0 = runs->begin[run] & -GRAIN, b1 = (runs->end[run] + GRAIN - 1) & -GRAIN;
-                        const uint32_t rid = tc::idesc_f16_f32(Half2<T>::kType, MROWS, b1 - b0, DIR, 0);
+                        const uint32_t rid = tc::idesc_f16_f32(Half2<__nv_bfloat16>::kType, MROWS, b1 - b0, DIR, 0);
                         for (int rs = 0; rs < rsteps; ++rs) {
                             ok = __all_sync(~0u, tc::mbar_wait(&full[pos.stage], pos.phase, abort));
                             if (!ok) break;
                             tc::fence_after_sync();
-                            issue(d + b0, pos.stage, (min(MM_BK, two_r - rs * MM_BK) + 15) / 16, rid, 1u);
+                            issue(d + b0, pos.stage, (min(MM_BK, inner_r - rs * MM_BK) + 15) / 16, rid, 1u);
                             pos.advance(stages);
                         }
                     }

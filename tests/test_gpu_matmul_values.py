@@ -34,3 +34,54 @@ def test_an_infinite_adapter_gives_infinities(counts, K, N, dtype, rank):
                              np.zeros((c["M"], N)))[0]
     assert np.isinf(want[own][:, [5, 150]]).all() and np.array_equal(np.isfinite(dX), np.isfinite(want))
     assert np.array_equal(dX[own][:, [5, 150]], want[own][:, [5, 150]])
+
+
+# (X, dY, A, B) of an fp16 layer whose weights are zero, so that the adapters' terms stand alone, and
+# rank-space rows far below fp16's smallest step, and above its largest value
+RANK_SPACE = {"small": (1.0, 1e-5, 3000.0, 1e-4), "large": (60.0, 30.0, 40.0, 60.0)}
+
+
+@pytest.mark.parametrize("size", list(RANK_SPACE))
+@pytest.mark.parametrize("counts,ids,rank,N,K", [([1] * 6, [0, 1, 2, 0, -1, 2], 16, 200, 264),
+                                                 ([0, 300, 1, 1, 0, 20, 5], [0, 1, 1, -1, 2, 2, 0], 48, 200, 264),
+                                                 ([700, 1300], [2, 0], 16, 200, 264), ([40, 300], [1, 0], 128, 77, 101)])
+def test_rank_space_rows_of_fp16_have_the_range_of_fp32(size, counts, ids, rank, N, K):
+    c = lora_case(21, "fp16", 4, 64, counts, ids, 3, rank, N, K, first=1, pad=2)
+    rng, t, o = gen(22), torch.float16, c["o"]
+    for name, scale in zip(("X", "dY", "A", "B"), RANK_SPACE[size]):
+        c[name].copy_(rows_of(rng, tuple(c[name].shape), t, scale).cuda())
+    c["args"][1].zero_()
+    if size == "large":                     # (the outputs have to stay below 65,504)
+        c["A"].div_(2000.0)
+    x, d, A, B = f64(c["X"]), f64(c["dY"]), f64(c["A"]), f64(c["B"])
+    al, W = c["alpha"].astype(np.float64), np.zeros((N, K))
+    eps, n = torch.finfo(t).eps / 2, max(N, K) + 3 * rank + 20
+
+    dX, dA, dB = gq.gptq_matmul_lora_backward(c["dY"], c["X"], *c["args"], dX=torch.zeros(c["M"], K, dtype=t, device="cuda"))
+    want = ref.lora_backward(d, x, W, A, B, al, o, c["ids"], np.zeros((c["M"], K)))
+    S = ref.lora_backward(*map(np.abs, (d, x, W, A, B)), al, o, c["ids"], np.zeros((c["M"], K)))
+    rows = np.repeat(np.array(ids), counts)
+    U = np.abs(np.concatenate([al[a] * d[1 + i:2 + i] @ B[a] for i, a in enumerate(rows) if a >= 0]))
+    if size == "large":
+        assert U.max() > 65504
+    else:
+        assert U.max() < 2.0 ** -22
+    # two bf16 parts of U, of A one or two: 2^-17 + 2^-18 of each product; half of fp16's smallest step
+    check(f64(dX), want[0], eps * np.abs(want[0]) + (n * 2.0 ** -23 + 2.0 ** -16) * S[0] * (1 + eps) + 2.0 ** -25)
+    # 22 bits of U and T, or 2^-39 of the adapter's largest
+    m = len(rows)
+    for got, w, s, other, big in ((dA, want[1], S[1], x, U.max()),
+                                  (dB, want[2], S[2], d, np.abs(al.max() * x @ A.reshape(-1, K).T).max())):
+        check(f64(got), w, ((n + min(m, 512) + m // 512) * 2.0 ** -23 + 2.0 ** -21) * s
+              + 2.0 ** -39 * big * np.abs(other).sum(0).max() + 1e-37)
+
+    if size == "large":
+        c["A"].mul_(2000.0)
+        c["B"].div_(20000.0)
+    A, B = f64(c["A"]), f64(c["B"])
+    T = np.abs(np.concatenate([al[a] * x[1 + i:2 + i] @ A[a].T for i, a in enumerate(rows) if a >= 0]))
+    assert size == "small" or T.max() > 65504
+    y = gq.gptq_matmul_lora(c["X"], *c["args"], out=torch.zeros(c["M"], N, dtype=t, device="cuda"))
+    want = ref.lora(x, W, A, B, al, o, c["ids"], np.zeros((c["M"], N)))
+    S = ref.lora(*map(np.abs, (x, W, A, B)), al, o, c["ids"], np.zeros((c["M"], N)))
+    check(f64(y), want, eps * np.abs(want) + (n * 2.0 ** -23 + 2.0 ** -16) * S * (1 + eps) + 2.0 ** -25)
