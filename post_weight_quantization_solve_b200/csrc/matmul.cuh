@@ -260,13 +260,19 @@ __device__ __forceinline__ void unpack8(const uint32_t (&w)[B], uint32_t (&q)[4]
     }
 }
 
+// What bf16 leaves of a scale, as a pair; nothing of an infinite one.
+__device__ __forceinline__ uint32_t rest_of_scale(float s, uint32_t hi) {
+    const float rest = s - __uint_as_float(hi & 0xffff0000u);
+    const float v = isfinite(rest) ? rest : 0.f;
+    return Half2<__nv_bfloat16>::pack(v, v);
+}
+
 // Four values' pairs times one scale (as scale32).
 template <typename T>
 __device__ __forceinline__ void scale8(uint32_t (&v)[4], float s) {
     if constexpr (Half2<T>::kType == 1) {
         const uint32_t hi = Half2<T>::pack(s, s);
-        const float rest = s - __uint_as_float(hi & 0xffff0000u);
-        const uint32_t lo = Half2<T>::pack(rest, rest);
+        const uint32_t lo = rest_of_scale(s, hi);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t t;
@@ -289,8 +295,7 @@ template <typename T>
 __device__ __forceinline__ void scale32(uint32_t (&v)[16], float s) {
     if constexpr (Half2<T>::kType == 1) {
         const uint32_t hi = Half2<T>::pack(s, s);
-        const float rest = s - __uint_as_float(hi & 0xffff0000u);
-        const uint32_t lo = Half2<T>::pack(rest, rest);
+        const uint32_t lo = rest_of_scale(s, hi);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             uint32_t t;

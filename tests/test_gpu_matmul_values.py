@@ -85,3 +85,23 @@ def test_rank_space_rows_of_fp16_have_the_range_of_fp32(size, counts, ids, rank,
     want = ref.lora(x, W, A, B, al, o, c["ids"], np.zeros((c["M"], N)))
     S = ref.lora(*map(np.abs, (x, W, A, B)), al, o, c["ids"], np.zeros((c["M"], N)))
     check(f64(y), want, eps * np.abs(want) + (n * 2.0 ** -23 + 2.0 ** -16) * S * (1 + eps) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("bits,rows", [(2, 5), (3, 40), (4, 5), (8, 300)])
+def test_an_infinite_scale_gives_infinities(dtype, bits, rows):
+    rng, t, N, K = gen(bits), TYPES[dtype], 140, 256
+    codes = rng.integers(0, 2 ** bits, (1, N, K)).astype(np.uint8)
+    codes[0, 3, 64:128] = 2 ** bits - 1                     # positive weights
+    scales = (0.01 + 0.02 * rng.random((1, N, 4))).astype(np.float32)
+    scales[0, 3, 1] = np.inf
+    words = torch.from_numpy(ref.pack(codes, bits).view(np.int32)).cuda()
+    x = torch.rand(rows, K).add_(0.5).to(t)
+    d = torch.rand(rows, N).add_(0.5).to(t)
+    args = (words, dev(scales), bits)
+    y = f64(gq.gptq_matmul_grouped(x.cuda(), *args, dev(off([rows])), 64))
+    dx = f64(gq.gptq_matmul_grouped_dx(d.cuda(), *args, K, dev(off([rows])), 64))
+    W = ref.weights(codes, bits, scales, 64)[0]
+    for got, want in ((y, f64(x) @ W.T), (dx, f64(d) @ W)):
+        bad = np.isinf(want)
+        assert bad.any() and np.array_equal(got[bad], want[bad]) and np.isfinite(got[~bad]).all()
