@@ -595,9 +595,13 @@ static LoraSpace lora_space(void *ws, bool backward, int64_t M, int N, int K, in
         s.U_pair = c.take<__half>((size_t)M * 2 * rank);
         s.most = c.take<uint32_t>(2 * (size_t)L);
         s.Bt = c.take<uint16_t>((size_t)L * N * rank);
-        const size_t pb = (size_t)adapter_parts(M, L, N) * L * N * rank, pa = (size_t)adapter_parts(M, L, K) * L * K * rank;
-        s.parts_a = c.take<float>(pa);
-        s.parts_b = c.take<float>(pb);
+        // (a single part goes to the gradient itself)
+        auto parts = [&](int width) {
+            const int n = adapter_parts(M, L, width);
+            return n > 1 ? c.take<float>((size_t)n * L * width * rank) : nullptr;
+        };
+        s.parts_a = parts(K);
+        s.parts_b = parts(N);
         s.list_off = c.take<int32_t>(L + 1);
         s.list = c.take<int32_t>(std::max(R, 1));
     }
