@@ -157,32 +157,48 @@ __global__ void __launch_bounds__(MW * KW * 32) k_rank_rows(const __grid_constan
     const T *x0 = r0 + g < end ? X + (int64_t)(r0 + g) * p.ldx : nullptr;
     const T *x1 = r0 + g + 8 < end ? X + (int64_t)(r0 + g + 8) * p.ldx : nullptr;
     const T *A = static_cast<const T *>(p.A) + (int64_t)id * p.rank * p.inner;
-    float acc[NR][4];
+    // The matrix unit rounds each sum the same way, so a chain is CHAIN steps (two products each), and
+    // the chains are added in fp32 to nearest (one chain of 214 products: U 3.6e-6 off in the mean).
+    constexpr int CHAIN = 8;
+    float total[NR][4];
 #pragma unroll
     for (int j = 0; j < NR; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+        for (int i = 0; i < 4; ++i) total[j][i] = 0.f;
     const int steps = (p.inner + 31) / 32;
     const int s0 = (int)((int64_t)steps * rank / p.split), s1 = (int)((int64_t)steps * (rank + 1) / p.split);
     const bool xv = p.xvec != 0, av = p.avec != 0;
     constexpr int AHEAD = NR <= 2 ? 4 : NR <= 4 ? 2 : 1;      // steps in flight
-#pragma unroll AHEAD
-    for (int step = s0 + kw; step < s1; step += KW) {
-        const int c = step * 32 + quad * 8;
-        const uint4 a = piece<T>(x0, c, p.inner, xv), b = piece<T>(x1, c, p.inner, xv);
+#pragma unroll 1
+    for (int chain = s0 + kw; chain < s1; chain += CHAIN * KW) {
+        const int end_step = min(s1, chain + CHAIN * KW);
+        float acc[NR][4];
 #pragma unroll
-        for (int j = 0; j < NR; ++j) {
-            const int row = j * 8 + g;
-            const uint4 w = piece<T>(row < p.rank ? A + (int64_t)row * p.inner : nullptr, c, p.inner, av);
-            mma_16816<T>(acc[j], a.x, b.x, a.y, b.y, w.x, w.y);
-            mma_16816<T>(acc[j], a.z, b.z, a.w, b.w, w.z, w.w);
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+#pragma unroll AHEAD
+        for (int step = chain; step < end_step; step += KW) {
+            const int c = step * 32 + quad * 8;
+            const uint4 a = piece<T>(x0, c, p.inner, xv), b = piece<T>(x1, c, p.inner, xv);
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+                const int row = j * 8 + g;
+                const uint4 w = piece<T>(row < p.rank ? A + (int64_t)row * p.inner : nullptr, c, p.inner, av);
+                mma_16816<T>(acc[j], a.x, b.x, a.y, b.y, w.x, w.y);
+                mma_16816<T>(acc[j], a.z, b.z, a.w, b.w, w.z, w.w);
+            }
         }
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) total[j][i] += acc[j][i];
     }
 #pragma unroll
     for (int j = 0; j < NR; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            part[kw][mw * 16 + g + 8 * (i >> 1)][j * 8 + 2 * quad + (i & 1)] = acc[j][i];
+            part[kw][mw * 16 + g + 8 * (i >> 1)][j * 8 + 2 * quad + (i & 1)] = total[j][i];
     __syncthreads();
     const int rows = n;
     for (int i = threadIdx.x; i < rows * NR * 8; i += THREADS) {
@@ -222,13 +238,14 @@ constexpr int RK_A = 128 * RK_BK * 2;                   // 32 KB; only `rank` ro
 constexpr int RK_STAGE = RK_X + RK_A;
 constexpr int RK_SMEM = RK_STAGES * RK_STAGE + 1024 + 256;
 constexpr int RK_THREADS = 192;
-constexpr int RK_ACCS = 8;
+constexpr int RK_ACCS = 8, RK_CHAIN = 4;                // accumulators; steps of one
 }  // namespace
 
 // Roles: warp 0 tiled copies, warp 1 TMEM and MMAs, warps 2-5 outputs. The lanes past the rank
-// multiply what the stage happens to hold; nothing reads them. The steps go to eight accumulators
-// in turn, added in fp32 to nearest at the end: the tensor core's own accumulation rounds each
-// step the same way (one chain of 256 MMAs was 4e-6 off in the mean).
+// multiply what the stage happens to hold; nothing reads them. The tensor core's own accumulation
+// rounds each step the same way (one chain of 256 MMAs was 4e-6 off in the mean), so a chain is
+// RK_CHAIN steps of 8 MMAs; the chains go to eight accumulators in turn, and the outputs' warps add
+// them in fp32 to nearest while the next ones run.
 template <typename T>
 __global__ void __launch_bounds__(RK_THREADS, 1)
     k_rank_tc(const __grid_constant__ RankMaps maps, const __grid_constant__ RankArgs args) {
@@ -240,7 +257,9 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + RK_STAGES * RK_STAGE);
     uint64_t *empty = full + RK_STAGES;
     uint64_t *tfull = empty + RK_STAGES;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tfull + 1);
+    uint64_t *tempty = tfull + RK_ACCS;
+    uint64_t *drain = tempty + RK_ACCS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     __shared__ int found[4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -250,7 +269,11 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
-        tc::mbar_init(tfull, 1);
+        for (int k = 0; k < RK_ACCS; ++k) {
+            tc::mbar_init(&tfull[k], 1);
+            tc::mbar_init(&tempty[k], (p.rank + 31) / 32);      // the warps that have outputs
+        }
+        tc::mbar_init(drain, 1);
         *abort = 0;
         tc::fence_mbar_init();
         tc::prefetch_tmap(xmap);
@@ -297,7 +320,11 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
             const uint64_t ad0 = tc::desc_sw128(tc::smem_u32(smem) + RK_X, 16, 1024);
             bool ok = true;
             for (int s = s0; s < s1; ++s) {
-                const int i = s - s0, stage = i % RK_STAGES;
+                const int i = s - s0, stage = i % RK_STAGES, chain = i / RK_CHAIN, acc = chain % RK_ACCS;
+                if (i % RK_CHAIN == 0) {
+                    ok = __all_sync(~0u, tc::mbar_wait(&tempty[acc], ((chain / RK_ACCS) & 1) ^ 1, abort));
+                    if (!ok) break;
+                }
                 ok = __all_sync(~0u, tc::mbar_wait(&full[stage], (i / RK_STAGES) & 1, abort));
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -305,40 +332,51 @@ __global__ void __launch_bounds__(RK_THREADS, 1)
                 if (tc::elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < RK_BK / 16; ++kk)
-                        tc::mma_bf16(tmem + (i % RK_ACCS) * RK_ROWS, ad0 + by + ((kk >> 2) * (RK_A / 2) + (kk & 3) * 32 >> 4),
+                        tc::mma_bf16(tmem + acc * RK_ROWS, ad0 + by + ((kk >> 2) * (RK_A / 2) + (kk & 3) * 32 >> 4),
                                      bd0 + by + ((kk >> 2) * (RK_X / 2) + (kk & 3) * 32 >> 4), idesc,
-                                     (i >= RK_ACCS || kk > 0) ? 1u : 0u);
+                                     (i % RK_CHAIN > 0 || kk > 0) ? 1u : 0u);
                     tc::mma_commit(&empty[stage]);
+                    if (i % RK_CHAIN == RK_CHAIN - 1 || s == s1 - 1) tc::mma_commit(&tfull[acc]);
                 }
                 __syncwarp();
             }
             // (also after a time-out: what was issued completes before TMEM is released)
-            if (tc::elect_one()) tc::mma_commit(tfull);
+            if (tc::elect_one()) tc::mma_commit(drain);
             __syncwarp();
             volatile int never = 0;
-            tc::mbar_wait(tfull, 0, &never);
+            tc::mbar_wait(drain, 0, &never);
         } else {
-            // lane = rank index: into shared memory, over stages that the MMAs have read
+            // lane = rank index
             const int quad = warp & 3, j = quad * 32 + lane;
-            volatile int never = 0;
-            const bool ok = __all_sync(~0u, tc::mbar_wait(tfull, 0, &never)) && !*abort;
-            tc::fence_after_sync();
-            if (ok && quad * 32 < p.rank) {
-                for (int c = 0; c < n16; c += 16) {
-                    float add[16];
+            if (quad * 32 < p.rank) {
+                float total[RK_ROWS];
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) add[q] = 0.f;
-                    for (int k = 0; k < min(RK_ACCS, s1 - s0); ++k) {
+                for (int q = 0; q < RK_ROWS; ++q) total[q] = 0.f;
+                bool ok = true;
+                const int chains = (s1 - s0 + RK_CHAIN - 1) / RK_CHAIN;
+                for (int chain = 0; chain < chains; ++chain) {
+                    const int acc = chain % RK_ACCS;
+                    ok = __all_sync(~0u, tc::mbar_wait(&tfull[acc], (chain / RK_ACCS) & 1, abort));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < RK_ROWS; c += 16) {
+                        if (c >= n16) break;
                         uint32_t v[16];
-                        tc::tmem_ld_32x32b_x16(tmem + k * RK_ROWS + c + ((uint32_t)(quad * 32) << 16), v);
+                        tc::tmem_ld_32x32b_x16(tmem + acc * RK_ROWS + c + ((uint32_t)(quad * 32) << 16), v);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) add[q] += __uint_as_float(v[q]);
+                        for (int q = 0; q < 16; ++q) total[c + q] += __uint_as_float(v[q]);
                     }
-                    if (j < p.rank) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&tempty[acc]);
+                }
+                // into shared memory, over stages that the last products have read
+                if (ok && j < p.rank) {
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) sums[(c + q) * p.rank + j] = add[q];
-                    }
+                    for (int q = 0; q < RK_ROWS; ++q)
+                        if (q < n16) sums[q * p.rank + j] = total[q];
                 }
             }
             tc::fence_before_sync();

@@ -105,3 +105,24 @@ def test_an_infinite_scale_gives_infinities(dtype, bits, rows):
     for got, want in ((y, f64(x) @ W.T), (dx, f64(d) @ W)):
         bad = np.isinf(want)
         assert bad.any() and np.array_equal(got[bad], want[bad]) and np.isfinite(got[~bad]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("counts,rank,N,K,chain", [([7] * 60, 128, 13656, 264, 16), ([22], 64, 9408, 960, 16),
+                                                   ([300], 16, 264, 65528, 32), ([1000, 200], 64, 30000, 136, 32)])
+def test_rank_space_sums_do_not_drift(dtype, counts, rank, N, K, chain):
+    """The matrix units cut each step of a sum off, by half of 2^-23 of it in the mean and always towards
+    zero, so a chain of n steps is n / 2 such halves off; chains, and the parts that are added to
+    nearest, count 4 more, as do the gradients' own sums of at most 32 steps of these few rows (16)."""
+    ids = [i % 2 for i in range(len(counts))]
+    c = lora_case(31, dtype, 4, 0, counts, ids, 2, rank, N, K)
+    _, dA, dB = gq.gptq_matmul_lora_backward(c["dY"], c["X"], *c["args"], want=(False, True, True))
+    x, d, A, B = (c[n].double() for n in ("X", "dY", "A", "B"))
+    wA, wB = torch.zeros_like(A), torch.zeros_like(B)
+    for r, a in enumerate(ids):
+        p, f = slice(int(c["o"][r]), int(c["o"][r + 1])), float(c["alpha"][a])
+        wA[a] += f * (d[p] @ B[a]).t() @ x[p]
+        wB[a] += f * d[p].t() @ (x[p] @ A[a].t())
+    own = min(32, max(counts) / 16 if len(counts) < 3 else 4)
+    for got, want in ((dA, wA), (dB, wB)):
+        assert (got.double() - want).norm() <= (chain / 2 + 4 + own / 2) * 2.0 ** -23 * want.norm()
