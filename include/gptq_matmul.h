@@ -25,10 +25,13 @@ extern "C" {
  *              ld_words >= ceil(K bits / 32). Rows that start on 16-byte boundaries
  *              (words 16-byte aligned, ld_words % 4 == 0) are read fastest.
  *   scales     device fp32 [experts][N] (groupsize 0) or
- *              [experts][N][ceil(K / groupsize)].
+ *              [experts][N][ceil(K / groupsize)]. An infinite or NaN scale makes its channel's
+ *              outputs infinite or NaN (of the input gradient: its group's columns).
  *   g_idx      device int32 [experts][K], the group of each column (each in
  *              [0, ceil(K / groupsize)), else GPTQ_ERR_ARG in the status word), or NULL:
- *              column k in group k / groupsize (natural order and static groups).
+ *              column k in group k / groupsize. A layer quantised in natural order or with
+ *              static groups has that g_idx too: give NULL for it. Its groups are looked up
+ *              column by column, at up to twelve times the time.
  *   experts    1..512; a plain projection is one expert.
  *   N, K       1..GPTQ_MAX_DIM.  bits 2, 3, 4 or 8.  groupsize 0, 32, 64 or 128.
  */

@@ -528,8 +528,9 @@ def gptq_matmul_grouped(X, words, scales, bits, offsets=None, groupsize=0, g_idx
                         status=None, stream=None):
     """out[t] = W^_e X[t] for offsets[e] <= t < offsets[e + 1] over packed layers (see
     include/gptq_matmul.h). words [experts][N][..] or [N][..] (one layer; then scales and
-    g_idx have no leading dimension either). Without `out`, a new [M][N] tensor, whose rows
-    outside the ranges are not initialised. Returns out."""
+    g_idx have no leading dimension either). g_idx: for act-order layers; None where column k is in
+    group k // groupsize, which is faster. Without `out`, a new [M][N] tensor, whose rows outside
+    the ranges are not initialised. Returns out."""
     dev = _device(X, "X")
     M, K, x, ldx = _rows(X, dev, "X")
     t = X.dtype

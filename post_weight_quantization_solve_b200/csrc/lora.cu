@@ -17,8 +17,8 @@
 //                its row and of its adapter row, which permutes the contraction index alike on
 //                both sides.
 // A cluster of up to 8 blocks shares the contraction of a tile when there are few tiles.
-// 8,192 rows of 4,096 with rank 64: 23 us, 67 MB at 2.9 TB/s (cold); 48 rows with an adapter each of
-// rank 16: 12 us, the latency of one launch and its reads.
+// 8,192 rows of 4,096 with rank 64: 24 us, 67 MB at 2.8 TB/s (cold); 48 rows with an adapter each of
+// rank 16: 12 us, the latency of one launch and its reads. k_rank_scale: 5 us for 700 rows of rank 32.
 // B_a is stored [N][rank]; the backward pass reads it transposed (k_lora_setup).
 #include <algorithm>
 

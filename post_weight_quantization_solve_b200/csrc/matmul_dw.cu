@@ -16,8 +16,9 @@
 // The tensor core's fp32 accumulation rounds each step the same way, so a chain is 512 rows (32
 // MMAs) only: two accumulators in turn, and the epilogue adds each chain to its sums in registers,
 // in fp32 to nearest and in order. Mean error over 1,024 rows: 1.7e-6 in one chain, 4.7e-7 in
-// chains of 512 (plain fp32 sums: 3.4e-7), 2.5e-7 in chains of 256, at 245, 275 and 310 us for
-// eight experts of 4,096 x 4,096. Nothing is added across blocks, so results do not change from
+// chains of 512 (plain fp32 sums: 3.4e-7), 2.5e-7 in chains of 256, at 245, 275 and 310 us side by
+// side for eight experts of 4,096 x 4,096 (chains of 512: 338 to 349 us under a full load's clocks, the
+// tensor pipe 48 % busy: products wait for accumulators, whose readers wait for TMEM). Nothing is added across blocks, so results do not change from
 // run to run.
 // Outputs leave through shared memory as tiled stores (or adds) of 32 x 32 boxes: row by row they
 // took 25,000 clocks a tile, three times its products. Layouts that tiled stores refuse go row

@@ -89,8 +89,11 @@ gptq_status matmul_tc(const MatmulArg &m, int dir, int dtype, int bits, cudaStre
     p.epi = p.split > 1 ? p.cols * MM_LANES * 4 : p.accs == 1 ? p.cols * MM_LANES * 2 : 32 * MM_LANES * 2;
     const int stage = MM_B_BYTES + (dir == 1 ? MM_A_BYTES : 0);
     size_t fixed = ring_bytes(bits, dir) + p.epi + MM_TABLE + 1024 + 320;
-    // by g_idx: each unpacking thread keeps its row's scales in shared memory where they leave two
-    // operand stages (gathered from global memory for each code, they cost 13,000 clocks a step)
+    // by g_idx: each unpacking thread keeps its row's scales in shared memory, 1,536 bytes a group, where
+    // they leave two operand stages (gathered from global memory for each code, they cost 13,000 clocks
+    // a step). Groups that fit, by bits 2, 3, 4, 8: forward 83, 75, 67, 67 with single blocks, 46, 38,
+    // 30, 30 with pairs and split tiles; input gradient 49, 45, 49, 41, split 11, 7, 11, 25. Neither
+    // pairs nor the split are given up for a table.
     const size_t table = (size_t)m.w.groups * MM_WARP_OUT * 32 * 4;
     if (m.w.g_idx && fixed + table + 2 * stage <= SMEM_MOST) {
         p.idx_table = 1;

@@ -18,8 +18,10 @@
 //
 // Scales: with one scale a channel the forward product multiplies exact integers c - z and the
 // scale enters in fp32 at the end. Where the scale changes along the contraction (input
-// groups, the input gradient) or adapters share the accumulators, each weight s (c - z) is
-// rounded once to the rows' 16-bit type, as a dequantised layer in that type would hold it.
+// groups, the input gradient) or adapters share the accumulators (their terms carry no scale), each
+// weight s (c - z) is rounded once to the rows' 16-bit type, as a dequantised layer in that type would
+// hold it: bf16 outputs are then 2.4e-3 off 64 bits in the mean instead of 1.7e-3, fp16 2.9e-4 instead
+// of 2.1e-4. Two operands a weight would not lose that, at twice the products.
 //
 // Adapters: after the steps of W^, each run of rows with one adapter adds
 // sum_j P_a[.][j] T[t][j] over the run's columns alone (runs are widened to the MMA's column borders,
@@ -42,10 +44,12 @@
 // 128 rows x 128 codes (a step) at a time, through a ring of their own that runs ahead across tiles.
 // Tiles of at most 128 rows use two accumulators in turn, so a tile's end costs the next one nothing.
 //
-// 16,384 rows over eight layers of 4,096 -> 14,336, 4 bits: 1.28 to 1.45 ms with the clock that the
-// power cap leaves (1.33 to 1.5 PFLOP/s). 512 rows over 32 layers of 2,048 -> 2,816, groups of 128:
-// 67 us, bound by unpacking (1,000 to 1,500 clocks a step). Input gradient of 8,192 rows over eight
-// layers of 4,096 x 4,096, groups of 128: 265 to 310 us, the tensor pipe 51 % busy.
+// 16,384 rows over eight layers of 4,096 -> 14,336, 4 bits: 1.45 to 1.51 ms with the clock that the
+// power cap leaves (1.28 to 1.33 PFLOP/s). 512 rows over 32 layers of 2,048 -> 2,816, groups of 128:
+// 70 us, about 1,550 clocks a step, of which 870 are issue slots (55 % busy, the integer pipe 46 %): the
+// chain of one half-step, wait, read, unpack, wait, store, and what three sets leave of it. Input
+// gradient of 8,192 rows over eight layers of 4,096 x 4,096, groups of 128: 319 to 331 us, about 2,200
+// clocks a step; the tensor pipe is 47 % busy, the issue slots 54 %.
 #pragma once
 
 #include <algorithm>
@@ -158,7 +162,7 @@ struct MmRing {
     static constexpr int ROW = 16 * B;
     static constexpr int ROWS = DIR == 0 ? 128 : 64;
     static constexpr int STAGE = ROWS * ROW;
-    // the input gradient's operand stages leave less room
+    // the input gradient's operand stages leave less room (4 bits with six stages: 322 us for 321)
     static constexpr int STAGES = B >= (DIR == 0 ? 8 : 4) ? 3 : 6;
     static_assert(STAGES % UNPACK_SETS == 0, "a set's stages are its own");
     static constexpr int WORDS = STAGES * STAGE;
